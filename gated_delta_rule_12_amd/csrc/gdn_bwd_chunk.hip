@@ -132,45 +132,6 @@ __device__ __forceinline__ int blk_m(int i) { return i >= 6 ? 3 : i >= 3 ? 2 : i
 __device__ __forceinline__ int blk_n(int i) { const int m = blk_m(i); return i - m * (m + 1) / 2; }
 __device__ __forceinline__ void st4f(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
 
-__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
-    s = a + b;
-    const float bb = s - a;
-    e = (a - (s - bb)) + (b - bb);
-}
-
-// Chunk gates on one wave (lane t = token t of the chunk; past the sequence
-// end alpha = 1, beta = 0): the log-gate prefix as hi + lo, the prediction
-// prefix, beta and alpha.
-struct Gate {
-    float hi, lo, phi, plo, beta, alpha;
-};
-__device__ __forceinline__ Gate gate_from(float alpha, float beta, int nt, int order, int lane) {
-    Gate g;
-    g.alpha = lane < nt ? alpha : 1.f;
-    g.beta = lane < nt ? beta : 0.f;
-    float hi = lane < nt ? logf(g.alpha) : 0.f, lo = 0.f;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const float h2 = __shfl_up(hi, o, 64), l2 = __shfl_up(lo, o, 64);
-        if (lane >= o) {
-            float s, e;
-            two_sum(hi, h2, s, e);
-            hi = s;
-            lo = (lo + l2) + e;
-        }
-    }
-    g.hi = hi;
-    g.lo = lo;
-    if (order == GDN_PREDICT_THEN_DECAY) {
-        g.phi = __shfl_up(hi, 1, 64);
-        g.plo = __shfl_up(lo, 1, 64);
-        if (lane == 0) g.phi = g.plo = 0.f;
-    } else {
-        g.phi = hi;
-        g.plo = lo;
-    }
-    return g;
-}
 // (token rows past the sequence end are read at the last real row and
 // replaced by the defaults)
 __device__ __forceinline__ Gate chunk_gate(const Problem& p, int64_t row0, int nt, int lane) {
@@ -181,11 +142,6 @@ __device__ __forceinline__ Gate chunk_gate(const Problem& p, int64_t row0, int n
 // Rows of a chunk's token factors (lane t: token t): the gate prefix pair,
 // the prediction prefix pair, beta, gamma_t, gamma'_t and R_t = gamma_C / gamma_t.
 enum { kGhi, kGlo, kGphi, kGplo, kGbeta, kGgam, kGgamp, kGR };
-
-// e^{(hb - ha) + (lb - la)}
-__device__ __forceinline__ float ratio(float hb, float lb, float ha, float la) {
-    return __expf((hb - ha) + (lb - la));
-}
 
 // Per-chunk records of the workspace.  Fragment sets: [m][tp][lane][8] =
 // X[16 (2 tp + e) + 4 g + q][key_col(m, c)] (e = 0, 1; q = 0..3) for X = K,

@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <algorithm>
+
 struct gdn_timer;  // caller-owned per-kernel timer (include/gdn.h)
 
 namespace gdn {
@@ -128,6 +130,54 @@ struct RawInputs {
 size_t raw_inputs_bytes(const Problem& p);
 RawInputs raw_inputs_at(const Problem& p, char* base);
 hipError_t raw_prologue(const Problem& p, const RawInputs& r, hipStream_t st);
+
+// Packed ragged sequences over a pool of states (gdn_packed.hip): sequence s
+// holds tokens cu[s] .. cu[s + 1] - 1 of [N, heads, features] arrays and its
+// states live in slots of [slots, Hv, dv, dk] pools.
+struct Packed {
+    int64_t N, S, Hk, Hv, dk, dv, n_in, n_out, max_len;  // n_in, n_out: slots of the pools
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    int dtype, gate, order;
+    float scale;
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* alpha;
+    const float* beta;
+    const int32_t* cu;
+    const float* s_in;         // pool, null: zero start states
+    const int32_t* slots_in;   // null: sequence s starts from slot s
+    float* s_out;              // pool, null: end states not wanted
+    const int32_t* slots_out;  // null: sequence s ends in slot s
+    void* out;                 // [N, Hv, dv], dtype
+    gdn_timer* timer;
+};
+// Whether the chunk kernels serve these shapes, and the bytes they need.
+bool packed_chunked(const Packed& p);
+size_t packed_workspace(const Packed& p);
+hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st);
+
+// Layer norm (gdn_norm.hip).
+struct LayerNorm {
+    int64_t rows, n;
+    int x_dtype, y_dtype;  // of x and dx; of y and dy
+    float eps;
+    const void* x;
+    const void* dy;
+    const float* weight;
+    const float* bias;
+    void* y;
+    void* dx;
+    float* mean;
+    float* rstd;
+    float* dweight;
+    float* dbias;
+    float* part;  // workspace of the backward
+    gdn_timer* timer;
+};
+size_t layer_norm_workspace(int64_t rows, int64_t n);
+hipError_t layer_norm_fwd(const LayerNorm& p, hipStream_t st);
+hipError_t layer_norm_bwd(const LayerNorm& p, hipStream_t st);
 
 // Start state copy/zero for empty sequences (T == 0).
 hipError_t copy_state(const Problem& p, hipStream_t st);

@@ -50,43 +50,6 @@
 namespace gdn {
 namespace {
 
-__device__ __forceinline__ f32x4 mfma(const u16x8& a, const u16x8& b, const f32x4& c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-
-// Two fp32 values -> bf16 pair, round to nearest even (one v_cvt_pk_bf16_f32).
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2_t));
-}
-
-// x = hi + lo + O(2^-18 |x|): hi = bf16(x), lo = bf16(x - hi), both RNE.
-// x - hi is exact in fp32 and is formed by one bf16 dot product per element,
-// x + (-1) hi + (-0) hi' (v_dot2c_f32_bf16), instead of a shift and a
-// subtraction.  The zero factors are -0: the pair (-1, +0) would be emitted as
-// the inline constant -1.0, which the instruction reads as (+0, -1) (checked
-// lane by lane on gfx950); (-1, -0) and (-0, -1) are encoded as literals.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16(a, b);
-    const bf16x2_t h = __builtin_bit_cast(bf16x2_t, hi);
-    const bf16x2_t m0 = {(__bf16)-1.f, (__bf16)-0.f}, m1 = {(__bf16)-0.f, (__bf16)-1.f};
-    lo = pack_bf16(__builtin_amdgcn_fdot2_f32_bf16(h, m0, a, false), __builtin_amdgcn_fdot2_f32_bf16(h, m1, b, false));
-}
-
-__device__ __forceinline__ void split4(const f32x4& x, u16x4& hi, u16x4& lo) {
-    uint32_t h0, l0, h1, l1;
-    split2(x[0], x[1], h0, l0);
-    split2(x[2], x[3], h1, l1);
-    hi = __builtin_bit_cast(u16x4, uint2{h0, h1});
-    lo = __builtin_bit_cast(u16x4, uint2{l0, l1});
-}
-
-__device__ __forceinline__ u16x8 cat(const u16x4& a, const u16x4& b) {
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
 // ---------------------------------------------------------------------------
 // stage 1: T' and the gate block per chunk-head
 // ---------------------------------------------------------------------------

@@ -1,11 +1,14 @@
 // Pieces shared by the MFMA kernel files (gdn_mfma.hip, the chunked forward;
-// gdn_bwd_chunk.hip, the chunked backward): vector types, the fp32 MFMA and
-// its operand layout, a wave prefix sum, and the in-LDS inverse of the unit
-// lower-triangular UT system.  Internal to libgdn.
+// gdn_bwd_chunk.hip, the chunked backward; gdn_packed.hip, the packed
+// forward): vector types, the fp32 and bf16 MFMA and their operand layouts,
+// bf16 splits, a wave prefix sum, the gate prefix as a compensated pair, and
+// the in-LDS inverse of the unit lower-triangular UT system.  Internal to libgdn.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "../../include/gdn.h"
 
 namespace gdn {
 namespace {
@@ -43,6 +46,45 @@ __device__ __forceinline__ f32x4 mfma_f32(float a, float b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
+// D += A B on a 16 x 16 x 32 bf16 tile: lane l = 16 g + c supplies A[c][8 g ..]
+// and B[8 g ..][c]; accumulator as above.
+__device__ __forceinline__ f32x4 mfma(const u16x8& a, const u16x8& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+// Two fp32 values -> bf16 pair, round to nearest even (one v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2_t));
+}
+
+// x = hi + lo + O(2^-18 |x|): hi = bf16(x), lo = bf16(x - hi), both RNE.
+// x - hi is exact in fp32 and is formed by one bf16 dot product per element,
+// x + (-1) hi + (-0) hi' (v_dot2c_f32_bf16), instead of a shift and a
+// subtraction.  The zero factors are -0: the pair (-1, +0) would be emitted as
+// the inline constant -1.0, which the instruction reads as (+0, -1) (checked
+// lane by lane on gfx950); (-1, -0) and (-0, -1) are encoded as literals.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16(a, b);
+    const bf16x2_t h = __builtin_bit_cast(bf16x2_t, hi);
+    const bf16x2_t m0 = {(__bf16)-1.f, (__bf16)-0.f}, m1 = {(__bf16)-0.f, (__bf16)-1.f};
+    lo = pack_bf16(__builtin_amdgcn_fdot2_f32_bf16(h, m0, a, false), __builtin_amdgcn_fdot2_f32_bf16(h, m1, b, false));
+}
+
+__device__ __forceinline__ void split4(const f32x4& x, u16x4& hi, u16x4& lo) {
+    uint32_t h0, l0, h1, l1;
+    split2(x[0], x[1], h0, l0);
+    split2(x[2], x[3], h1, l1);
+    hi = __builtin_bit_cast(u16x4, uint2{h0, h1});
+    lo = __builtin_bit_cast(u16x4, uint2{l0, l1});
+}
+
+__device__ __forceinline__ u16x8 cat(const u16x4& a, const u16x4& b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 __device__ __forceinline__ float wave_incl_scan(float x, int lane) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -50,6 +92,54 @@ __device__ __forceinline__ float wave_incl_scan(float x, int lane) {
         if (lane >= o) x += y;
     }
     return x;
+}
+
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+    s = a + b;
+    const float bb = s - a;
+    e = (a - (s - bb)) + (b - bb);
+}
+
+// Chunk gates on one wave (lane t = token t of the chunk; past the sequence
+// end alpha = 1, beta = 0): the log-gate prefix as hi + lo, the prediction
+// prefix, beta and alpha.
+struct Gate {
+    float hi, lo, phi, plo, beta, alpha;
+};
+// (la: the log gate of this lane's token, 0 past the end)
+__device__ __forceinline__ Gate gate_prefix(float la, float alpha, float beta, int nt, int order, int lane) {
+    Gate g;
+    g.alpha = lane < nt ? alpha : 1.f;
+    g.beta = lane < nt ? beta : 0.f;
+    float hi = la, lo = 0.f;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const float h2 = __shfl_up(hi, o, 64), l2 = __shfl_up(lo, o, 64);
+        if (lane >= o) {
+            float s, e;
+            two_sum(hi, h2, s, e);
+            hi = s;
+            lo = (lo + l2) + e;
+        }
+    }
+    g.hi = hi;
+    g.lo = lo;
+    if (order == GDN_PREDICT_THEN_DECAY) {
+        g.phi = __shfl_up(hi, 1, 64);
+        g.plo = __shfl_up(lo, 1, 64);
+        if (lane == 0) g.phi = g.plo = 0.f;
+    } else {
+        g.phi = hi;
+        g.plo = lo;
+    }
+    return g;
+}
+__device__ __forceinline__ Gate gate_from(float alpha, float beta, int nt, int order, int lane) {
+    return gate_prefix(lane < nt ? logf(alpha) : 0.f, alpha, beta, nt, order, lane);
+}
+// e^{(hb - ha) + (lb - la)}
+__device__ __forceinline__ float ratio(float hb, float lb, float ha, float la) {
+    return __expf((hb - ha) + (lb - la));
 }
 
 // The UT inverse T = (I + A)^{-1} in fp32, in place in LDS.  On entry AT

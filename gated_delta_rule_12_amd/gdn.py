@@ -35,7 +35,10 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_recurrent_ref", "gdn_seqpar_fwd", "gdn_decode_s
            "gdn_timer_create", "gdn_timer_destroy", "gdn_timer_read", "gdn_chunk_fwd_timed",
            "gdn_seqpar_fwd_timed", "gdn_decode_step_timed", "gdn_backward_timed",
            "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_raw", "gdn_chunk_fwd_raw_timed",
-           "gdn_raw_workspace_bytes", "gdn_backward_path")
+           "gdn_raw_workspace_bytes", "gdn_backward_path",
+           "gdn_packed_fwd", "gdn_packed_fwd_timed", "gdn_packed_workspace_bytes", "gdn_packed_path",
+           "gdn_layer_norm_fwd", "gdn_layer_norm_fwd_timed", "gdn_layer_norm_backward",
+           "gdn_layer_norm_backward_timed", "gdn_layer_norm_workspace_bytes")
 
 _lib = None
 
@@ -102,9 +105,21 @@ def lib():
     L.gdn_timer_read.argtypes = [vp, ctypes.c_int, ctypes.c_char_p, sz,
                                  ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
     L.gdn_timer_read.restype = ctypes.c_int
+    L.gdn_packed_fwd.argtypes = ([i64] * 9 + [i32, i32, i32, f32] + [vp, i64] * 3 + [vp] * 8 + [vp, sz, vp])
+    L.gdn_packed_fwd.restype = ctypes.c_int
+    L.gdn_packed_workspace_bytes.argtypes = [i64] * 7 + [i32, i32]
+    L.gdn_packed_workspace_bytes.restype = sz
+    L.gdn_packed_path.argtypes = [i64, i64, i32, i32]
+    L.gdn_packed_path.restype = ctypes.c_int
+    L.gdn_layer_norm_fwd.argtypes = [i64, i64, i32, i32, f32] + [vp] * 7
+    L.gdn_layer_norm_fwd.restype = ctypes.c_int
+    L.gdn_layer_norm_backward.argtypes = [i64, i64, i32, i32] + [vp] * 9 + [sz, vp]
+    L.gdn_layer_norm_backward.restype = ctypes.c_int
+    L.gdn_layer_norm_workspace_bytes.argtypes = [i64, i64]
+    L.gdn_layer_norm_workspace_bytes.restype = sz
     # the *_timed variants: the same arguments plus the timer
     for name in ("gdn_chunk_fwd", "gdn_chunk_fwd_raw", "gdn_seqpar_fwd", "gdn_decode_step",
-                 "gdn_backward"):
+                 "gdn_backward", "gdn_packed_fwd", "gdn_layer_norm_fwd", "gdn_layer_norm_backward"):
         f = getattr(L, name + "_timed")
         f.argtypes = getattr(L, name).argtypes + [vp]
         f.restype = ctypes.c_int
@@ -164,6 +179,18 @@ def gdn_chunk_segments(B, T, H, dk, dv, chunk, dtype, gate) -> int:
 
 def gdn_seqpar_segments(B, T, H, dk, dv, chunk, dtype, gate, n_segments) -> int:
     return int(lib().gdn_seqpar_segments(B, T, H, dk, dv, chunk, dtype, gate, n_segments))
+
+
+def gdn_packed_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, dtype, gate) -> int:
+    return int(lib().gdn_packed_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, dtype, gate))
+
+
+def gdn_packed_path(dk, dv, dtype, gate) -> int:
+    return int(lib().gdn_packed_path(dk, dv, dtype, gate))
+
+
+def gdn_layer_norm_workspace_bytes(rows, n) -> int:
+    return int(lib().gdn_layer_norm_workspace_bytes(rows, n))
 
 
 def gdn_status_str(status: int) -> str:
@@ -466,3 +493,195 @@ def decode_step(q, k, v, alpha, beta, state=None, *, order=GDN_PREDICT_THEN_DECA
     if rc != GDN_OK:
         raise GdnError(rc, name)
     return out, state_out
+
+
+# ---- packed ragged sequences over a pool of states ------------------------------
+
+def _on_device(device, fn, args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _packed_check(q, k, v, alpha, beta, cu_seqlens, pools, slots):
+    import torch
+    if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[0] != q.shape[0]:
+        raise ValueError("q, k must be [N,Hk,dk] and v [N,Hv,dv]")
+    N, Hk, dk = q.shape
+    Hv, dv = v.shape[1:]
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt:
+        raise TypeError("q, k, v must share a dtype")
+    for t, d in ((q, dk), (k, dk), (v, dv)):
+        if t.numel() and (t.stride(2) != 1 or (t.stride(1) != d and t.shape[1] > 1)):
+            raise ValueError("the heads and features of a token of q, k, v must be contiguous")
+    if alpha.shape == (N, Hv):
+        gate = GDN_GATE_SCALAR
+    elif alpha.shape == (N, Hv, dk):
+        gate = GDN_GATE_CHANNEL
+    else:
+        raise ValueError("alpha must be [N,Hv] or [N,Hv,dk]")
+    if beta.shape != (N, Hv):
+        raise ValueError("beta must be [N,Hv]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [S+1]")
+    S = cu_seqlens.shape[0] - 1
+    for t in pools:
+        if t is not None and (t.dim() != 4 or t.shape[1:] != (Hv, dv, dk)):
+            raise ValueError("state pools must be [slots,Hv,dv,dk]")
+    for t in slots:
+        if t is not None and t.shape != (S,):
+            raise ValueError("slots must be [S]")
+    dev = q.device
+    for t in (cu_seqlens, *slots):
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError("cu_seqlens and slots must be int32")
+    for t in (alpha, beta, *pools):
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError("alpha, beta and states must be float32")
+    for t in (q, k, v, alpha, beta, cu_seqlens, *pools, *slots):
+        if t is not None and (not t.is_cuda or t.device != dev):
+            raise ValueError("all tensors must be on one GPU")
+    for t in (alpha, beta, cu_seqlens, *pools, *slots):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("all tensors but q, k, v must be contiguous")
+    return N, S, Hk, Hv, dk, dv, gate
+
+
+def _token_strides(q, k, v):
+    """Elements between tokens; a lone token's stride says nothing."""
+    def one(t):
+        row = t.shape[1] * t.shape[2]
+        return t.stride(0) if t.shape[0] > 1 else row
+    return one(q), one(k), one(v)
+
+
+def packed_workspace_for(q, v, alpha, cu_seqlens, max_len=None):
+    """A workspace for packed_fwd on tensors like these."""
+    import torch
+    N, Hk, dk = q.shape
+    gate = GDN_GATE_SCALAR if alpha.dim() == 2 else GDN_GATE_CHANNEL
+    n = gdn_packed_workspace_bytes(N, cu_seqlens.shape[0] - 1, Hk, v.shape[1], dk, v.shape[2],
+                                   N if max_len is None else max_len, _dtype_code(q), gate)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+
+
+def packed_fwd(q, k, v, alpha, beta, cu_seqlens, state_in=None, slots_in=None, state_out=None,
+               slots_out=None, *, max_len=None, order=GDN_PREDICT_THEN_DECAY, scale=1.0, out=None,
+               workspace=None, timer=None):
+    """Packed ragged sequences with a pool of states: gdn_packed_fwd.
+    q, k [N,Hk,dk], v [N,Hv,dv] (bf16 or fp32; slices of a wider projection
+    along the heads are taken as they are), alpha [N,Hv] or [N,Hv,dk], beta
+    [N,Hv], cu_seqlens [S+1] int32; state pools [slots,Hv,dv,dk], slots [S]
+    int32 (-1: a zero start state, an end state not written; None: sequence s
+    has slot s).  state_out None: a new pool [S,Hv,dv,dk], in the sequences'
+    order.  max_len: a bound on the lengths (it picks kernels; None: N).
+    Returns (out [N,Hv,dv] of q's dtype, state_out)."""
+    import torch
+    N, S, Hk, Hv, dk, dv, gate = _packed_check(q, k, v, alpha, beta, cu_seqlens,
+                                               (state_in, state_out), (slots_in, slots_out))
+    if state_out is None:
+        if slots_out is not None:
+            raise ValueError("slots_out needs state_out")
+        state_out = torch.empty((S, Hv, dv, dk), dtype=torch.float32, device=q.device)
+    if out is None:
+        out = torch.empty((N, Hv, dv), dtype=q.dtype, device=q.device)
+    elif out.shape != (N, Hv, dv) or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [N,Hv,dv] of q's dtype")
+    if max_len is None:
+        max_len = N
+    code = _dtype_code(q)
+    if workspace is None:
+        n = lib().gdn_packed_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, code, gate)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    sq, sk, sv = _token_strides(q, k, v)
+    args = (N, S, Hk, Hv, dk, dv, 0 if state_in is None else state_in.shape[0], state_out.shape[0], max_len, code, gate, order, scale,
+            _addr(q), sq, _addr(k), sk, _addr(v), sv, _addr(alpha), _addr(beta), _addr(cu_seqlens),
+            _addr(state_in), _addr(slots_in), _addr(state_out), _addr(slots_out), _addr(out),
+            _addr(workspace), 0 if workspace is None else workspace.numel())
+    rc = _on_device(q.device, lambda *a: _call("gdn_packed_fwd", a, timer), args)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_packed_fwd")
+    return out, state_out
+
+
+# ---- layer norm -------------------------------------------------------------------
+
+def _norm_code(dtype):
+    import torch
+    if dtype == torch.bfloat16:
+        return GDN_BF16
+    if dtype == torch.float32:
+        return GDN_F32
+    raise TypeError(f"layer norm takes bfloat16 or float32, got {dtype}")
+
+
+def _norm_check(x, params, stats):
+    import torch
+    if x.dim() < 1 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be contiguous and on the GPU")
+    n = x.shape[-1]
+    if n == 0:
+        raise ValueError("rows must hold at least one element")
+    rows = x.numel() // n
+    for t in params:
+        if t is not None and t.shape != (n,):
+            raise ValueError("weight and bias must be [n]")
+    for t in stats:
+        if t is not None and t.numel() != rows:
+            raise ValueError("mean and rstd must hold one value a row")
+    for t in (*params, *stats):
+        if t is not None and (t.dtype != torch.float32 or t.device != x.device or not t.is_contiguous()):
+            raise ValueError("weight, bias, mean and rstd must be contiguous float32 on x's GPU")
+    return rows, n
+
+
+def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=None, out=None, timer=None):
+    """Layer norm over the last dimension: gdn_layer_norm_fwd.  x bf16 or fp32,
+    weight and bias [n] fp32 or None; out_dtype: bf16 or fp32 (None: x's).
+    Returns (y, mean, rstd), the statistics fp32 and shaped as x without its
+    last dimension."""
+    import torch
+    rows, n = _norm_check(x, (weight, bias), ())
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape or out.device != x.device or not out.is_contiguous() or out_dtype not in (None, out.dtype):
+        raise ValueError("out must be contiguous, shaped as x and of out_dtype")
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    args = (rows, n, _norm_code(x.dtype), _norm_code(out.dtype), eps, _addr(x), _addr(weight), _addr(bias),
+            _addr(out), _addr(mean), _addr(rstd))
+    rc = _on_device(x.device, lambda *a: _call("gdn_layer_norm_fwd", a, timer), args)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_layer_norm_fwd")
+    return out, mean, rstd
+
+
+def layer_norm_backward(grad_y, x, weight, mean, rstd, *, want_x=True, want_weight=True, want_bias=True,
+                        workspace=None, timer=None):
+    """Gradients of layer_norm_fwd: gdn_layer_norm_backward.  Returns (grad_x of
+    x's dtype, grad_weight [n], grad_bias [n] fp32), None where not wanted."""
+    import torch
+    rows, n = _norm_check(x, (weight,), (mean, rstd))
+    if grad_y.shape != x.shape or grad_y.device != x.device or not grad_y.is_contiguous():
+        raise ValueError("grad_y must be contiguous and shaped as x")
+    dev = x.device
+    dx = torch.empty_like(x) if want_x else None
+    dw = torch.empty(n, dtype=torch.float32, device=dev) if want_weight else None
+    db = torch.empty(n, dtype=torch.float32, device=dev) if want_bias else None
+    if workspace is None and (want_weight or want_bias):
+        workspace = torch.empty(lib().gdn_layer_norm_workspace_bytes(rows, n), dtype=torch.uint8, device=dev)
+    args = (rows, n, _norm_code(x.dtype), _norm_code(grad_y.dtype), _addr(grad_y), _addr(x), _addr(weight),
+            _addr(mean), _addr(rstd), _addr(dx), _addr(dw), _addr(db), _addr(workspace),
+            0 if workspace is None else workspace.numel())
+    rc = _on_device(dev, lambda *a: _call("gdn_layer_norm_backward", a, timer), args)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_layer_norm_backward")
+    return dx, dw, db

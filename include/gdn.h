@@ -296,6 +296,107 @@ int gdn_seqpar_fwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv,
                    float* out, float* state_out,
                    void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * gdn_packed_fwd — the forward over packed ragged sequences with a pool of
+ * states: a server's step (prompts of any length beside single and drafted
+ * tokens) or a trainer's packed documents, in one call.  Sequence s holds
+ * tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1; it starts from slot
+ * slots_in[s] of the pool state_in and its end state goes to slot
+ * slots_out[s] of the pool state_out.  Value head h reads key head
+ * h / (Hv / Hk) (the recurrence above per value head).
+ *   q, k        [N, Hk, dk], v [N, Hv, dv]; bf16 or fp32 (dtype); tokens
+ *               q_stride, k_stride, v_stride elements apart (a slice of a
+ *               wider projection), heads of a token contiguous
+ *   alpha       [N, Hv] fp32 (scalar gate) or [N, Hv, dk] (channel), >= 0 (a
+ *               zero gate forgets the state)
+ *   beta        [N, Hv] fp32
+ *   cu_seqlens  [S + 1] int32, on the device, not falling, within 0 .. N
+ *   state_in    [n_in, Hv, dv, dk] fp32, or NULL: every start state zero
+ *   slots_in    [S] int32 on the device, or NULL: sequence s has slot s; an
+ *               index outside the pool (-1): a zero start state
+ *   state_out   [n_out, Hv, dv, dk] fp32, or NULL: end states not wanted; may
+ *               equal state_in (in place)
+ *   slots_out   as slots_in; an index outside the pool: not written.  Slots
+ *               that no sequence writes are left as they were.  Two sequences
+ *               may start from one slot; a slot that is written must not be
+ *               another sequence's in slots_out, nor another's start (its
+ *               contents would depend on timing)
+ *   out         [N, Hv, dv], dtype (rounded once); rows outside every
+ *               sequence are left as they were
+ *   max_len     the caller's bound on the lengths.  It only picks kernels
+ *               and the workspace: longer sequences are computed all the
+ *               same.  1 for single tokens; N where nothing is known
+ *   workspace   gdn_packed_workspace_bytes(...) bytes (0 without chunk
+ *               kernels); two calls that may overlap need two
+ * A NaN or an infinity in v reaches the later tokens of its value feature and
+ * the other tokens of its chunk (64), nothing of other sequences or heads.
+ * An empty sequence copies its start state.  Values of cu_seqlens out of
+ * order or range are clamped, so they never lead out of the buffers.
+ * Sequences of 64 tokens or more run in chunks on the matrix cores for
+ * bf16, scalar gates, dk = dv in {64, 128} (gdn_packed_path); everything
+ * else runs token by token.  Both hold states and sums in fp32.  No call
+ * synchronises; all of them can be captured into a graph.
+ * Alignment: q, k, v, out, the pools, a channel alpha and the workspace on
+ * 16 bytes, token strides multiples of 16 bytes; the rest on 4; else
+ * GDN_E_ARG.  dk, dv as for gdn_chunk_fwd.  GDN_E_SHAPE: negative sizes, Hv
+ * not a multiple of Hk, strides shorter than a row, a pool without indices
+ * smaller than S, N or S of 2^31 or more, (N / 64 + S) Hv of 2^27 or more.
+ */
+int gdn_packed_fwd(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                   int64_t n_in, int64_t n_out, int64_t max_len, int32_t dtype, int32_t gate, int32_t order,
+                   float scale, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, const float* alpha, const float* beta,
+                   const int32_t* cu_seqlens, const float* state_in, const int32_t* slots_in,
+                   float* state_out, const int32_t* slots_out, void* out,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gdn_packed_fwd needs for these arguments (0: none, or the
+ * arguments do not validate).  Host only. */
+size_t gdn_packed_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk,
+                                  int64_t dv, int64_t max_len, int32_t dtype, int32_t gate);
+
+/* Whether gdn_packed_fwd has chunk kernels for long sequences of these shapes
+ * (GDN_PATH_MFMA) or runs every sequence token by token (GDN_PATH_VALU), or a
+ * negative status.  Host only. */
+int gdn_packed_path(int64_t dk, int64_t dv, int32_t dtype, int32_t gate);
+
+/*
+ * gdn_layer_norm_fwd — layer norm of rows of n elements, as the DeltaNet
+ * block normalises the heads' outputs (rows of dv) and its input (rows of
+ * model width): y = (x - mean) rstd weight + bias, rstd = 1 / sqrt(var + eps),
+ * var the mean of (x - mean)^2.  One pass over x; statistics in fp32.
+ *   x           [rows, n], x_dtype;  y [rows, n], y_dtype (rounded once)
+ *   weight      [n] fp32 or NULL (ones);  bias [n] fp32 or NULL (zeros)
+ *   mean, rstd  [rows] fp32, what the backward takes, or NULL: not wanted
+ * y may equal x (same dtype).  Pointers aligned to their elements; rows of a
+ * multiple of 8 (bf16 to bf16) or 4 elements with 16-byte aligned pointers
+ * move in whole vectors, others element by element.  n <= 16384, else
+ * GDN_E_UNSUPPORTED.
+ */
+int gdn_layer_norm_fwd(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps,
+                       const void* x, const float* weight, const float* bias, void* y,
+                       float* mean, float* rstd, void* stream);
+
+/*
+ * gdn_layer_norm_backward — its gradients: with g = grad_y weight and
+ * xhat = (x - mean) rstd,
+ *   grad_x = rstd (g - mean(g) - xhat mean(g xhat)),
+ *   grad_weight = sum over rows of grad_y xhat, grad_bias = sum of grad_y.
+ * grad_y has y_dtype, grad_x x_dtype; either may be the other's buffer if the
+ * types agree.  grad_x, grad_weight, grad_bias NULL: not wanted.  The sums
+ * over rows are taken in a fixed order (repeated calls give identical
+ * results); they need gdn_layer_norm_workspace_bytes(rows, n) bytes.
+ */
+int gdn_layer_norm_backward(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype,
+                            const void* grad_y, const void* x, const float* weight,
+                            const float* mean, const float* rstd, void* grad_x,
+                            float* grad_weight, float* grad_bias,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gdn_layer_norm_backward needs (0 when the sizes do not
+ * validate).  Host only. */
+size_t gdn_layer_norm_workspace_bytes(int64_t rows, int64_t n);
+
 /* Workspace bytes needed by gdn_seqpar_fwd with n_segments, or, for
  * n_segments = 1, by either gdn_seqpar_fwd or gdn_chunk_fwd; 0 when the
  * arguments do not validate.  Host only. */
@@ -391,6 +492,23 @@ int gdn_backward_timed(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv,
                        float* grad_beta, float* grad_state0,
                        void* workspace, size_t workspace_bytes, void* stream,
                        gdn_timer* timer);
+
+int gdn_packed_fwd_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                         int64_t n_in, int64_t n_out, int64_t max_len, int32_t dtype, int32_t gate,
+                         int32_t order, float scale, const void* q, int64_t q_stride,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         const float* alpha, const float* beta, const int32_t* cu_seqlens,
+                         const float* state_in, const int32_t* slots_in, float* state_out,
+                         const int32_t* slots_out, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream, gdn_timer* timer);
+int gdn_layer_norm_fwd_timed(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps,
+                             const void* x, const float* weight, const float* bias, void* y,
+                             float* mean, float* rstd, void* stream, gdn_timer* timer);
+int gdn_layer_norm_backward_timed(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype,
+                                  const void* grad_y, const void* x, const float* weight,
+                                  const float* mean, const float* rstd, void* grad_x,
+                                  float* grad_weight, float* grad_bias, void* workspace,
+                                  size_t workspace_bytes, void* stream, gdn_timer* timer);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,207 @@
+"""gdn_layer_norm_fwd / _backward against the definition in 64 bits.
+
+Tolerances, derived before the first run: fp32 sums over a row of n elements
+(a thread's run of up to 32, then a tree) are off by at most about
+(32 + log2 n) 2^-24 < 3e-6 of the sum of magnitudes, and each step of the
+formulas by 2^-24: 1e-5 of the largest value of the output for y and dx, 1e-5
+relative for mean (to the row's largest value) and rstd; a bf16 output adds
+half a step, 2^-8 of the value.  The weight's sums run over up to `rows`
+terms, at most rows / 1024 + 64 of them in sequence: 1e-5 of the root of the
+terms' square sum times their number's root, which bounds their magnitudes' sum.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from gated_delta_rule_12_amd import gdn
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    gdn.lib()
+
+
+def T(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+def make(rows, n, xt, yt, seed, offset=0.0):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    x = ((torch.randn(rows, n, generator=g) * (0.5 + torch.rand(rows, 1, generator=g)) + offset).to(T(xt))).cuda()
+    dy = torch.randn(rows, n, generator=g).to(T(yt)).cuda()
+    return x, dy, (1 + 0.3 * torch.randn(n, generator=g)).cuda(), (0.2 * torch.randn(n, generator=g)).cuda()
+
+
+def near(a, ref, dtype, axis_max=None):
+    a, ref = a.double().cpu(), ref.cpu()
+    top = ref.abs().max() if ref.numel() else 0.0
+    lim = 1e-5 * top + (2.0**-8 * ref.abs() if dtype == "bf16" else 0.0)
+    bad = (a - ref).abs() > lim
+    assert not bad.any(), (int(bad.sum()), float((a - ref).abs().max()), float(top))
+
+
+SIZES = [(1, 1), (5, 3), (1, 128), (16, 128), (1000, 128), (77, 16), (130, 24), (33, 127), (9, 100), (64, 256), (300, 512),
+         (7, 1000), (19, 2048), (3, 1025), (11, 4097), (5, 8192), (2, 16384), (4, 12345), (1, 16383), (5000, 64), (70001, 8)]
+
+
+@pytest.mark.parametrize("xt,yt", [("f32", "bf16"), ("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("rows,n", SIZES)
+def test_forward_and_backward(rows, n, xt, yt):
+    import torch
+    print(f"case rows={rows} n={n} {xt} {yt}", flush=True)
+    x, dy, w, b = make(rows, n, xt, yt, rows + n, offset=0.5)
+    y, mean, rstd = gdn.layer_norm_fwd(x, w, b, eps=EPS, out_dtype=T(yt))
+    X = x.double()
+    mu = X.mean(1)
+    r = ((X - mu[:, None]).square().mean(1) + EPS).rsqrt()
+    xhat = (X - mu[:, None]) * r[:, None]
+    near(mean, mu, "f32")
+    # rstd takes up a rounding of the centred values: relative to their size
+    assert ((rstd.double() - r).abs() <= 1e-5 * r * (1 + X.abs().max(1).values * r * 2.0**-10)).all()
+    if n > 1:
+        near(y, xhat * w.double() + b.double(), yt)
+    dx, dw, db = gdn.layer_norm_backward(dy, x, w, mean, rstd)
+    # from the statistics the forward left, as the call gets them
+    mu, r = mean.double(), rstd.double()
+    xhat = (X - mu[:, None]) * r[:, None]
+    D = dy.double()
+    g = D * w.double()
+    m1, m2 = g.mean(1, keepdim=True), (g * xhat).mean(1, keepdim=True)
+    ref = r[:, None] * (g - m1 - xhat * m2)
+    scale = (r[:, None] * (g.abs() + m1.abs() + (xhat * m2).abs())).max().cpu()
+    lim = 1e-5 * scale + (2.0**-8 * ref.abs().cpu() if xt == "bf16" else 0.0)
+    assert ((dx.double() - ref).abs().cpu() <= lim).all()
+    for got, terms in ((dw, D * xhat), (db, D)):
+        lim = 1e-5 * terms.square().sum(0).sqrt() * rows**0.5
+        assert ((got.double() - terms.sum(0)).abs() <= lim + 1e-30).all()
+
+
+def test_gradients_against_differences():
+    """The gradients of a weighted sum of the outputs, by central differences of the 64-bit definition."""
+    import torch
+    x, dy, w, b = make(6, 40, "f32", "f32", 3)
+    y, mean, rstd = gdn.layer_norm_fwd(x, w, b)
+    dx, dw, db = gdn.layer_norm_backward(dy, x, w, mean, rstd)
+
+    def loss(X, W, B):
+        m = X.mean(1, keepdim=True)
+        return (((X - m) / ((X - m).square().mean(1, keepdim=True) + EPS).sqrt() * W + B) * dy.double()).sum()
+    args = [x.double(), w.double(), b.double()]
+    h = 1e-5
+    for which, got in enumerate((dx, dw, db)):
+        flat = args[which].reshape(-1)
+        for i in range(0, flat.numel(), 7):
+            old = float(flat[i])
+            flat[i] = old + h
+            up = loss(*args)
+            flat[i] = old - h
+            down = loss(*args)
+            flat[i] = old
+            # second differences of this loss are of the order of its values: h^2 of them
+            assert abs(float(up - down) / (2 * h) - float(got.reshape(-1)[i])) <= 1e-4
+
+
+def test_without_weight_and_parts():
+    import torch
+    x, dy, w, b = make(50, 96, "f32", "bf16", 4)
+    y, mean, rstd = gdn.layer_norm_fwd(x, out_dtype=torch.bfloat16)
+    X = x.double()
+    xhat = (X - X.mean(1, keepdim=True)) * (X.var(1, unbiased=False, keepdim=True) + EPS).rsqrt()
+    near(y, xhat, "bf16")
+    y2, _, _ = gdn.layer_norm_fwd(x, w, out_dtype=torch.bfloat16)
+    near(y2, xhat * w.double(), "bf16")
+    whole = gdn.layer_norm_backward(dy, x, w, mean, rstd)
+    for i, kw in enumerate(("want_x", "want_weight", "want_bias")):
+        part = gdn.layer_norm_backward(dy, x, w, mean, rstd, **{k: k == kw for k in ("want_x", "want_weight", "want_bias")})
+        assert torch.equal(part[i], whole[i]) and all(p is None for j, p in enumerate(part) if j != i)
+
+
+def test_constant_large_and_bad_rows():
+    """A constant row, a row far from zero, infinities and NaN in one row."""
+    import torch
+    x, dy, w, b = make(8, 128, "f32", "f32", 5)
+    x[1] = 3.0
+    x[2] += 1e4
+    x[4, 5] = float("inf")
+    x[5, 6] = float("nan")
+    y, mean, rstd = gdn.layer_norm_fwd(x, w, b)
+    assert torch.equal(y[1], b)
+    assert abs(float(rstd[1]) - EPS**-0.5) < 1e-2
+    X = x[2].double()
+    ref = (X - X.mean()) * (X.var(unbiased=False) + EPS).rsqrt() * w.double() + b.double()
+    # the row's values are 1e4 with fp32 steps of 1e-3: taken as given, so only
+    # the mean's rounding shows, 2^-24 1e4 against a spread of one
+    assert (y[2].double() - ref).abs().max() < 1e-2
+    rows = torch.tensor([0, 1, 2, 3, 6, 7]).cuda()
+    assert torch.isfinite(y[rows]).all() and torch.isnan(y[5]).all() and not torch.isfinite(y[4]).any()
+    dx, dw, db = gdn.layer_norm_backward(dy, x, w, mean, rstd)
+    assert torch.isfinite(dx[rows]).all() and torch.isfinite(db).all()
+
+
+def test_unaligned_views_and_aliases():
+    import torch
+    x, dy, w, b = make(40, 64, "bf16", "bf16", 6)
+    ref = gdn.layer_norm_fwd(x, w, b)[0]
+    flat = torch.zeros(40 * 64 + 1, dtype=torch.bfloat16, device="cuda")
+    flat[1:] = x.reshape(-1)
+    view = flat[1:].view(40, 64)
+    assert view.data_ptr() % 16 != 0
+    y, mean, rstd = gdn.layer_norm_fwd(view, w, b)
+    near(y, ref.double(), "bf16")
+    inplace = x.clone()
+    gdn.layer_norm_fwd(inplace, w, b, out=inplace)
+    assert torch.equal(inplace, ref)
+
+
+def test_empty_and_deterministic_and_replayed():
+    import torch
+    x = torch.empty((0, 64), device="cuda")
+    y, mean, rstd = gdn.layer_norm_fwd(x)
+    dx, dw, db = gdn.layer_norm_backward(y, x, None, mean, rstd)
+    torch.cuda.synchronize()
+    assert y.shape == (0, 64) and (dw == 0).all() and (db == 0).all()
+    x, dy, w, b = make(30011, 128, "f32", "bf16", 7)
+    y, mean, rstd = gdn.layer_norm_fwd(x, w, b, out_dtype=torch.bfloat16)
+    first = gdn.layer_norm_backward(dy, x, w, mean, rstd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gdn.layer_norm_backward(dy, x, w, mean, rstd)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = gdn.layer_norm_backward(dy, x, w, mean, rstd)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, first))
+
+
+def test_after_the_delta_rule():
+    """The heads' norm behind the packed rule, forward and backward, as a block uses it."""
+    import torch
+    from packed_case import Packed
+    c = Packed((70, 200, 1), 2, 4, 64, 64, seed=21).make()
+    out, _ = gdn.packed_fwd(*(c.cuda(n) for n in ("q", "k", "v", "alpha", "beta", "cu", "pool", "slots_in")))
+    w = torch.rand(64).cuda() + 0.5
+    y, mean, rstd = gdn.layer_norm_fwd(out, w)
+    ref, _ = c.forward()
+    ref = torch.from_numpy(ref)
+    mu = ref.mean(-1, keepdim=True)
+    want = (ref - mu) * ((ref - mu).square().mean(-1, keepdim=True) + EPS).rsqrt() * w.double().cpu()
+    # two bf16 roundings: the rule's outputs (scaled by rstd) and the norm's
+    lim = 2.0**-8 * (ref.abs() * rstd.double().cpu()[..., None] * w.max().item() + want.abs()) * 1.01 + 2.0**-8 * (
+        (ref.abs() * rstd.double().cpu()[..., None]).amax(-1, keepdim=True) * (w.max().item() * (1 + want.abs())))
+    assert ((y.double().cpu() - want).abs() <= lim).all()
+    assert mean.shape == (271, 4)

@@ -1,0 +1,128 @@
+"""Host-side checks of the packed rule's and layer norm's entry points: sizes,
+paths and refusals, which come before any device is touched (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from gated_delta_rule_12_amd import gdn
+
+F = ctypes.c_void_p(0x10000)  # never dereferenced: every call below is refused first
+NUL = ctypes.c_void_p(0)
+OK, ARG, SHAPE, UNSUP, WS = gdn.GDN_OK, gdn.GDN_E_ARG, gdn.GDN_E_SHAPE, gdn.GDN_E_UNSUPPORTED, gdn.GDN_E_WORKSPACE
+
+
+def fwd(N=100, S=2, Hk=2, Hv=4, dk=64, dv=64, n_in=2, n_out=2, max_len=1, dtype=1, gate=0, order=0, q=F, sq=None, k=F,
+        sk=None, v=F, sv=None, alpha=F, beta=F, cu=F, s_in=F, slots_in=NUL, s_out=F, slots_out=NUL, out=F, ws=NUL, wsb=0):
+    sq = Hk * dk if sq is None else sq
+    sk = Hk * dk if sk is None else sk
+    sv = Hv * dv if sv is None else sv
+    return gdn.lib().gdn_packed_fwd(N, S, Hk, Hv, dk, dv, n_in, n_out, max_len, dtype, gate, order, 1.0, q, sq, k, sk, v, sv,
+                                    alpha, beta, cu, s_in, slots_in, s_out, slots_out, out, ws, wsb, NUL)
+
+
+ODD = ctypes.c_void_p(0x10002)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dtype=2), ARG), (dict(gate=3), ARG), (dict(order=-1), ARG),
+    (dict(N=-1), SHAPE), (dict(S=-1), SHAPE), (dict(Hk=3), SHAPE), (dict(Hk=0), SHAPE), (dict(dk=0), SHAPE),
+    (dict(max_len=-1), SHAPE), (dict(n_in=-1), SHAPE), (dict(N=2**31), SHAPE), (dict(S=2**31), SHAPE),
+    (dict(S=2**25, Hv=8, n_in=2**25, n_out=2**25), SHAPE),     # more workgroups than a grid holds
+    (dict(dk=72), UNSUP), (dict(dv=144), UNSUP), (dict(dk=8), UNSUP),
+    (dict(sq=127), SHAPE), (dict(sv=255), SHAPE), (dict(sk=2**31), SHAPE),
+    (dict(sq=132), ARG), (dict(sk=129), ARG), (dict(sv=258, dtype=0), ARG),   # strides of whole 16-byte pieces
+    (dict(q=NUL), ARG), (dict(k=NUL), ARG), (dict(v=NUL), ARG), (dict(alpha=NUL), ARG), (dict(beta=NUL), ARG),
+    (dict(cu=NUL), ARG), (dict(out=NUL), ARG),
+    (dict(q=ODD), ARG), (dict(k=ODD), ARG), (dict(v=ODD), ARG), (dict(out=ODD), ARG), (dict(s_in=ODD), ARG),
+    (dict(s_out=ODD), ARG), (dict(cu=ODD), ARG), (dict(slots_in=ODD), ARG), (dict(beta=ODD), ARG),
+    (dict(alpha=ctypes.c_void_p(0x10004), gate=1), ARG),
+    (dict(n_in=1), SHAPE), (dict(n_out=1), SHAPE),             # a pool without indices holds every sequence
+    (dict(max_len=100), WS), (dict(max_len=100, ws=F, wsb=16), WS),
+    (dict(S=0), OK), (dict(Hk=0, Hv=0), OK),                   # nothing to do
+])
+def test_packed_refusals(kw, want):
+    assert fwd(**kw) == want
+
+
+def test_packed_workspace_and_path():
+    ws = gdn.gdn_packed_workspace_bytes
+    assert gdn.gdn_packed_path(128, 128, 1, 0) == gdn.GDN_PATH_MFMA
+    assert gdn.gdn_packed_path(64, 64, 1, 0) == gdn.GDN_PATH_MFMA
+    for a in ((64, 128, 1, 0), (128, 128, 0, 0), (128, 128, 1, 1), (32, 32, 1, 0)):
+        assert gdn.gdn_packed_path(*a) == gdn.GDN_PATH_VALU
+    assert gdn.gdn_packed_path(60, 64, 1, 0) == UNSUP and gdn.gdn_packed_path(64, 64, 5, 0) == ARG
+    # single tokens, and shapes without chunk kernels, need none
+    assert ws(256, 256, 16, 16, 128, 128, 1, 1, 0) == 0
+    assert ws(5000, 3, 4, 4, 128, 128, 5000, 0, 0) == 0
+    assert ws(5000, 3, 4, 4, 128, 128, 5000, 1, 1) == 0
+    assert ws(5000, 3, 4, 3, 128, 128, 5000, 1, 0) == 0      # refused
+    small, large = ws(5000, 3, 4, 4, 128, 128, 400, 1, 0), ws(5000, 3, 4, 4, 128, 128, 5000, 1, 0)
+    assert 0 < small < large and large % 256 == 0
+
+
+def norm_fwd(rows=4, n=64, xt=0, yt=1, x=F, w=F, b=F, y=F, m=F, r=F):
+    return gdn.lib().gdn_layer_norm_fwd(rows, n, xt, yt, 1e-5, x, w, b, y, m, r, NUL)
+
+
+def norm_bwd(rows=4, n=64, xt=0, yt=1, dy=F, x=F, w=F, m=F, r=F, dx=F, dw=F, db=F, ws=F, wsb=1 << 30):
+    return gdn.lib().gdn_layer_norm_backward(rows, n, xt, yt, dy, x, w, m, r, dx, dw, db, ws, wsb, NUL)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(xt=2), ARG), (dict(yt=-1), ARG), (dict(rows=-1), SHAPE), (dict(n=0), SHAPE), (dict(n=16385), UNSUP),
+    (dict(x=NUL), ARG), (dict(y=NUL), ARG), (dict(x=ODD), ARG), (dict(w=ODD), ARG), (dict(b=ODD), ARG), (dict(m=ODD), ARG),
+    (dict(y=ctypes.c_void_p(0x10001)), ARG), (dict(rows=0), OK),
+])
+def test_norm_forward_refusals(kw, want):
+    assert norm_fwd(**kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(xt=2), ARG), (dict(yt=7), ARG), (dict(rows=-1), SHAPE), (dict(n=-3), SHAPE), (dict(n=20000), UNSUP),
+    (dict(dy=NUL), ARG), (dict(x=NUL), ARG), (dict(m=NUL), ARG), (dict(r=NUL), ARG), (dict(dx=ODD), ARG), (dict(dw=ODD), ARG),
+    (dict(ws=NUL), WS), (dict(wsb=100), WS), (dict(ws=ctypes.c_void_p(0x10008)), ARG),
+    (dict(dx=NUL, dw=NUL, db=NUL), OK),
+])
+def test_norm_backward_refusals(kw, want):
+    assert norm_bwd(**kw) == want
+
+
+def test_norm_workspace():
+    ws = gdn.gdn_layer_norm_workspace_bytes
+    assert ws(10, 0) == 0 and ws(10, 16385) == 0 and ws(-1, 64) == 0
+    assert ws(1, 64) >= 8 * 64
+    assert ws(1 << 20, 128) <= 2 * 4 * 1024 * 128
+
+
+def test_binding_refuses_before_the_library():
+    """Shapes, types, devices and strides are checked in the binding."""
+    import torch
+    z = torch.zeros
+    q, v = z(10, 2, 64, dtype=torch.bfloat16), z(10, 4, 64, dtype=torch.bfloat16)
+    a, cu = z(10, 4), torch.tensor([0, 4, 10], dtype=torch.int32)
+    pool = z(2, 4, 64, 64)
+    with pytest.raises(ValueError, match="GPU"):
+        gdn.packed_fwd(q, q, v, a, a, cu, pool)
+    for bad in (dict(q=z(10, 128)), dict(k=q[:9]), dict(v=v[:9]), dict(alpha=z(10, 3)), dict(beta=z(9, 4)), dict(cu=z(0)),
+                dict(cu=cu[None]), dict(pool=z(2, 4, 64)), dict(pool=z(2, 4, 32, 64)), dict(q=q.transpose(1, 2)),
+                dict(q=z(10, 2, 128, dtype=torch.bfloat16)[:, :, ::2])):
+        x = dict(q=q, k=q, v=v, alpha=a, beta=a, cu=cu, pool=pool)
+        x.update(bad)
+        if "q" in bad and "k" not in bad:
+            x["k"] = bad["q"]
+        with pytest.raises(ValueError):
+            gdn.packed_fwd(*x.values())
+    with pytest.raises(TypeError):
+        gdn.packed_fwd(q, q, v.float(), a, a, cu, pool)
+    with pytest.raises(TypeError):
+        gdn.packed_fwd(q, q, v, a, a, cu.long(), pool)
+    with pytest.raises(TypeError):
+        gdn.packed_fwd(q, q, v, a.double(), a, cu, pool)
+    with pytest.raises(ValueError, match="slots"):
+        gdn.packed_fwd(q, q, v, a, a, cu, pool, cu)
+    with pytest.raises(ValueError, match="state_out"):
+        gdn.packed_fwd(q, q, v, a, a, cu, pool, None, None, cu[:2])
+    with pytest.raises(ValueError):
+        gdn.layer_norm_fwd(z(4, 64))
+    with pytest.raises(ValueError):
+        gdn.layer_norm_backward(z(4, 64), z(4, 64), None, z(4), z(4))
