@@ -318,7 +318,7 @@ def _own(s):
                                 order=c["order"])
         return {"out": out, "state": s["pool_out"]}
     dq, dk, dv, da, db, ds = gdn.packed_backward(*args, s["pool"], s["slots"], s["grad_out"], s["grad_state"],
-                                                 max_len=s["max_len"], order=c["order"])
+                                                 order=c["order"])
     return {"dq": dq, "dk": dk, "dv": dv, "dalpha": da, "dbeta": db, "dstate": ds}
 
 
