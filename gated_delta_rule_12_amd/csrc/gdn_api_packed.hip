@@ -79,6 +79,39 @@ int packed_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int6
     return finish(packed_forward(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
+int packed_bwd_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in, int32_t dtype,
+                      int32_t gate, int32_t order, float scale, const void* q, int64_t q_stride, const void* k,
+                      int64_t k_stride, const void* v, int64_t v_stride, const float* alpha, const float* beta,
+                      const int32_t* cu_seqlens, const float* state_in, const int32_t* slots_in, const void* grad_out,
+                      const float* grad_state_out, float* grad_q, float* grad_k, float* grad_v, float* grad_alpha,
+                      float* grad_beta, float* grad_state0, void* workspace, size_t workspace_bytes, void* stream,
+                      gdn_timer* timer) {
+    PackedBwd b{};
+    Packed& p = b.p;
+    p = packed_sizes(N, S, Hk, Hv, dk, dv, n_in, 0, N, dtype, gate, order);
+    int s = packed_check(p);
+    if (s != GDN_OK) return s;
+    if (!chunked_backward_supported(dk, dv, gate)) return GDN_E_UNSUPPORTED;
+    if (S * Hv == 0) return GDN_OK;
+    p.scale = scale;
+    p.q = q; p.k = k; p.v = v;
+    p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.alpha = alpha; p.beta = beta; p.cu = cu_seqlens;
+    p.s_in = state_in; p.slots_in = slots_in;
+    p.timer = timer;
+    if ((s = packed_inputs(p)) != GDN_OK) return s;
+    if (N > 0 && (!grad_out || !grad_q || !grad_k || !grad_v || !grad_alpha || !grad_beta)) return GDN_E_ARG;
+    if (!aligned(grad_out, 16) || !aligned(grad_state_out, 16) || !aligned(grad_q, 16) || !aligned(grad_k, 16) ||
+        !aligned(grad_v, 16) || !aligned(grad_alpha, 4) || !aligned(grad_beta, 4) || !aligned(grad_state0, 16) ||
+        !aligned(workspace, 16))
+        return GDN_E_ARG;
+    const size_t need = packed_backward_workspace(p);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_E_WORKSPACE;
+    b.dout = grad_out; b.ds_out = grad_state_out;
+    b.dq = grad_q; b.dk = grad_k; b.dv = grad_v; b.dalpha = grad_alpha; b.dbeta = grad_beta; b.ds0 = grad_state0;
+    return finish(packed_backward(b, workspace, static_cast<hipStream_t>(stream)));
+}
+
 int norm_check(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype) {
     if ((x_dtype != GDN_F32 && x_dtype != GDN_BF16) || (y_dtype != GDN_F32 && y_dtype != GDN_BF16)) return GDN_E_ARG;
     if (rows < 0 || n <= 0 || rows > ((int64_t)1 << 40)) return GDN_E_SHAPE;
@@ -168,6 +201,36 @@ int gdn_packed_path(int64_t dk, int64_t dv, int32_t dtype, int32_t gate) {
     const int s = packed_check(p);
     if (s != GDN_OK) return s;
     return packed_chunked(p) ? GDN_PATH_MFMA : GDN_PATH_VALU;
+}
+
+int gdn_packed_backward(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in,
+                        int32_t dtype, int32_t gate, int32_t order, float scale, const void* q, int64_t q_stride,
+                        const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* alpha,
+                        const float* beta, const int32_t* cu_seqlens, const float* state_in, const int32_t* slots_in,
+                        const void* grad_out, const float* grad_state_out, float* grad_q, float* grad_k, float* grad_v,
+                        float* grad_alpha, float* grad_beta, float* grad_state0, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    return packed_bwd_common(N, S, Hk, Hv, dk, dv, n_in, dtype, gate, order, scale, q, q_stride, k, k_stride, v, v_stride,
+                             alpha, beta, cu_seqlens, state_in, slots_in, grad_out, grad_state_out, grad_q, grad_k, grad_v,
+                             grad_alpha, grad_beta, grad_state0, workspace, workspace_bytes, stream, nullptr);
+}
+
+int gdn_packed_backward_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in,
+                        int32_t dtype, int32_t gate, int32_t order, float scale, const void* q, int64_t q_stride,
+                        const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* alpha,
+                        const float* beta, const int32_t* cu_seqlens, const float* state_in, const int32_t* slots_in,
+                        const void* grad_out, const float* grad_state_out, float* grad_q, float* grad_k, float* grad_v,
+                        float* grad_alpha, float* grad_beta, float* grad_state0, void* workspace, size_t workspace_bytes,
+                        void* stream, gdn_timer* timer) {
+    return packed_bwd_common(N, S, Hk, Hv, dk, dv, n_in, dtype, gate, order, scale, q, q_stride, k, k_stride, v, v_stride,
+                             alpha, beta, cu_seqlens, state_in, slots_in, grad_out, grad_state_out, grad_q, grad_k, grad_v,
+                             grad_alpha, grad_beta, grad_state0, workspace, workspace_bytes, stream, timer);
+}
+
+size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                                           int32_t dtype, int32_t gate) {
+    const Packed p = packed_sizes(N, S, Hk, Hv, dk, dv, 0, 0, N, dtype, gate, GDN_PREDICT_THEN_DECAY);
+    return packed_check(p) != GDN_OK || !chunked_backward_supported(dk, dv, gate) ? 0 : packed_backward_workspace(p);
 }
 
 int gdn_layer_norm_fwd(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps, const void* x,

@@ -173,7 +173,7 @@ struct Bwd {
             const bool ok = e < kSub * RB && u < m && rb * RB + q < p.dv;
             const int64_t th = (b * p.T + ts + u) * p.H + h;
             s.v[i] = ok ? gdn_ld<DT>(p.v, th * p.dv + rb * RB + q) : 0.f;
-            s.dout[i] = ok ? a.dout[th * p.dv + rb * RB + q] : 0.f;
+            s.dout[i] = ok ? static_cast<const float*>(a.dout)[th * p.dv + rb * RB + q] : 0.f;
         }
     }
     __device__ void stage_store(const Stage& s) const {

@@ -51,6 +51,7 @@
 
 #include "gdn_internal.h"
 #include "gdn_mfma_common.h"
+#include "gdn_packed_common.h"
 #include "../../include/gdn.h"
 
 namespace gdn {
@@ -132,11 +133,100 @@ __device__ __forceinline__ int blk_m(int i) { return i >= 6 ? 3 : i >= 3 ? 2 : i
 __device__ __forceinline__ int blk_n(int i) { const int m = blk_m(i); return i - m * (m + 1) / 2; }
 __device__ __forceinline__ void st4f(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
 
+// Where a chunk's rows lie: offsets of its first token, and what a token
+// further adds, in elements; and its record in the workspace.
+struct ChunkAt {
+    int64_t ci;  // record
+    int nt;      // tokens
+    int64_t g0, q0, k0, v0, o0;  // alpha and beta; q; k; v; dL/d out, dv (and dq, dk)
+};
+// One (sequence, head)'s chunks: the dense batch [B, T, H, D] ...
+template <int D>
+struct DenseGeo {
+    int64_t T, H, NC, bh0;
+    __device__ int64_t gs() const { return H; }
+    __device__ int64_t qs() const { return H * D; }
+    __device__ int64_t ks() const { return H * D; }
+    __device__ int64_t vs() const { return H * D; }
+    __device__ int64_t os() const { return H * D; }
+    struct Head {
+        int64_t bl, b, h, state;  // state: of [B, H, D, D] arrays
+        int64_t start;            // of the start state, below zero: none
+        int NC;
+    };
+    __device__ Head head(int64_t bl) const {
+        Head x;
+        x.bl = bl;
+        x.state = x.start = bh0 + bl;
+        x.b = x.state / H;
+        x.h = x.state - x.b * H;
+        x.NC = (int)NC;
+        return x;
+    }
+    __device__ ChunkAt at(const Head& x, int c) const {
+        const int64_t row0 = (x.b * T + (int64_t)c * C) * H + x.h;
+        return {x.bl * NC + c, (int)min<int64_t>(C, T - (int64_t)c * C), row0, row0 * D, row0 * D, row0 * D, row0 * D};
+    }
+    __device__ bool chunk(int64_t block, int, ChunkAt& x) const {
+        const int64_t bl = block / NC;
+        x = at(head(bl), (int)(block - bl * NC));
+        return true;
+    }
+};
+// ... and packed sequences (gdn_packed_common.h), heads h0 .. h0 + nh - 1 of
+// one launch.  Gradients of q and k are per value head here; k_bfold adds
+// those of a shared key head.
+template <int D>
+struct PackedGeo {
+    Offsets off;
+    int Hk, Hv, group, h0, nh;
+    int64_t q_stride, k_stride, v_stride, n_in;
+    const int32_t* slots;
+    __device__ int64_t gs() const { return Hv; }
+    __device__ int64_t qs() const { return q_stride; }
+    __device__ int64_t ks() const { return k_stride; }
+    __device__ int64_t vs() const { return v_stride; }
+    __device__ int64_t os() const { return (int64_t)Hv * D; }
+    struct Head {
+        int64_t begin, n, place, state, start;
+        int hl, NC;
+    };
+    __device__ Head head_of(int64_t s, int hl) const {
+        const Span sp = span_of(off, s);
+        Head x;
+        x.begin = sp.begin;
+        x.n = sp.n;
+        x.place = (sp.begin >> 6) + s;
+        x.hl = hl;
+        x.NC = (int)((sp.n + C - 1) / C);
+        x.state = s * Hv + h0 + hl;
+        const int64_t slot = slots ? (int64_t)slots[s] : s;
+        x.start = slot < 0 || slot >= n_in ? -1 : slot * Hv + h0 + hl;
+        return x;
+    }
+    __device__ Head head(int64_t idx) const {
+        const int64_t s = (int)idx / nh;
+        return head_of(s, (int)idx - (int)s * nh);
+    }
+    __device__ ChunkAt at(const Head& x, int c) const {
+        const int64_t t = x.begin + (int64_t)c * C, h = h0 + x.hl, hk = h / group;
+        return {(x.place + c) * nh + x.hl, (int)min<int64_t>(C, x.n - (int64_t)c * C), t * Hv + h, t * q_stride + hk * D,
+                t * k_stride + hk * D, t * v_stride + h * D, (t * Hv + h) * D};
+    }
+    __device__ bool chunk(int64_t block, int lane, ChunkAt& x) const {
+        const int place = (int)block / nh, hl = (int)block - place * nh;
+        const Head hd = head_of(seq_of_place(off, place, 6, lane), hl);
+        const int64_t c = place - hd.place;
+        if (c < 0 || c >= hd.NC) return false;
+        x = at(hd, (int)c);
+        return true;
+    }
+};
 // (token rows past the sequence end are read at the last real row and
 // replaced by the defaults)
-__device__ __forceinline__ Gate chunk_gate(const Problem& p, int64_t row0, int nt, int lane) {
-    const int64_t r = row0 + (int64_t)min(lane, nt - 1) * p.H;
-    return gate_from(p.alpha[r], p.beta[r], nt, p.order, lane);
+__device__ __forceinline__ Gate chunk_gate(const Problem& p, const ChunkAt& x, int64_t stride, int lane) {
+    const int64_t r = x.g0 + (int64_t)min(lane, x.nt - 1) * stride;
+    return gate_from(p.alpha[r], p.beta[r], x.nt, p.order, lane);
 }
 
 // Rows of a chunk's token factors (lane t: token t): the gate prefix pair,
@@ -180,8 +270,8 @@ struct CbWs {
 // bf16 inputs the K rows sit in the UT tile itself (A goes there once the
 // Gram products are done) and dL/d out comes in two column halves, which
 // keeps the workgroup at 36 KiB, four per compute unit.
-template <int D, int DT>
-__global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 4 : 2) void k_bprep(BwdProblem a, CbWs ws) {
+template <int D, int DT, int OT, class Geo>
+__global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 4 : 2) void k_bprep(BwdProblem a, CbWs ws, Geo geo) {
     using E = std::conditional_t<DT == GDN_BF16, uint16_t, float>;
     constexpr int NB = D / 16, MT = D / 64;
     constexpr int LDK = D + (DT == GDN_BF16 ? 8 : 4);
@@ -202,29 +292,26 @@ __global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 4 : 2) void k_bprep(BwdP
     float* dOs = reinterpret_cast<float*>(kq);
 
     const Problem& p = a.p;
-    const int64_t ci = blockIdx.x;
-    const int64_t bl = ci / p.NC;
-    const int c = (int)(ci - bl * p.NC);
-    const int64_t bh = a.bh0 + bl, b = bh / p.H, h = bh - b * p.H;
-    const int64_t t0 = (int64_t)c * C;
-    const int nt = (int)min<int64_t>(C, p.T - t0);
-    const int64_t row0 = (b * p.T + t0) * p.H + h;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g4 = l >> 4, c16 = l & 15;
+    ChunkAt ck;
+    if (!geo.chunk(blockIdx.x, l, ck)) return;
+    const int64_t ci = ck.ci;
+    const int nt = ck.nt;
 
     // K and Q rows into LDS (rows past the sequence end zero)
     constexpr int KP = C * PPR / kThreads;
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
         const int e = tid + kThreads * i, t = e / PPR, pc = e % PPR;
-        const int64_t src = (row0 + (int64_t)min(t, nt - 1) * p.H) * D + pc * EP;
-        u32x4 kv = *reinterpret_cast<const u32x4*>(static_cast<const E*>(p.k) + src);
-        u32x4 qv = *reinterpret_cast<const u32x4*>(static_cast<const E*>(p.q) + src);
+        const int64_t tr = min(t, nt - 1);
+        u32x4 kv = *reinterpret_cast<const u32x4*>(static_cast<const E*>(p.k) + ck.k0 + tr * geo.ks() + pc * EP);
+        u32x4 qv = *reinterpret_cast<const u32x4*>(static_cast<const E*>(p.q) + ck.q0 + tr * geo.qs() + pc * EP);
         if (t >= nt) kv = qv = u32x4{0, 0, 0, 0};
         *reinterpret_cast<u32x4*>(&Ks[t * LDK + pc * EP]) = kv;
         *reinterpret_cast<u32x4*>(&Qs[t * LDK + pc * EP]) = qv;
     }
     if (w == 0) {
-        const Gate g = chunk_gate(p, row0, nt, l);
+        const Gate g = chunk_gate(p, ck, geo.gs(), l);
         ghi[l] = g.hi;
         glo[l] = g.lo;
         gphi[l] = g.phi;
@@ -340,7 +427,7 @@ __global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 4 : 2) void k_bprep(BwdP
 #pragma unroll
         for (int i = 0; i < OP; ++i) {
             const int e = tid + kThreads * i, t = e / (DH / 4), pc = e % (DH / 4);
-            dov[i] = ld4f(a.dout + (row0 + (int64_t)min(t, nt - 1) * p.H) * D + DH * hh + 4 * pc);
+            dov[i] = ld4in<OT>(a.dout, ck.o0 + (int64_t)min(t, nt - 1) * geo.os() + DH * hh + 4 * pc);
             if (t >= nt) dov[i] = zero4();
         }
     };
@@ -477,43 +564,41 @@ struct RevIn {
     R8<DT> kt[MT][2];
 };
 
-template <int D, int DT, int NS>
+template <int D, int DT, int NS, class Geo>
 struct ChainCtx {
     static constexpr int NB = D / 16, MT = D / 64;
     using Sh = ChainShared<NS>;
     const BwdProblem& a;
     const CbWs& ws;
-    int64_t bl, b, h, bh;
+    const Geo& geo;
+    typename Geo::Head hd;
     int rho, r0, w, l, g4, c16, NC, tid;  // rho: the first slice (rows r0 = 16 rho ..)
-    __device__ int64_t row0(int c) const { return (b * a.p.T + (int64_t)c * C) * a.p.H + h; }
-    __device__ int ntok(int c) const { return (int)min<int64_t>(C, a.p.T - (int64_t)c * C); }
-    __device__ int64_t cidx(int c) const { return bl * NC + c; }
+    __device__ ChunkAt at(int c) const { return geo.at(hd, c); }
+    __device__ int ntok(int c) const { return at(c).nt; }
+    __device__ int64_t cidx(int c) const { return at(c).ci; }
     // gate rows (and, forward, the V slices) of chunk c, clamped to a real chunk
     __device__ void load_gate(GateIn<DT, NS>& x, int c, bool fwd) const {
-        c = min(max(c, 0), NC - 1);
-        const int64_t r = row0(c);
-        const int nt = ntok(c);
-        x.gr = *reinterpret_cast<const f32x2*>(ws.Gr + cidx(c) * Rec<D>::kGr + 2 * tid);
+        const ChunkAt y = at(min(max(c, 0), NC - 1));
+        x.gr = *reinterpret_cast<const f32x2*>(ws.Gr + y.ci * Rec<D>::kGr + 2 * tid);
         if (fwd) {
-            const int64_t o = (r + (int64_t)min(tid >> 2, nt - 1) * a.p.H) * D + r0 + 4 * (tid & 3);
+            const int64_t o = y.v0 + (int64_t)min(tid >> 2, y.nt - 1) * geo.vs() + r0 + 4 * (tid & 3);
 #pragma unroll
             for (int s = 0; s < NS; ++s) x.vr[s] = ldr<DT>(a.p.v, o + 16 * s);
         }
     }
     template <class In>
     __device__ void load_common(In& x, int c) const {
-        const int64_t r = row0(c);
-        const int nt = ntok(c);
-        const int64_t ci = cidx(c);
+        const ChunkAt y = at(c);
+        const int64_t ci = y.ci;
 #pragma unroll
-        for (int at = 0; at < 4; ++at) {
-            const int64_t o = (r + (int64_t)min(16 * at + c16, nt - 1) * a.p.H) * D + key_of<D>(w, 0, 4 * g4);
+        for (int tb = 0; tb < 4; ++tb) {
+            const int64_t o = y.k0 + (int64_t)min(16 * tb + c16, y.nt - 1) * geo.ks() + key_of<D>(w, 0, 4 * g4);
             if constexpr (MT == 2) {
                 const R8<DT> k8 = ldr8<DT>(a.p.k, o);
-                x.kx[at][0] = k8.h[0];
-                x.kx[at][MT - 1] = k8.h[1];
+                x.kx[tb][0] = k8.h[0];
+                x.kx[tb][MT - 1] = k8.h[1];
             } else {
-                x.kx[at][0] = ldr<DT>(a.p.k, o);
+                x.kx[tb][0] = ldr<DT>(a.p.k, o);
             }
         }
 #pragma unroll
@@ -609,8 +694,8 @@ struct ChainCtx {
     }
 };
 
-template <int D, int DT, int NS>
-__device__ void chain_forward(const ChainCtx<D, DT, NS>& cx, ChainShared<NS>& sh, f32x4 (&St)[NS][D / 64]) {
+template <int D, int DT, int NS, class Geo>
+__device__ void chain_forward(const ChainCtx<D, DT, NS, Geo>& cx, ChainShared<NS>& sh, f32x4 (&St)[NS][D / 64]) {
     constexpr int MT = D / 64;
     const CbWs& ws = cx.ws;
     const int w = cx.w, l = cx.l, g4 = cx.g4, c16 = cx.c16;
@@ -706,11 +791,10 @@ __device__ void chain_forward(const ChainCtx<D, DT, NS>& cx, ChainShared<NS>& sh
     }
 }
 
-template <int D, int DT, int NS>
-__device__ void chain_reverse(const ChainCtx<D, DT, NS>& cx, ChainShared<NS>& sh, f32x4 (&St)[NS][D / 64]) {
+template <int D, int DT, int NS, class Geo>
+__device__ void chain_reverse(const ChainCtx<D, DT, NS, Geo>& cx, ChainShared<NS>& sh, f32x4 (&St)[NS][D / 64]) {
     constexpr int MT = D / 64;
     const BwdProblem& a = cx.a;
-    const Problem& p = a.p;
     const CbWs& ws = cx.ws;
     const int w = cx.w, l = cx.l, g4 = cx.g4;
     RevIn<D, DT, NS> xa, xb;
@@ -724,7 +808,7 @@ __device__ void chain_reverse(const ChainCtx<D, DT, NS>& cx, ChainShared<NS>& sh
     f32x4 pdD[NS], pdU[NS], pdv[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) pdD[s] = pdU[s] = pdv[s] = zero4();
-    int64_t pci = cx.cidx(cx.NC - 1), prow = cx.row0(cx.NC - 1);
+    int64_t pci = cx.cidx(cx.NC - 1), prow = cx.at(cx.NC - 1).o0;
     int pnt = 0;
     // chunk c from cur; fetches chunk c - 1 into nxt and the gates of chunk
     // c - 2 into g2; turns g1 (chunk c - 1) into LDS rows at the end
@@ -737,7 +821,7 @@ __device__ void chain_reverse(const ChainCtx<D, DT, NS>& cx, ChainShared<NS>& sh
         for (int s = 0; s < NS; ++s) {
             cx.store_rows(sh, 2, ws.dDl + pci * Rec<D>::kRows, D, pdD[s], C, s);
             cx.store_rows(sh, 3, ws.dUp + pci * Rec<D>::kRows, D, pdU[s], C, s);
-            cx.store_rows(sh, 4, a.dv + prow * D, p.H * D, pdv[s], pnt, s);
+            cx.store_rows(sh, 4, a.dv + prow, cx.geo.os(), pdv[s], pnt, s);
         }
         cx.store_state(sh, ws.dSf + ci * Rec<D>::kState, St);
         cx.partial_KS(sh, cur, St, nt);
@@ -773,7 +857,7 @@ __device__ void chain_reverse(const ChainCtx<D, DT, NS>& cx, ChainShared<NS>& sh
             pdv[s] = bt * du[s];
         }
         pci = ci;
-        prow = cx.row0(c);
+        prow = cx.at(c).o0;
         pnt = nt;
         __syncthreads();
         // dS^T <- gamma_C dS^T + scale Q^T diag(gamma) dO - K^T diag(gamma' beta) dU'
@@ -806,14 +890,14 @@ __device__ void chain_reverse(const ChainCtx<D, DT, NS>& cx, ChainShared<NS>& sh
     for (int s = 0; s < NS; ++s) {
         cx.store_rows(sh, 2, ws.dDl + pci * Rec<D>::kRows, D, pdD[s], C, s);
         cx.store_rows(sh, 3, ws.dUp + pci * Rec<D>::kRows, D, pdU[s], C, s);
-        cx.store_rows(sh, 4, a.dv + prow * D, p.H * D, pdv[s], pnt, s);
+        cx.store_rows(sh, 4, a.dv + prow, cx.geo.os(), pdv[s], pnt, s);
     }
 }
 
 // NS adjacent 16-row slices of a head's state per workgroup and direction:
 // two on heads x slices that fill the compute units that way, one otherwise.
-template <int D, int DT, int NS>
-__global__ __launch_bounds__(kThreads, NS == 1 ? 2 : 1) void k_bchain(BwdProblem a, CbWs ws) {
+template <int D, int DT, int NS, class Geo>
+__global__ __launch_bounds__(kThreads, NS == 1 ? 2 : 1) void k_bchain(BwdProblem a, CbWs ws, Geo geo) {
     constexpr int NB = D / 16, MT = D / 64;
     constexpr int NSL = NB / NS;  // workgroups per head and direction
     __shared__ ChainShared<NS> sh;
@@ -827,40 +911,37 @@ __global__ __launch_bounds__(kThreads, NS == 1 ? 2 : 1) void k_bchain(BwdProblem
     const int64_t head = lin / (2 * NSL);
     const int rem = (int)(lin - head * 2 * NSL);
     const bool rev = rem < NSL;
-    ChainCtx<D, DT, NS> cx{a, ws};
-    cx.bl = head;
+    ChainCtx<D, DT, NS, Geo> cx{a, ws, geo, geo.head(head)};
     cx.rho = NS * (rev ? rem : rem - NSL);
     cx.r0 = 16 * cx.rho;
-    cx.bh = a.bh0 + cx.bl;
-    cx.b = cx.bh / p.H;
-    cx.h = cx.bh - cx.b * p.H;
     const int tid = threadIdx.x;
     cx.tid = tid;
     cx.w = tid >> 6;
     cx.l = tid & 63;
     cx.g4 = cx.l >> 4;
     cx.c16 = cx.l & 15;
-    cx.NC = p.NC;
+    cx.NC = cx.hd.NC;
     // the slices' state rows as accumulator tiles of S^T: tile mi of slice s
     // holds S[r0 + 16 s + c16][key_of(w, mi, 4 g4 + r)]
     f32x4 St[NS][MT];
-    const float* init = rev ? a.ds_out : p.s0;
+    const float* init = rev ? a.ds_out : cx.hd.start >= 0 ? p.s0 : nullptr;
+    const int64_t row = (rev ? cx.hd.state : cx.hd.start) * D + cx.r0 + cx.c16;
 #pragma unroll
     for (int s = 0; s < NS; ++s)
 #pragma unroll
         for (int mi = 0; mi < MT; ++mi)
-            St[s][mi] = init ? ld4f(init + ((cx.bh * D + cx.r0 + 16 * s + cx.c16) * D) + key_of<D>(cx.w, mi, 4 * cx.g4))
+            St[s][mi] = init ? ld4f(init + (row + 16 * s) * D + key_of<D>(cx.w, mi, 4 * cx.g4))
                              : zero4();
-    if (p.NC > 0) {
-        if (rev) chain_reverse<D, DT, NS>(cx, sh, St);
-        else chain_forward<D, DT, NS>(cx, sh, St);
+    if (cx.NC > 0) {
+        if (rev) chain_reverse<D, DT, NS, Geo>(cx, sh, St);
+        else chain_forward<D, DT, NS, Geo>(cx, sh, St);
     }
     if (rev && a.ds0) {
 #pragma unroll
         for (int s = 0; s < NS; ++s)
 #pragma unroll
             for (int mi = 0; mi < MT; ++mi)
-                st4f(a.ds0 + ((cx.bh * D + cx.r0 + 16 * s + cx.c16) * D) + key_of<D>(cx.w, mi, 4 * cx.g4), St[s][mi]);
+                st4f(a.ds0 + (row + 16 * s) * D + key_of<D>(cx.w, mi, 4 * cx.g4), St[s][mi]);
     }
 }
 
@@ -887,19 +968,16 @@ struct GradShared {
 // block's whole set at once, the next phase's before the barrier that ends
 // the current one, the state products' next value block while the current
 // one multiplies.
-template <int D, int DT>
-__global__ __launch_bounds__(kThreads, 2) void k_bgrad(BwdProblem a, CbWs ws) {
+template <int D, int DT, int OT, class Geo>
+__global__ __launch_bounds__(kThreads, 2) void k_bgrad(BwdProblem a, CbWs ws, Geo geo) {
     constexpr int NB = D / 16, MT = D / 64;
     __shared__ __attribute__((aligned(16))) GradShared sh;
     const Problem& p = a.p;
-    const int64_t ci = blockIdx.x;
-    const int64_t bl = ci / p.NC;
-    const int c = (int)(ci - bl * p.NC);
-    const int64_t bh = a.bh0 + bl, b = bh / p.H, h = bh - b * p.H;
-    const int64_t t0 = (int64_t)c * C;
-    const int nt = (int)min<int64_t>(C, p.T - t0);
-    const int64_t row0 = (b * p.T + t0) * p.H + h;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g4 = l >> 4, c16 = l & 15;
+    ChunkAt ck;
+    if (!geo.chunk(blockIdx.x, l, ck)) return;
+    const int64_t ci = ck.ci;
+    const int nt = ck.nt;
     const float* U = ws.U + ci * Rec<D>::kRows;
     const float* Dl = ws.Dl + ci * Rec<D>::kRows;
     const float* dDl = ws.dDl + ci * Rec<D>::kRows;
@@ -912,11 +990,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_bgrad(BwdProblem a, CbWs ws) {
     const float* dSf = ws.dSf + ci * Rec<D>::kState;
     const InE<DT>* KTf = static_cast<const InE<DT>*>(ws.KTf) + ci * Rec<D>::kFrag;
     const InE<DT>* QTf = static_cast<const InE<DT>*>(ws.QTf) + ci * Rec<D>::kFrag;
-    auto rowaddr = [&](int t) { return (row0 + (int64_t)min(t, nt - 1) * p.H) * D; };
+    auto rowaddr = [&](int t) { return ck.o0 + (int64_t)min(t, nt - 1) * geo.os(); };
 
     // ---- phase 0: gates, dU'.U, cleared sums
     if (w == 0) {
-        const Gate g = chunk_gate(p, row0, nt, l);
+        const Gate g = chunk_gate(p, ck, geo.gs(), l);
         sh.ghi[l] = g.hi;
         sh.glo[l] = g.lo;
         sh.gphi[l] = g.phi;
@@ -957,13 +1035,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_bgrad(BwdProblem a, CbWs ws) {
     for (int job = w; job < 20; job += 4) {
         const int kind = job / 10, tb = blk_m(job % 10), jb = blk_n(job % 10);
         const int ta = 16 * tb + c16, ja = 16 * jb + c16;  // A-operand row, B-operand row
-        const float* Ar = kind == 0 ? a.dout + rowaddr(ta) : dDl + ta * D;
+        const int64_t oa = rowaddr(ta);
         const float* Br = (kind == 0 ? Dl : U) + ja * D;
         const float ok = (kind == 0 && ta >= nt) ? 0.f : 1.f;
         f32x4 av[NB], bv[NB];
 #pragma unroll
         for (int vb = 0; vb < NB; ++vb) {
-            av[vb] = ld4f(Ar + 16 * vb + 4 * g4);
+            av[vb] = kind == 0 ? ld4in<OT>(a.dout, oa + 16 * vb + 4 * g4) : ld4f(dDl + ta * D + 16 * vb + 4 * g4);
             bv[vb] = ld4f(Br + 16 * vb + 4 * g4);
         }
         const f32x4 pv = kind == 0 ? ld4f(PTg + ja * C + 16 * tb + 4 * g4) : zero4();  // P[t][j], r = 0..3
@@ -1061,7 +1139,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_bgrad(BwdProblem a, CbWs ws) {
         }
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-            x.ao[tb] = ld4f(a.dout + rowaddr(16 * tb + c16) + 16 * vb + 4 * g4);
+            x.ao[tb] = ld4in<OT>(a.dout, rowaddr(16 * tb + c16) + 16 * vb + 4 * g4);
             x.au[tb] = ld4f(dUp + (16 * tb + c16) * D + 16 * vb + 4 * g4);
             x.ad[tb] = ld4f(Dl + (16 * tb + c16) * D + 16 * vb + 4 * g4);
         }
@@ -1166,7 +1244,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_bgrad(BwdProblem a, CbWs ws) {
             for (int r = 0; r < 4; ++r) {
                 const int t = 16 * tb + 4 * g4 + r;
                 if (t < nt) {
-                    const int64_t o = (row0 + (int64_t)t * p.H) * D + key_col<D>(db, c16);
+                    const int64_t o = ck.o0 + (int64_t)t * geo.os() + key_col<D>(db, c16);
                     a.dq[o] = q[r];
                     a.dk[o] = kk[r];
                 }
@@ -1216,32 +1294,108 @@ __global__ __launch_bounds__(kThreads, 2) void k_bgrad(BwdProblem a, CbWs ws) {
         acc += __shfl_xor(acc, 1, 64);
         acc += __shfl_xor(acc, 2, 64);
         if (part == 0 && s < nt) {
-            const int64_t o = row0 + (int64_t)s * p.H;
+            const int64_t o = ck.g0 + (int64_t)s * geo.gs();
             a.dalpha[o] = acc / sh.galpha[s];
             a.dbeta[o] = sh.db1[s] + sh.db2[0][s] + sh.db2[1][s] + sh.db2[2][s] + sh.db2[3][s];
         }
     }
 }
 
-template <int D, int DT>
-hipError_t launch_chunked(const BwdProblem& a, const CbWs& ws, hipStream_t st) {
-    const int64_t nch = a.nbh * a.p.NC;
+// nch chunk workgroups; a.nbh (sequence, head) pairs
+template <int D, int DT, int OT, class Geo>
+hipError_t launch_chunked(const BwdProblem& a, const CbWs& ws, const Geo& geo, int64_t nch, hipStream_t st) {
     prof_begin(a.p.timer, "k_bprep", st);
-    hipLaunchKernelGGL((k_bprep<D, DT>), dim3((unsigned)nch), dim3(kThreads), 0, st, a, ws);
+    hipLaunchKernelGGL((k_bprep<D, DT, OT, Geo>), dim3((unsigned)nch), dim3(kThreads), 0, st, a, ws, geo);
     prof_end(a.p.timer, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     prof_begin(a.p.timer, "k_bchain", st);
     if (chain_slices(a.nbh, D) == 2)
-        hipLaunchKernelGGL((k_bchain<D, DT, 2>), dim3((unsigned)(a.nbh * (D / 16))), dim3(kThreads), 0, st, a, ws);
+        hipLaunchKernelGGL((k_bchain<D, DT, 2, Geo>), dim3((unsigned)(a.nbh * (D / 16))), dim3(kThreads), 0, st, a, ws, geo);
     else
-        hipLaunchKernelGGL((k_bchain<D, DT, 1>), dim3((unsigned)(2 * a.nbh * (D / 16))), dim3(kThreads), 0, st, a, ws);
+        hipLaunchKernelGGL((k_bchain<D, DT, 1, Geo>), dim3((unsigned)(2 * a.nbh * (D / 16))), dim3(kThreads), 0, st, a, ws, geo);
     prof_end(a.p.timer, st);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     prof_begin(a.p.timer, "k_bgrad", st);
-    hipLaunchKernelGGL((k_bgrad<D, DT>), dim3((unsigned)nch), dim3(kThreads), 0, st, a, ws);
+    hipLaunchKernelGGL((k_bgrad<D, DT, OT, Geo>), dim3((unsigned)nch), dim3(kThreads), 0, st, a, ws, geo);
     prof_end(a.p.timer, st);
     return hipGetLastError();
+}
+
+// Gradients of q and k of a shared key head: those of its value heads added
+// in their order.  A workgroup per chunk place and key head; bound by memory.
+template <int D>
+__global__ __launch_bounds__(kThreads) void k_bfold(PackedGeo<D> geo, const float* sq, const float* sk, float* dq, float* dk) {
+    const int nk = geo.nh / geo.group, place = blockIdx.x / nk, hkl = blockIdx.x - place * nk;
+    const int64_t s = seq_of_place(geo.off, place, 6, threadIdx.x & 63);
+    const Span sp = span_of(geo.off, s);
+    const int64_t c = place - ((sp.begin >> 6) + s);
+    if (c < 0 || c * C >= sp.n) return;
+    const int nt = (int)min<int64_t>(C, sp.n - c * C);
+    const int64_t t0 = sp.begin + c * C;
+    const int hk = geo.h0 / geo.group + hkl;
+    for (int e = threadIdx.x; e < nt * (D / 4); e += kThreads) {
+        const int64_t t = t0 + e / (D / 4);
+        const int d = 4 * (e % (D / 4));
+        const int64_t src = (t * geo.Hv + (int64_t)hk * geo.group) * D + d, dst = (t * geo.Hk + hk) * D + d;
+        f32x4 x = ld4f(sq + src), y = ld4f(sk + src);
+        for (int g = 1; g < geo.group; ++g) {
+            x += ld4f(sq + src + g * D);
+            y += ld4f(sk + src + g * D);
+        }
+        st4f(dq + dst, x);
+        st4f(dk + dst, y);
+    }
+}
+
+// Gradients of tokens outside every sequence (in front of the first, behind
+// the last): zero.  blockIdx.y: which array.
+struct ClearArgs {
+    float* x[5];
+    int64_t row[5];  // floats of a token
+};
+__global__ __launch_bounds__(kThreads) void k_bclear(Offsets off, ClearArgs c) {
+    const int64_t row = c.row[blockIdx.y], front = cu_at(off, 0), back = max(cu_at(off, off.S), front);
+    float* x = c.x[blockIdx.y];
+    const int64_t n = (front + off.N - back) * row, gap = (back - front) * row;
+    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n; e += (int64_t)gridDim.x * kThreads)
+        x[e < front * row ? e : e + gap] = 0.f;
+}
+
+template <int D>
+hipError_t launch_packed(const PackedBwd& b, BwdProblem a, const CbWs& ws, float* part_q, float* part_k, int64_t heads,
+                         hipStream_t st) {
+    const Packed& p = b.p;
+    PackedGeo<D> geo{};
+    geo.off = {p.cu, p.N, p.S};
+    geo.Hk = (int)p.Hk;
+    geo.Hv = (int)p.Hv;
+    geo.group = (int)(p.Hv / p.Hk);
+    geo.q_stride = p.q_stride;
+    geo.k_stride = p.k_stride;
+    geo.v_stride = p.v_stride;
+    geo.n_in = p.n_in;
+    geo.slots = p.slots_in;
+    const int64_t places = p.N / C + p.S;
+    a.dq = geo.group > 1 ? part_q : b.dq;
+    a.dk = geo.group > 1 ? part_k : b.dk;
+    for (int64_t h0 = 0; h0 < p.Hv; h0 += heads) {
+        geo.h0 = (int)h0;
+        geo.nh = (int)std::min<int64_t>(heads, p.Hv - h0);
+        a.nbh = p.S * geo.nh;
+        const hipError_t e = p.dtype == GDN_BF16
+                                 ? launch_chunked<D, GDN_BF16, GDN_BF16>(a, ws, geo, places * geo.nh, st)
+                                 : launch_chunked<D, GDN_F32, GDN_F32>(a, ws, geo, places * geo.nh, st);
+        if (e != hipSuccess) return e;
+        if (geo.group > 1) {
+            prof_begin(p.timer, "k_bfold", st);
+            hipLaunchKernelGGL(k_bfold<D>, dim3((unsigned)(places * (geo.nh / geo.group))), dim3(kThreads), 0, st, geo, part_q,
+                               part_k, b.dq, b.dk);
+            prof_end(p.timer, st);
+            if (hipGetLastError() != hipSuccess) return hipErrorUnknown;
+        }
+    }
+    return hipSuccess;
 }
 
 }  // namespace
@@ -1250,14 +1404,41 @@ bool chunked_backward_supported(int64_t dk, int64_t dv, int gate) {
     return gate == GDN_GATE_SCALAR && dk == dv && (dk == 64 || dk == 128);
 }
 
-// Workspace bytes per (batch, head) of the chunked backward; larger batches
-// run in groups of heads so that the workspace stays within the cap.
-static size_t chunked_bytes_per_head(int64_t T, int64_t D) {
-    const size_t nc = (size_t)((T + C - 1) / C);
+// Workspace bytes of one chunk of one head, and of a (batch, head)'s chunks;
+// larger batches run in groups of heads so that the workspace stays within
+// the cap.
+static size_t chunk_bytes(int64_t D) {
     const size_t nb = (size_t)(D / 16);
-    const size_t per_chunk = sizeof(float) * (4 * (size_t)C * C + 2 * nb * 4 * 64 * 4 + 2 * nb * nb * 64 * 4 +
-                                              5 * (size_t)C * D + (size_t)D * D + 8 * (size_t)C);
-    return nc * per_chunk;
+    return sizeof(float) * (4 * (size_t)C * C + 2 * nb * 4 * 64 * 4 + 2 * nb * nb * 64 * 4 + 5 * (size_t)C * D +
+                            (size_t)D * D + 8 * (size_t)C);
+}
+static size_t chunked_bytes_per_head(int64_t T, int64_t D) { return (size_t)((T + C - 1) / C) * chunk_bytes(D); }
+// the pieces of nch chunks' records, each 256-byte aligned
+static CbWs carve(char* base, size_t nch, int64_t D) {
+    const size_t nb = (size_t)(D / 16);
+    size_t off = 0;
+    auto take = [&](size_t floats) {
+        float* q = reinterpret_cast<float*>(base + off);
+        off += align256(floats * sizeof(float));
+        return q;
+    };
+    CbWs ws;
+    ws.T = take(nch * C * C);
+    ws.TT = take(nch * C * C);
+    ws.PT = take(nch * C * C);
+    ws.AtT = take(nch * C * C);
+    ws.KTf = take(nch * nb * 4 * 64 * 4);  // (sized for fp32 inputs)
+    ws.QTf = take(nch * nb * 4 * 64 * 4);
+    ws.Sf = take(nch * nb * nb * 64 * 4);
+    ws.dSf = take(nch * nb * nb * 64 * 4);
+    ws.U = take(nch * C * D);
+    ws.Dl = take(nch * C * D);
+    ws.dDl = take(nch * C * D);
+    ws.dUp = take(nch * C * D);
+    ws.Ef = take(nch * C * D);
+    ws.Hf = take(nch * D * D);
+    ws.Gr = take(nch * 8 * C);
+    return ws;
 }
 constexpr size_t kChunkedWsCap = size_t(8) << 30;
 static int64_t chunked_heads_per_launch(int64_t B, int64_t T, int64_t H, int64_t D) {
@@ -1281,49 +1462,86 @@ hipError_t backward_chunked(const BwdProblem& a_in, void* workspace, hipStream_t
         // dS_0 = dS_T: the chain kernel with no chunks (its whole grid, both
         // directions, as the block order assumes; the forward half does nothing)
         BwdProblem g = a0;
-        g.bh0 = 0;
         g.nbh = BH;
         CbWs ws{};
-        hipLaunchKernelGGL((D == 64 ? k_bchain<64, GDN_BF16, 1> : k_bchain<128, GDN_BF16, 1>),
-                           dim3((unsigned)(2 * BH * (D / 16))), dim3(kThreads), 0, st, g, ws);
+        const dim3 grid((unsigned)(2 * BH * (D / 16))), block(kThreads);
+        if (D == 64)
+            hipLaunchKernelGGL((k_bchain<64, GDN_BF16, 1, DenseGeo<64>>), grid, block, 0, st, g, ws,
+                               DenseGeo<64>{p.T, p.H, p.NC, 0});
+        else
+            hipLaunchKernelGGL((k_bchain<128, GDN_BF16, 1, DenseGeo<128>>), grid, block, 0, st, g, ws,
+                               DenseGeo<128>{p.T, p.H, p.NC, 0});
         return hipGetLastError();
     }
     const int64_t gsz = chunked_heads_per_launch(p.B, p.T, p.H, D);
-    const size_t nch = (size_t)gsz * (size_t)p.NC;
-    const size_t nb = (size_t)(D / 16);
-    char* base = static_cast<char*>(workspace);
-    size_t off = 0;
-    auto take = [&](size_t floats) {
-        float* q = reinterpret_cast<float*>(base + off);
-        off += align256(floats * sizeof(float));
-        return q;
-    };
-    CbWs ws;
-    ws.T = take(nch * C * C);
-    ws.TT = take(nch * C * C);
-    ws.PT = take(nch * C * C);
-    ws.AtT = take(nch * C * C);
-    ws.KTf = take(nch * nb * 4 * 64 * 4);  // (sized for fp32 inputs)
-    ws.QTf = take(nch * nb * 4 * 64 * 4);
-    ws.Sf = take(nch * nb * nb * 64 * 4);
-    ws.dSf = take(nch * nb * nb * 64 * 4);
-    ws.U = take(nch * C * D);
-    ws.Dl = take(nch * C * D);
-    ws.dDl = take(nch * C * D);
-    ws.dUp = take(nch * C * D);
-    ws.Ef = take(nch * C * D);
-    ws.Hf = take(nch * D * D);
-    ws.Gr = take(nch * 8 * C);
+    const CbWs ws = carve(static_cast<char*>(workspace), (size_t)gsz * (size_t)p.NC, D);
     for (int64_t bh0 = 0; bh0 < BH; bh0 += gsz) {
         BwdProblem g = a0;
-        g.bh0 = bh0;
         g.nbh = std::min<int64_t>(gsz, BH - bh0);
+        const int64_t nch = g.nbh * p.NC;
         hipError_t e;
-        if (D == 64) e = p.dtype == GDN_BF16 ? launch_chunked<64, GDN_BF16>(g, ws, st) : launch_chunked<64, GDN_F32>(g, ws, st);
-        else e = p.dtype == GDN_BF16 ? launch_chunked<128, GDN_BF16>(g, ws, st) : launch_chunked<128, GDN_F32>(g, ws, st);
+        if (D == 64) {
+            const DenseGeo<64> geo{p.T, p.H, p.NC, bh0};
+            e = p.dtype == GDN_BF16 ? launch_chunked<64, GDN_BF16, GDN_F32>(g, ws, geo, nch, st)
+                                    : launch_chunked<64, GDN_F32, GDN_F32>(g, ws, geo, nch, st);
+        } else {
+            const DenseGeo<128> geo{p.T, p.H, p.NC, bh0};
+            e = p.dtype == GDN_BF16 ? launch_chunked<128, GDN_BF16, GDN_F32>(g, ws, geo, nch, st)
+                                    : launch_chunked<128, GDN_F32, GDN_F32>(g, ws, geo, nch, st);
+        }
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+// Packed sequences.  Value heads of one launch: whole key heads' groups, as
+// many as the cap holds; behind the records, with shared key heads, the
+// gradients of q and k per value head.
+static int64_t packed_heads_per_launch(const Packed& p) {
+    const int64_t group = p.Hv / p.Hk;
+    const size_t per = (size_t)(p.N / C + p.S) * chunk_bytes(p.dk) * (size_t)group;
+    return group * std::max<int64_t>(1, std::min<int64_t>(p.Hk, (int64_t)(kChunkedWsCap / per)));
+}
+static size_t packed_records(const Packed& p) {
+    return (size_t)(p.N / C + p.S) * (size_t)packed_heads_per_launch(p) * chunk_bytes(p.dk) + 15 * 256;
+}
+static size_t packed_part(const Packed& p) {
+    return p.Hv > p.Hk ? align256((size_t)p.N * (size_t)(p.Hv * p.dk) * sizeof(float)) : 0;
+}
+
+size_t packed_backward_workspace(const Packed& p) {
+    if (p.S * p.Hv == 0 || p.N == 0) return 0;
+    return align256(packed_records(p)) + 2 * packed_part(p);
+}
+
+hipError_t packed_backward(const PackedBwd& b, void* workspace, hipStream_t st) {
+    const Packed& p = b.p;
+    BwdProblem a{};
+    a.p.dk = p.dk; a.p.dv = p.dv;
+    a.p.dtype = p.dtype; a.p.gate = p.gate; a.p.order = p.order;
+    a.p.scale = p.scale;
+    a.p.q = p.q; a.p.k = p.k; a.p.v = p.v; a.p.alpha = p.alpha; a.p.beta = p.beta; a.p.s0 = p.s_in;
+    a.p.timer = p.timer;
+    a.dout = b.dout;
+    a.ds_out = b.ds_out;
+    a.dv = b.dv; a.dalpha = b.dalpha; a.dbeta = b.dbeta;
+    a.ds0 = b.ds0;
+    const Offsets off{p.cu, p.N, p.S};
+    if (p.N > 0) {
+        const ClearArgs c{{b.dq, b.dk, b.dv, b.dalpha, b.dbeta}, {p.Hk * p.dk, p.Hk * p.dk, p.Hv * p.dv, p.Hv, p.Hv}};
+        prof_begin(p.timer, "k_bclear", st);
+        hipLaunchKernelGGL(k_bclear, dim3(64, 5), dim3(kThreads), 0, st, off, c);
+        prof_end(p.timer, st);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    char* base = static_cast<char*>(workspace);
+    const int64_t heads = p.N > 0 ? packed_heads_per_launch(p) : p.Hv;
+    const CbWs ws = p.N > 0 ? carve(base, (size_t)(p.N / C + p.S) * (size_t)heads, p.dk) : CbWs{};
+    float* part_q = p.N > 0 ? reinterpret_cast<float*>(base + align256(packed_records(p))) : nullptr;
+    float* part_k = p.N > 0 ? part_q + packed_part(p) / sizeof(float) : nullptr;
+    return p.dk == 64 ? launch_packed<64>(b, a, ws, part_q, part_k, heads, st)
+                      : launch_packed<128>(b, a, ws, part_q, part_k, heads, st);
 }
 
 }  // namespace gdn

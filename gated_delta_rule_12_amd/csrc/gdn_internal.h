@@ -96,7 +96,7 @@ hipError_t mfma_correct(const Problem& p, const Split& sp, char* ws, const WsLay
 // gradients, the gradient outputs and the checkpoint workspace.
 struct BwdProblem {
     Problem p;
-    const float* dout;    // [B, T, H, dv]
+    const void* dout;     // [B, T, H, dv], fp32 (packed sequences: the inputs' type)
     const float* ds_out;  // [B, H, dv, dk] or null (zero)
     float* dq;            // [B, T, H, dk]
     float* dk;            // [B, T, H, dk]
@@ -106,7 +106,7 @@ struct BwdProblem {
     float* ds0;           // [B, H, dv, dk] or null
     float* ckpt;          // workspace: states at every 16-token run start
     float* part;          // workspace: per (row block, token) partial sums
-    int64_t bh0, nbh;     // the (batch, head) pairs of one launch
+    int64_t bh0, nbh;     // the (batch, head) pairs of one launch (chunked: nbh, the rest in its geometry)
 };
 size_t backward_ckpt_bytes(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, int gate);
 size_t backward_workspace(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv, int gate);
@@ -156,6 +156,21 @@ struct Packed {
 bool packed_chunked(const Packed& p);
 size_t packed_workspace(const Packed& p);
 hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st);
+
+// Its gradients (gdn_bwd_chunk.hip): scalar gate, dk = dv in {64, 128}.
+struct PackedBwd {
+    Packed p;
+    const void* dout;     // [N, Hv, dv], dtype
+    const float* ds_out;  // [S, Hv, dv, dk] or null (zero)
+    float* dq;            // [N, Hk, dk]
+    float* dk;            // [N, Hk, dk]
+    float* dv;            // [N, Hv, dv]
+    float* dalpha;        // [N, Hv]
+    float* dbeta;         // [N, Hv]
+    float* ds0;           // [S, Hv, dv, dk] or null
+};
+size_t packed_backward_workspace(const Packed& p);
+hipError_t packed_backward(const PackedBwd& b, void* ws, hipStream_t st);
 
 // Layer norm (gdn_norm.hip).
 struct LayerNorm {

@@ -26,14 +26,11 @@
 //     start states (k_pk_chain: S_start(g + 1) = S_end(g) + S_start(g) M(g),
 //     the sequence-parallel notes' increment and correction) and the output
 //     pass from the true start states.
-// Lengths are known on the device only.  Chunks and segments of sequence s
-// get consecutive places from cu[s] / 64 + s on (segments: of their length in
-// tokens): ceil(n / 64) places never reach the next sequence's first, and
-// N / 64 + S places are enough, so no kernel has to lay out a table.  cu is
-// clamped to 0 .. N and to rising order, slots outside the pool read as zero
-// states and are not written, so no content of either leads out of bounds.
+// Chunks and segments have their places by rule (gdn_packed_common.h).  Slots
+// outside the pool read as zero states and are not written.
 #include "gdn_internal.h"
 #include "gdn_mfma_common.h"
+#include "gdn_packed_common.h"
 #include "../../include/gdn.h"
 
 namespace gdn {
@@ -44,6 +41,7 @@ constexpr int kChunkMin = 64;
 
 struct Pk {
     Packed p;
+    Offsets at;
     int Hv, group;   // value heads; value heads per key head
     int rec_below;   // k_pk_rec takes sequences of fewer tokens
     int seg_shift;   // a segment holds 2^seg_shift tokens
@@ -56,38 +54,6 @@ struct Pk {
     float* s_start;  // [place, head][D][D]: start states of the output pass
 };
 
-__device__ __forceinline__ int64_t cu_at(const Packed& p, int64_t s) {
-    const int64_t x = p.cu[s];
-    return x < 0 ? 0 : x > p.N ? p.N : x;
-}
-struct Span {
-    int64_t begin;
-    int64_t n;
-};
-__device__ __forceinline__ Span span_of(const Packed& p, int64_t s) {
-    const int64_t a = cu_at(p, s), b = cu_at(p, s + 1);
-    return {a, b > a ? b - a : 0};
-}
-// The sequence whose places hold `place` (2^shift tokens a place), found by
-// a whole wave: 64 candidates a round.
-__device__ __forceinline__ int64_t seq_of_place(const Packed& p, int64_t place, int shift, int lane) {
-    int64_t lo = 0, cnt = p.S;
-    while (cnt > 1) {
-        const int64_t step = (cnt + 63) >> 6;
-        bool le = false;
-        if (lane * step < cnt) {
-            const int64_t s = lo + lane * step;
-            le = (cu_at(p, s) >> shift) + s <= place;
-        }
-        // (the count is unsigned: none of them has to give 0 too, as in front
-        // of the first sequence)
-        const int hits = (int)__popcll(__ballot(le));
-        const int64_t k = hits > 0 ? hits - 1 : 0;
-        lo += k * step;
-        cnt = min(step, cnt - k * step);
-    }
-    return lo;
-}
 __device__ __forceinline__ const float* state_from(const Packed& p, int64_t s, int64_t h) {
     const int64_t slot = p.slots_in ? (int64_t)p.slots_in[s] : s;
     if (!p.s_in || slot < 0 || slot >= p.n_in) return nullptr;
@@ -150,7 +116,7 @@ __global__ __launch_bounds__(kRecThreads) void k_pk_rec(Pk a) {
     const int nrb = (dv + RB - 1) / RB;
     const int sh_id = blockIdx.x / nrb, rb = blockIdx.x - sh_id * nrb;
     const int s = sh_id / a.Hv, h = sh_id - s * a.Hv, hk = h / a.group;
-    const Span sp = span_of(p, s);
+    const Span sp = span_of(a.at, s);
     if (sp.n >= a.rec_below) return;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, c = l % LPR;
     const bool dtp = p.order == GDN_DECAY_THEN_PREDICT;
@@ -388,8 +354,8 @@ __global__ __launch_bounds__(kThreads) void k_pk_prep(Pk a) {
     const Packed& p = a.p;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g4 = l >> 4, c16 = l & 15;
     const int place = blockIdx.x / a.Hv, h = blockIdx.x - place * a.Hv, hk = h / a.group;
-    const int64_t s = seq_of_place(p, place, 6, l);
-    const Span sp = span_of(p, s);
+    const int64_t s = seq_of_place(a.at, place, 6, l);
+    const Span sp = span_of(a.at, s);
     const int64_t c = place - ((sp.begin >> 6) + s);
     if (sp.n < kChunkMin || c < 0 || c * C >= sp.n) return;
     const int64_t t0 = sp.begin + c * C;
@@ -512,8 +478,8 @@ __global__ __launch_bounds__(seg_threads<D>(), D == 128 ? 2 : 2) void k_pk_seg(P
     const Packed& p = a.p;
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g4 = l >> 4, c16 = l & 15;
     const int place = blockIdx.x / a.Hv, h = blockIdx.x - place * a.Hv, hk = h / a.group;
-    const int64_t s = seq_of_place(p, place, a.seg_shift, l);
-    const Span sp = span_of(p, s);
+    const int64_t s = seq_of_place(a.at, place, a.seg_shift, l);
+    const Span sp = span_of(a.at, s);
     const int64_t base = (sp.begin >> a.seg_shift) + s;  // the sequence's first place
     const int64_t gi = place - base, ng = (sp.n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
     if (sp.n < kChunkMin || gi < 0 || gi >= ng || (!OUT && gi == ng - 1)) return;
@@ -811,7 +777,7 @@ __global__ __launch_bounds__(4 * D) void k_pk_chain(Pk a) {
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g4 = l >> 4, c16 = l & 15;
     const int rt = blockIdx.x % NB;
     const int sh_id = blockIdx.x / NB, s = sh_id / a.Hv, h = sh_id - s * a.Hv;
-    const Span sp = span_of(p, s);
+    const Span sp = span_of(a.at, s);
     const int64_t ng = (sp.n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
     if (sp.n < kChunkMin || ng < 2) return;
     const int64_t base = (sp.begin >> a.seg_shift) + s;
@@ -931,6 +897,7 @@ size_t packed_workspace(const Packed& p) { return layout(p).total; }
 hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st) {
     Pk a{};
     a.p = p;
+    a.at = {p.cu, p.N, p.S};
     a.Hv = (int)p.Hv;
     a.group = (int)(p.Hv / p.Hk);
     const PkLayout L = layout(p);

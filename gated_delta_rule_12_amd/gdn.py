@@ -37,6 +37,7 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_recurrent_ref", "gdn_seqpar_fwd", "gdn_decode_s
            "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_raw", "gdn_chunk_fwd_raw_timed",
            "gdn_raw_workspace_bytes", "gdn_backward_path",
            "gdn_packed_fwd", "gdn_packed_fwd_timed", "gdn_packed_workspace_bytes", "gdn_packed_path",
+           "gdn_packed_backward", "gdn_packed_backward_timed", "gdn_packed_backward_workspace_bytes",
            "gdn_layer_norm_fwd", "gdn_layer_norm_fwd_timed", "gdn_layer_norm_backward",
            "gdn_layer_norm_backward_timed", "gdn_layer_norm_workspace_bytes")
 
@@ -111,6 +112,10 @@ def lib():
     L.gdn_packed_workspace_bytes.restype = sz
     L.gdn_packed_path.argtypes = [i64, i64, i32, i32]
     L.gdn_packed_path.restype = ctypes.c_int
+    L.gdn_packed_backward.argtypes = ([i64] * 7 + [i32, i32, i32, f32] + [vp, i64] * 3 + [vp] * 13 + [vp, sz, vp])
+    L.gdn_packed_backward.restype = ctypes.c_int
+    L.gdn_packed_backward_workspace_bytes.argtypes = [i64] * 6 + [i32, i32]
+    L.gdn_packed_backward_workspace_bytes.restype = sz
     L.gdn_layer_norm_fwd.argtypes = [i64, i64, i32, i32, f32] + [vp] * 7
     L.gdn_layer_norm_fwd.restype = ctypes.c_int
     L.gdn_layer_norm_backward.argtypes = [i64, i64, i32, i32] + [vp] * 9 + [sz, vp]
@@ -119,7 +124,7 @@ def lib():
     L.gdn_layer_norm_workspace_bytes.restype = sz
     # the *_timed variants: the same arguments plus the timer
     for name in ("gdn_chunk_fwd", "gdn_chunk_fwd_raw", "gdn_seqpar_fwd", "gdn_decode_step",
-                 "gdn_backward", "gdn_packed_fwd", "gdn_layer_norm_fwd", "gdn_layer_norm_backward"):
+                 "gdn_backward", "gdn_packed_fwd", "gdn_packed_backward", "gdn_layer_norm_fwd", "gdn_layer_norm_backward"):
         f = getattr(L, name + "_timed")
         f.argtypes = getattr(L, name).argtypes + [vp]
         f.restype = ctypes.c_int
@@ -187,6 +192,10 @@ def gdn_packed_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, dtype, gate) -> in
 
 def gdn_packed_path(dk, dv, dtype, gate) -> int:
     return int(lib().gdn_packed_path(dk, dv, dtype, gate))
+
+
+def gdn_packed_backward_workspace_bytes(N, S, Hk, Hv, dk, dv, dtype, gate) -> int:
+    return int(lib().gdn_packed_backward_workspace_bytes(N, S, Hk, Hv, dk, dv, dtype, gate))
 
 
 def gdn_layer_norm_workspace_bytes(rows, n) -> int:
@@ -585,11 +594,11 @@ def packed_fwd(q, k, v, alpha, beta, cu_seqlens, state_in=None, slots_in=None, s
     order.  max_len: a bound on the lengths (it picks kernels; None: N).
     Returns (out [N,Hv,dv] of q's dtype, state_out)."""
     import torch
+    if state_out is None and slots_out is not None:
+        raise ValueError("slots_out needs state_out")
     N, S, Hk, Hv, dk, dv, gate = _packed_check(q, k, v, alpha, beta, cu_seqlens,
                                                (state_in, state_out), (slots_in, slots_out))
     if state_out is None:
-        if slots_out is not None:
-            raise ValueError("slots_out needs state_out")
         state_out = torch.empty((S, Hv, dv, dk), dtype=torch.float32, device=q.device)
     if out is None:
         out = torch.empty((N, Hv, dv), dtype=q.dtype, device=q.device)
@@ -610,6 +619,39 @@ def packed_fwd(q, k, v, alpha, beta, cu_seqlens, state_in=None, slots_in=None, s
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_packed_fwd")
     return out, state_out
+
+
+def packed_backward(q, k, v, alpha, beta, cu_seqlens, state_in, slots_in, grad_out, grad_state_out=None, *,
+                    order=GDN_PREDICT_THEN_DECAY, scale=1.0, want_grad_state0=True, workspace=None, timer=None):
+    """Gradients through packed_fwd: gdn_packed_backward (scalar gate, dk = dv in
+    {64, 128}).  grad_out [N,Hv,dv] of q's dtype = dL/d out; grad_state_out
+    [S,Hv,dv,dk] fp32 = dL/d of the end states, in the sequences' order, or
+    None (zero).  Returns (dq, dk, dv, dalpha, dbeta, dstate0), fp32, shaped
+    like q, k, v, alpha, beta and the sequences' states [S,Hv,dv,dk] (None when
+    not wanted); rows outside every sequence are zero."""
+    import torch
+    N, S, Hk, Hv, dk, dv, gate = _packed_check(q, k, v, alpha, beta, cu_seqlens, (state_in,), (slots_in,))
+    dev, f32 = q.device, torch.float32
+    if grad_out.shape != (N, Hv, dv) or grad_out.dtype != q.dtype or grad_out.device != dev or not grad_out.is_contiguous():
+        raise ValueError("grad_out must be a contiguous [N,Hv,dv] of q's dtype")
+    if grad_state_out is not None and (grad_state_out.shape != (S, Hv, dv, dk) or grad_state_out.dtype != f32 or
+                                       grad_state_out.device != dev or not grad_state_out.is_contiguous()):
+        raise ValueError("grad_state_out must be a contiguous float32 [S,Hv,dv,dk]")
+    grads = [torch.empty(t.shape, dtype=f32, device=dev) for t in (q, k, v, alpha, beta)]
+    ds0 = torch.empty((S, Hv, dv, dk), dtype=f32, device=dev) if want_grad_state0 else None
+    code = _dtype_code(q)
+    if workspace is None:
+        n = lib().gdn_packed_backward_workspace_bytes(N, S, Hk, Hv, dk, dv, code, gate)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    sq, sk, sv = _token_strides(q, k, v)
+    args = (N, S, Hk, Hv, dk, dv, 0 if state_in is None else state_in.shape[0], code, gate, order, scale,
+            _addr(q), sq, _addr(k), sk, _addr(v), sv, _addr(alpha), _addr(beta), _addr(cu_seqlens),
+            _addr(state_in), _addr(slots_in), _addr(grad_out), _addr(grad_state_out), *map(_addr, grads), _addr(ds0),
+            _addr(workspace), 0 if workspace is None else workspace.numel())
+    rc = _on_device(dev, lambda *a: _call("gdn_packed_backward", a, timer), args)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_packed_backward")
+    return (*grads, ds0)
 
 
 # ---- layer norm -------------------------------------------------------------------

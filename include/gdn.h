@@ -361,6 +361,42 @@ size_t gdn_packed_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, 
 int gdn_packed_path(int64_t dk, int64_t dv, int32_t dtype, int32_t gate);
 
 /*
+ * gdn_packed_backward — gradients of a loss through gdn_packed_fwd, for the
+ * shapes of the chunked gdn_backward (scalar gate, dk = dv in {64, 128};
+ * others return GDN_E_UNSUPPORTED), bf16 or fp32, any lengths: that call's
+ * chunk-form chain rule in fp32, its sums in a fixed order.  Inputs as for
+ * gdn_packed_fwd, alpha > 0.
+ *   grad_out        [N, Hv, dv], dtype: dL/d out
+ *   grad_state_out  [S, Hv, dv, dk] fp32 in the sequences' order: dL/d of
+ *                   their end states; NULL: zero
+ *   grad_q, grad_k  [N, Hk, dk] fp32, summed over the value heads of a key
+ *                   head;  grad_v [N, Hv, dv], grad_alpha, grad_beta [N, Hv]
+ *                   fp32; rows outside every sequence are set to zero
+ *   grad_state0     [S, Hv, dv, dk] fp32: dL/d of each sequence's start state
+ *                   (sequences that share a slot each have their own); NULL:
+ *                   not wanted
+ *   workspace       gdn_packed_backward_workspace_bytes(...): per value head
+ *                   and chunk as gdn_backward, capped at about 8 GiB (more
+ *                   heads run in groups), and with shared key heads twice
+ *                   4 N Hv dk
+ * Alignment: as gdn_packed_fwd; the gradients on 16 bytes, grad_alpha and
+ * grad_beta on 4.
+ */
+int gdn_packed_backward(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                        int64_t n_in, int32_t dtype, int32_t gate, int32_t order, float scale,
+                        const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const float* alpha, const float* beta,
+                        const int32_t* cu_seqlens, const float* state_in, const int32_t* slots_in,
+                        const void* grad_out, const float* grad_state_out, float* grad_q,
+                        float* grad_k, float* grad_v, float* grad_alpha, float* grad_beta,
+                        float* grad_state0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gdn_packed_backward needs (0: none, or the arguments do not
+ * validate or are not supported).  Host only. */
+size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk,
+                                           int64_t dv, int32_t dtype, int32_t gate);
+
+/*
  * gdn_layer_norm_fwd — layer norm of rows of n elements, as the DeltaNet
  * block normalises the heads' outputs (rows of dv) and its input (rows of
  * model width): y = (x - mean) rstd weight + bias, rstd = 1 / sqrt(var + eps),
@@ -501,6 +537,16 @@ int gdn_packed_fwd_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t d
                          const float* state_in, const int32_t* slots_in, float* state_out,
                          const int32_t* slots_out, void* out, void* workspace,
                          size_t workspace_bytes, void* stream, gdn_timer* timer);
+int gdn_packed_backward_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                              int64_t n_in, int32_t dtype, int32_t gate, int32_t order, float scale,
+                              const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const float* alpha,
+                              const float* beta, const int32_t* cu_seqlens, const float* state_in,
+                              const int32_t* slots_in, const void* grad_out,
+                              const float* grad_state_out, float* grad_q, float* grad_k,
+                              float* grad_v, float* grad_alpha, float* grad_beta,
+                              float* grad_state0, void* workspace, size_t workspace_bytes,
+                              void* stream, gdn_timer* timer);
 int gdn_layer_norm_fwd_timed(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps,
                              const void* x, const float* weight, const float* bias, void* y,
                              float* mean, float* rstd, void* stream, gdn_timer* timer);

@@ -126,3 +126,30 @@ def test_binding_refuses_before_the_library():
         gdn.layer_norm_fwd(z(4, 64))
     with pytest.raises(ValueError):
         gdn.layer_norm_backward(z(4, 64), z(4, 64), None, z(4), z(4))
+
+
+def bwd(N=100, S=2, Hk=2, Hv=4, dk=64, dv=64, n_in=2, dtype=1, gate=0, order=0, q=F, k=F, v=F, sq=128, sk=128, sv=256, alpha=F,
+        beta=F, cu=F, s_in=F, slots_in=NUL, g=F, gs=F, dq=F, dkk=F, dvv=F, da=F, db=F, ds=F, ws=F, wsb=1 << 40):
+    return gdn.lib().gdn_packed_backward(N, S, Hk, Hv, dk, dv, n_in, dtype, gate, order, 1.0, q, sq, k, sk, v, sv, alpha, beta,
+                                         cu, s_in, slots_in, g, gs, dq, dkk, dvv, da, db, ds, ws, wsb, NUL)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dtype=2), ARG), (dict(gate=2), ARG), (dict(order=2), ARG), (dict(N=-1), SHAPE), (dict(Hk=3), SHAPE),
+    (dict(gate=1), UNSUP), (dict(dk=128), UNSUP), (dict(dk=32, dv=32), UNSUP), (dict(dk=60), UNSUP),
+    (dict(sq=100), SHAPE), (dict(sq=129), ARG), (dict(n_in=1), SHAPE),
+    (dict(q=NUL), ARG), (dict(cu=NUL), ARG), (dict(g=NUL), ARG), (dict(dq=NUL), ARG), (dict(dkk=NUL), ARG), (dict(dvv=NUL), ARG),
+    (dict(da=NUL), ARG), (dict(db=NUL), ARG), (dict(g=ODD), ARG), (dict(dq=ctypes.c_void_p(0x10004)), ARG), (dict(da=ODD), ARG),
+    (dict(ds=ctypes.c_void_p(0x10008)), ARG), (dict(gs=ODD), ARG), (dict(ws=NUL), WS), (dict(wsb=1000), WS), (dict(ws=ODD), ARG),
+    (dict(S=0), OK),
+])
+def test_packed_backward_refusals(kw, want):
+    assert bwd(**kw) == want
+
+
+def test_packed_backward_workspace():
+    ws = gdn.gdn_packed_backward_workspace_bytes
+    assert ws(100, 2, 2, 4, 32, 32, 1, 0) == 0 and ws(100, 2, 2, 4, 64, 64, 1, 1) == 0 and ws(0, 2, 2, 4, 64, 64, 1, 0) == 0
+    one, shared = ws(1000, 2, 4, 4, 64, 64, 1, 0), ws(1000, 2, 2, 4, 64, 64, 1, 0)
+    assert shared == one + 2 * (1000 * 4 * 64 * 4)
+    assert ws(1 << 20, 1, 64, 64, 128, 128, 1, 0) <= (8 << 30) + (1 << 20)  # heads in groups
