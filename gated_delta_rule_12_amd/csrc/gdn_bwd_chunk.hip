@@ -167,6 +167,16 @@ struct DenseGeo {
         const int64_t row0 = (x.b * T + (int64_t)c * C) * H + x.h;
         return {x.bl * NC + c, (int)min<int64_t>(C, T - (int64_t)c * C), row0, row0 * D, row0 * D, row0 * D, row0 * D};
     }
+    // workgroups go to the eight XCDs in turn; the logical order (head,
+    // direction, slice group) is laid over them so that consecutive logical
+    // indices, the `per` workgroups of a head that read the same chunk
+    // operands, share an XCD and its L2
+    __device__ void place(int64_t nbh, int per, int64_t& head, int& rem) const {
+        const int64_t N = nbh * per;
+        const int64_t lin = N % 8 == 0 ? (blockIdx.x % 8) * (N / 8) + blockIdx.x / 8 : blockIdx.x;
+        head = lin / per;
+        rem = (int)(lin - head * per);
+    }
     __device__ bool chunk(int64_t block, int, ChunkAt& x) const {
         const int64_t bl = block / NC;
         x = at(head(bl), (int)(block - bl * NC));
@@ -182,6 +192,7 @@ struct PackedGeo {
     int Hk, Hv, group, h0, nh;
     int64_t q_stride, k_stride, v_stride, n_in;
     const int32_t* slots;
+    int32_t* order;  // sequences by falling length (order_sequences)
     __device__ int64_t gs() const { return Hv; }
     __device__ int64_t qs() const { return q_stride; }
     __device__ int64_t ks() const { return k_stride; }
@@ -205,8 +216,21 @@ struct PackedGeo {
         return x;
     }
     __device__ Head head(int64_t idx) const {
-        const int64_t s = (int)idx / nh;
-        return head_of(s, (int)idx - (int)s * nh);
+        const int r = (int)idx / nh;
+        return head_of(order[r], (int)idx - r * nh);
+    }
+    // as the dense order, but the heads, longest first, dealt over the XCDs in
+    // turn
+    __device__ void place(int64_t nbh, int per, int64_t& head, int& rem) const {
+        const int g = (int)nbh / 8 * 8, b = (int)blockIdx.x;
+        if (b < g * per) {
+            const int j = b / 8;
+            head = (j / per) * 8 + b % 8;
+            rem = j % per;
+        } else {
+            head = b / per;
+            rem = b % per;
+        }
     }
     __device__ ChunkAt at(const Head& x, int c) const {
         const int64_t t = x.begin + (int64_t)c * C, h = h0 + x.hl, hk = h / group;
@@ -293,6 +317,12 @@ __global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 4 : 2) void k_bprep(BwdP
 
     const Problem& p = a.p;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g4 = l >> 4, c16 = l & 15;
+    if constexpr (std::is_same_v<Geo, PackedGeo<D>>) {
+        if (blockIdx.x == gridDim.x - 1) {  // one workgroup more: the chains' order
+            order_sequences(geo.off, geo.order, reinterpret_cast<int*>(AT), tid, kThreads);
+            return;
+        }
+    }
     ChunkAt ck;
     if (!geo.chunk(blockIdx.x, l, ck)) return;
     const int64_t ci = ck.ci;
@@ -902,14 +932,9 @@ __global__ __launch_bounds__(kThreads, NS == 1 ? 2 : 1) void k_bchain(BwdProblem
     constexpr int NSL = NB / NS;  // workgroups per head and direction
     __shared__ ChainShared<NS> sh;
     const Problem& p = a.p;
-    // workgroups go to the eight XCDs in turn; the logical order (head,
-    // direction, slice group) is laid over them so that consecutive logical
-    // indices, the 2 NSL workgroups of a head that read the same chunk
-    // operands, share an XCD and its L2
-    const int64_t N = 2 * a.nbh * NSL;
-    const int64_t lin = N % 8 == 0 ? (blockIdx.x % 8) * (N / 8) + blockIdx.x / 8 : blockIdx.x;
-    const int64_t head = lin / (2 * NSL);
-    const int rem = (int)(lin - head * 2 * NSL);
+    int64_t head;
+    int rem;
+    geo.place(a.nbh, 2 * NSL, head, rem);
     const bool rev = rem < NSL;
     ChainCtx<D, DT, NS, Geo> cx{a, ws, geo, geo.head(head)};
     cx.rho = NS * (rev ? rem : rem - NSL);
@@ -1305,7 +1330,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_bgrad(BwdProblem a, CbWs ws, Ge
 template <int D, int DT, int OT, class Geo>
 hipError_t launch_chunked(const BwdProblem& a, const CbWs& ws, const Geo& geo, int64_t nch, hipStream_t st) {
     prof_begin(a.p.timer, "k_bprep", st);
-    hipLaunchKernelGGL((k_bprep<D, DT, OT, Geo>), dim3((unsigned)nch), dim3(kThreads), 0, st, a, ws, geo);
+    hipLaunchKernelGGL((k_bprep<D, DT, OT, Geo>), dim3((unsigned)nch + (std::is_same_v<Geo, PackedGeo<D>> ? 1 : 0)),
+                       dim3(kThreads), 0, st, a, ws, geo);
     prof_end(a.p.timer, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -1363,8 +1389,8 @@ __global__ __launch_bounds__(kThreads) void k_bclear(Offsets off, ClearArgs c) {
 }
 
 template <int D>
-hipError_t launch_packed(const PackedBwd& b, BwdProblem a, const CbWs& ws, float* part_q, float* part_k, int64_t heads,
-                         hipStream_t st) {
+hipError_t launch_packed(const PackedBwd& b, BwdProblem a, const CbWs& ws, int32_t* order, float* part_q, float* part_k,
+                         int64_t heads, hipStream_t st) {
     const Packed& p = b.p;
     PackedGeo<D> geo{};
     geo.off = {p.cu, p.N, p.S};
@@ -1376,6 +1402,7 @@ hipError_t launch_packed(const PackedBwd& b, BwdProblem a, const CbWs& ws, float
     geo.v_stride = p.v_stride;
     geo.n_in = p.n_in;
     geo.slots = p.slots_in;
+    geo.order = order;
     const int64_t places = p.N / C + p.S;
     a.dq = geo.group > 1 ? part_q : b.dq;
     a.dk = geo.group > 1 ? part_k : b.dk;
@@ -1510,8 +1537,8 @@ static size_t packed_part(const Packed& p) {
 }
 
 size_t packed_backward_workspace(const Packed& p) {
-    if (p.S * p.Hv == 0 || p.N == 0) return 0;
-    return align256(packed_records(p)) + 2 * packed_part(p);
+    if (p.S * p.Hv == 0) return 0;
+    return align256(packed_records(p)) + 2 * packed_part(p) + align256((size_t)p.S * sizeof(int32_t));
 }
 
 hipError_t packed_backward(const PackedBwd& b, void* workspace, hipStream_t st) {
@@ -1536,12 +1563,14 @@ hipError_t packed_backward(const PackedBwd& b, void* workspace, hipStream_t st) 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     char* base = static_cast<char*>(workspace);
-    const int64_t heads = p.N > 0 ? packed_heads_per_launch(p) : p.Hv;
-    const CbWs ws = p.N > 0 ? carve(base, (size_t)(p.N / C + p.S) * (size_t)heads, p.dk) : CbWs{};
-    float* part_q = p.N > 0 ? reinterpret_cast<float*>(base + align256(packed_records(p))) : nullptr;
-    float* part_k = p.N > 0 ? part_q + packed_part(p) / sizeof(float) : nullptr;
-    return p.dk == 64 ? launch_packed<64>(b, a, ws, part_q, part_k, heads, st)
-                      : launch_packed<128>(b, a, ws, part_q, part_k, heads, st);
+    const int64_t heads = packed_heads_per_launch(p);
+    const CbWs ws = carve(base, (size_t)(p.N / C + p.S) * (size_t)heads, p.dk);
+    base += align256(packed_records(p));
+    float* part_q = reinterpret_cast<float*>(base);
+    float* part_k = reinterpret_cast<float*>(base + packed_part(p));
+    int32_t* order = reinterpret_cast<int32_t*>(base + 2 * packed_part(p));
+    return p.dk == 64 ? launch_packed<64>(b, a, ws, order, part_q, part_k, heads, st)
+                      : launch_packed<128>(b, a, ws, order, part_q, part_k, heads, st);
 }
 
 }  // namespace gdn

@@ -41,46 +41,38 @@ struct LnArgs {
     int want_params;
 };
 
-// V consecutive elements as loaded: 4 or 8 move as one or two 16-byte (8-byte)
-// pieces, 1 as an element
+// V consecutive elements as they lie in memory, kept so until they are used (a
+// row in flight takes half the registers in bf16), and as fp32
+typedef unsigned int u32x2v __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4v __attribute__((ext_vector_type(4)));
 template <int DT, int V>
-struct Vec {
-    float f[V];
+struct Raw {
+    static constexpr int kWords = V == 1 ? 1 : V * (DT == GDN_F32 ? 4 : 2) / 4;
+    uint32_t w[kWords];
 };
 template <int DT, int V>
-__device__ __forceinline__ Vec<DT, V> ldv(const void* base, int64_t i) {
-    Vec<DT, V> v;
+__device__ __forceinline__ void ld(Raw<DT, V>& r, const void* base, int64_t i) {
     if constexpr (V == 1) {
-        v.f[0] = gdn_ld<DT>(base, i);
-    } else if constexpr (DT == GDN_F32) {
-#pragma unroll
-        for (int k = 0; k < V; k += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i + k);
-            v.f[k] = x.x;
-            v.f[k + 1] = x.y;
-            v.f[k + 2] = x.z;
-            v.f[k + 3] = x.w;
-        }
+        if constexpr (DT == GDN_F32) r.w[0] = static_cast<const uint32_t*>(base)[i];
+        else r.w[0] = static_cast<const uint16_t*>(base)[i];
     } else {
-        uint32_t u[V / 2];
-        if constexpr (V == 8) {
-            const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-            u[0] = x.x;
-            u[1] = x.y;
-            u[2] = x.z;
-            u[3] = x.w;
+        const char* p = static_cast<const char*>(base) + i * (DT == GDN_F32 ? 4 : 2);
+        if constexpr (Raw<DT, V>::kWords == 2) {
+            const u32x2v x = *reinterpret_cast<const u32x2v*>(p);
+            r.w[0] = x[0];
+            r.w[1] = x[1];
         } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
-            u[0] = x.x;
-            u[1] = x.y;
-        }
+            const u32x4v x = *reinterpret_cast<const u32x4v*>(p);
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) {
-            v.f[2 * k] = __uint_as_float(u[k] << 16);
-            v.f[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+            for (int k = 0; k < 4; ++k) r.w[k] = x[k];
         }
     }
-    return v;
+}
+template <int DT, int V>
+__device__ __forceinline__ float el(const Raw<DT, V>& r, int e) {
+    if constexpr (DT == GDN_F32) return __uint_as_float(r.w[e]);
+    else if constexpr (V == 1) return __uint_as_float(r.w[0] << 16);
+    else return __uint_as_float(e & 1 ? r.w[e / 2] & 0xFFFF0000u : r.w[e / 2] << 16);
 }
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2v __attribute__((ext_vector_type(2)));
@@ -131,6 +123,39 @@ __device__ __forceinline__ float sum_row(float x, float* red) {
 template <int TPR>
 constexpr int ln_threads() { return TPR > 256 ? TPR : 256; }
 
+// A row's vectors of this thread; rows and columns past the end are zero.
+template <int DT, int V, int TPR, int NV>
+__device__ __forceinline__ void ld_row(Raw<DT, V> (&r)[NV], const void* base, int64_t row, bool on, int n, int c0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = c0 + i * TPR * V;
+#pragma unroll
+        for (int k = 0; k < Raw<DT, V>::kWords; ++k) r[i].w[k] = 0;
+        if (on && c < n) ld<DT, V>(r[i], base, row * n + c);
+    }
+}
+// V entries of a parameter row (w or b), `none` where it is not given
+template <int V>
+__device__ __forceinline__ void ld_param(float (&f)[V], const float* p, int c, float none) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = none;
+    if (!p) return;
+    if constexpr (V == 1) {
+        f[0] = p[c];
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p + c + k);
+            f[k] = x.x;
+            f[k + 1] = x.y;
+            f[k + 2] = x.z;
+            f[k + 3] = x.w;
+        }
+    }
+}
+
+// A workgroup's row groups take rows in steps of the grid, the next row in
+// flight while this one is worked off.
 template <int XT, int YT, int V, int TPR, int NV>
 __global__ __launch_bounds__(ln_threads<TPR>()) void k_ln_fwd(LnArgs a) {
     constexpr int RPB = ln_threads<TPR>() / TPR;
@@ -138,25 +163,23 @@ __global__ __launch_bounds__(ln_threads<TPR>()) void k_ln_fwd(LnArgs a) {
     const int n = (int)a.n;
     const int c0 = (threadIdx.x % TPR) * V;
     const float inv_n = 1.f / (float)n;
-    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
-        const int64_t row = row0 + threadIdx.x / TPR;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    Raw<XT, V> cur[NV], nxt[NV];
+    ld_row<XT, V, TPR, NV>(cur, a.x, row, row < a.rows, n, c0);
+    // (row - threadIdx.x / TPR is the same for the whole workgroup: so is the loop)
+    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += step, row += step) {
         const bool on = row < a.rows;
+        if (row0 + step < a.rows) ld_row<XT, V, TPR, NV>(nxt, a.x, row + step, row + step < a.rows, n, c0);
         float x[NV][V];
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * TPR * V;
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[i][e] = 0.f;
-            if (on && c < n) {
-                const Vec<XT, V> v = ldv<XT, V>(a.x, row * n + c);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    x[i][e] = v.f[e];
-                    s += v.f[e];
-                }
+            for (int e = 0; e < V; ++e) {
+                x[i][e] = el<XT, V>(cur[i], e);
+                s += x[i][e];
             }
-        }
         const float mean = sum_row<TPR>(s, red[0]) * inv_n;
         float q = 0.f;
 #pragma unroll
@@ -170,23 +193,26 @@ __global__ __launch_bounds__(ln_threads<TPR>()) void k_ln_fwd(LnArgs a) {
             }
         }
         const float rstd = 1.f / __fsqrt_rn(sum_row<TPR>(q, red[1]) * inv_n + a.eps);
-        if (!on) continue;
-        if (threadIdx.x % TPR == 0) {
-            if (a.mean) a.mean[row] = mean;
-            if (a.rstd) a.rstd[row] = rstd;
-        }
+        if (on) {
+            if (threadIdx.x % TPR == 0) {
+                if (a.mean) a.mean[row] = mean;
+                if (a.rstd) a.rstd[row] = rstd;
+            }
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * TPR * V;
-            if (c < n) {
-                float y[V];
-                const Vec<GDN_F32, V> w = a.w ? ldv<GDN_F32, V>(a.w, c) : Vec<GDN_F32, V>{};
-                const Vec<GDN_F32, V> b = a.b ? ldv<GDN_F32, V>(a.b, c) : Vec<GDN_F32, V>{};
+            for (int i = 0; i < NV; ++i) {
+                const int c = c0 + i * TPR * V;
+                if (c < n) {
+                    float y[V], w[V], b[V];
+                    ld_param<V>(w, a.w, c, 1.f);
+                    ld_param<V>(b, a.b, c, 0.f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) y[e] = x[i][e] * rstd * (a.w ? w.f[e] : 1.f) + b.f[e];
-                stv<YT, V>(a.y, row * n + c, y);
+                    for (int e = 0; e < V; ++e) y[e] = x[i][e] * rstd * w[e] + b[e];
+                    stv<YT, V>(a.y, row * n + c, y);
+                }
             }
         }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) cur[i] = nxt[i];
     }
 }
 
@@ -204,38 +230,41 @@ __global__ __launch_bounds__(ln_threads<TPR>()) void k_ln_bwd(LnArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = c0 + i * TPR * V;
-        const Vec<GDN_F32, V> v = a.w && c < n ? ldv<GDN_F32, V>(a.w, c) : Vec<GDN_F32, V>{};
+        ld_param<V>(w[i], c < n ? a.w : nullptr, c, 1.f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            w[i][e] = a.w ? v.f[e] : 1.f;
-            sw[i][e] = sb[i][e] = 0.f;
-        }
+        for (int e = 0; e < V; ++e) sw[i][e] = sb[i][e] = 0.f;
     }
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    Raw<XT, V> cx[NV], nx[NV];
+    Raw<YT, V> cd[NV], nd[NV];
+    float cm = 0.f, cr = 0.f, nm = 0.f, nr = 0.f;
+    auto fetch = [&](Raw<XT, V>(&x)[NV], Raw<YT, V>(&d)[NV], float& m, float& r, int64_t at) {
+        const bool on = at < a.rows;
+        ld_row<XT, V, TPR, NV>(x, a.x, at, on, n, c0);
+        ld_row<YT, V, TPR, NV>(d, a.dy, at, on, n, c0);
+        m = on ? a.mean[at] : 0.f;
+        r = on ? a.rstd[at] : 0.f;
+    };
+    fetch(cx, cd, cm, cr, row);
     int flip = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB, flip ^= 2) {
-        const int64_t row = row0 + threadIdx.x / TPR;
+    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += step, row += step, flip ^= 2) {
         const bool on = row < a.rows;
+        if (row0 + step < a.rows) fetch(nx, nd, nm, nr, row + step);
         float x[NV][V], g[NV][V];
-        const float mean = on ? a.mean[row] : 0.f, rstd = on ? a.rstd[row] : 0.f;
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * TPR * V;
+            // (a column past the end has dy = 0, and its x is never stored)
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[i][e] = g[i][e] = 0.f;
-            if (on && c < n) {
-                const Vec<XT, V> xv = ldv<XT, V>(a.x, row * n + c);
-                const Vec<YT, V> dv = ldv<YT, V>(a.dy, row * n + c);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float xh = (xv.f[e] - mean) * rstd;
-                    sw[i][e] += dv.f[e] * xh;
-                    sb[i][e] += dv.f[e];
-                    x[i][e] = xh;
-                    g[i][e] = dv.f[e] * w[i][e];
-                    s1 += g[i][e];
-                    s2 += g[i][e] * xh;
-                }
+            for (int e = 0; e < V; ++e) {
+                const float dy = el<YT, V>(cd[i], e), xh = (el<XT, V>(cx[i], e) - cm) * cr;
+                sw[i][e] += dy * xh;
+                sb[i][e] += dy;
+                x[i][e] = xh;
+                g[i][e] = dy * w[i][e];
+                s1 += g[i][e];
+                s2 += g[i][e] * xh;
             }
         }
         const float m1 = sum_row<TPR>(s1, red[flip]) * inv_n;
@@ -247,11 +276,18 @@ __global__ __launch_bounds__(ln_threads<TPR>()) void k_ln_bwd(LnArgs a) {
                 if (c < n) {
                     float dx[V];
 #pragma unroll
-                    for (int e = 0; e < V; ++e) dx[e] = rstd * (g[i][e] - m1 - x[i][e] * m2);
+                    for (int e = 0; e < V; ++e) dx[e] = cr * (g[i][e] - m1 - x[i][e] * m2);
                     stv<XT, V>(a.y, row * n + c, dx);
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            cx[i] = nx[i];
+            cd[i] = nd[i];
+        }
+        cm = nm;
+        cr = nr;
     }
     if (!a.want_params) return;
     float* pw = a.part + (int64_t)blockIdx.x * n;
@@ -287,8 +323,8 @@ __global__ __launch_bounds__(ln_threads<TPR>()) void k_ln_bwd(LnArgs a) {
 }
 
 // dw (blockIdx.y 0) and db (1) from `groups` partial rows: 16 columns a
-// workgroup, 16 threads a column
-constexpr int kPc = 16, kPr = 16;
+// workgroup, 64 threads a column
+constexpr int kPc = 16, kPr = 64;
 __global__ __launch_bounds__(kPc* kPr) void k_ln_params(const float* part, int groups, int64_t n, float* dw, float* db) {
     __shared__ float red[kPr][kPc + 1];
     float* dst = blockIdx.y ? db : dw;
@@ -319,7 +355,8 @@ __global__ __launch_bounds__(kPc* kPr) void k_ln_params(const float* part, int g
 
 // Backward workgroups: enough to fill the device a few times over, no more
 // than the rows give work for
-constexpr int kMaxGroups = 1024;
+constexpr int kMaxGroups = 512;
+constexpr int kFwdBlocks = 2048;
 int ln_rows_per_block(int tpr) { return tpr > 256 ? 1 : 256 / tpr; }
 
 // Threads a row and vectors a thread: the least that hold the row, at most 32
@@ -344,7 +381,7 @@ LnShape ln_shape(int64_t n, int v) {
 }
 int64_t ln_groups(int64_t rows, int tpr) {
     const int64_t rpb = ln_rows_per_block(tpr);
-    return std::min<int64_t>((rows + rpb - 1) / rpb, tpr > 256 ? kMaxGroups / 4 : kMaxGroups);
+    return std::min<int64_t>((rows + rpb - 1) / rpb, tpr > 256 ? kMaxGroups / 2 : kMaxGroups);
 }
 
 template <int XT, int YT, int V, int TPR, int NV>
@@ -357,7 +394,7 @@ hipError_t launch(const LnArgs& a, bool bwd, hipStream_t st) {
             hipLaunchKernelGGL((k_ln_bwd<XT, YT, V, TPR, NV>), dim3((unsigned)ln_groups(a.rows, TPR)), dim3(ln_threads<TPR>()),
                                0, st, a);
         else
-            hipLaunchKernelGGL((k_ln_fwd<XT, YT, V, TPR, NV>), dim3((unsigned)std::min<int64_t>(blocks, 1 << 20)),
+            hipLaunchKernelGGL((k_ln_fwd<XT, YT, V, TPR, NV>), dim3((unsigned)std::min<int64_t>(blocks, kFwdBlocks)),
                                dim3(ln_threads<TPR>()), 0, st, a);
         return hipGetLastError();
     }

@@ -28,6 +28,8 @@
 //     pass from the true start states.
 // Chunks and segments have their places by rule (gdn_packed_common.h).  Slots
 // outside the pool read as zero states and are not written.
+#include <type_traits>
+
 #include "gdn_internal.h"
 #include "gdn_mfma_common.h"
 #include "gdn_packed_common.h"
@@ -37,7 +39,7 @@ namespace gdn {
 namespace {
 
 // Sequences of fewer tokens go token by token where there is a choice.
-constexpr int kChunkMin = 64;
+constexpr int kChunkMin = 32;
 
 struct Pk {
     Packed p;
@@ -72,21 +74,30 @@ __device__ __forceinline__ float* state_to(const Packed& p, int64_t s, int64_t h
 // lane c at columns 4 (c + LPR i)), R rows a thread; the two dot products are
 // summed over the row's lanes by vector-ALU butterflies.  A single token is a
 // stream over the state (8 dk dv bytes a head; non-temporal, each byte is
-// touched once).  More tokens are staged kStage at a time, the next stage's
-// rows in flight while the current one is worked off.
+// touched once): k_pk_step.  k_pk_rec stages more of them kStage at a time in
+// LDS, the next stage's rows in flight while the current one is worked off.
 constexpr int kRecThreads = 256;
-constexpr int kStage = 16;
+constexpr int kStage = 8;
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
+// four consecutive input-typed elements, as loaded and as fp32
 template <int DT>
-__device__ __forceinline__ f32x4 ld4e(const void* p, int64_t i) {
-    if constexpr (DT == GDN_F32) {
-        return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
-    } else {
-        const u32x2 u = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + i);
+using R4 = std::conditional_t<DT == GDN_BF16, u32x2, f32x4>;
+template <int DT>
+__device__ __forceinline__ R4<DT> ldr(const void* base, int64_t i) {
+    if constexpr (DT == GDN_BF16) return *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + i);
+    else return *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + i);
+}
+template <int DT>
+__device__ __forceinline__ f32x4 cvt(const R4<DT>& u) {
+    if constexpr (DT == GDN_BF16)
         return f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xFFFF0000u), __uint_as_float(u[1] << 16),
                      __uint_as_float(u[1] & 0xFFFF0000u)};
-    }
+    else return u;
+}
+template <int DT>
+__device__ __forceinline__ f32x4 ld4e(const void* p, int64_t i) {
+    return cvt<DT>(ldr<DT>(p, i));
 }
 __device__ __forceinline__ float dot4e(const f32x4& x, const f32x4& y) {
     return x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
@@ -97,102 +108,161 @@ __device__ __forceinline__ void st_out(void* out, int64_t i, float x) {
     else static_cast<uint16_t*>(out)[i] = (uint16_t)pack_bf16(x, 0.f);
 }
 
-template <int LPR, int NP, int R, bool CH>
+// S' and o of one token: k, q, g (the gate) in the lane's pieces, v of its rows
+template <int LPR, int NP, int R>
+__device__ __forceinline__ void rec_token(f32x4 (&S)[R][NP], const f32x4 (&k)[NP], const f32x4 (&q)[NP],
+                                          const f32x4 (&g)[NP], const float (&v)[R], float beta, bool dtp, float scale,
+                                          float (&o)[R]) {
+    float pr[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        pr[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            if (dtp) S[j][i] *= g[i];
+            pr[j] += dot4e(S[j][i], k[i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) pr[j] = row_sum<LPR>(pr[j]);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const float e = beta * (v[j] - pr[j]);
+        o[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            S[j][i] = (dtp ? S[j][i] : S[j][i] * g[i]) + e * k[i];
+            o[j] += dot4e(S[j][i], q[i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) o[j] = scale * row_sum<LPR>(o[j]);
+}
+
+// The workgroup's place: sequence, head, rows; and the state pieces of a thread
+struct RecAt {
+    int s, h, hk, rb;
+    Span sp;
+    const float* src;
+    float* dst;
+};
+template <int RB>
+__device__ __forceinline__ bool rec_at(const Pk& a, RecAt& x) {
+    // workgroups go to the eight XCDs in turn: each XCD takes a run of
+    // sequences of its own
+    const unsigned nrb = ((unsigned)a.p.dv + RB - 1) / RB, one = nrb * a.Hv, run = 8 * one;
+    const unsigned g = blockIdx.x / run, r = blockIdx.x - g * run;
+    const unsigned block = (g + 1) * run <= gridDim.x ? g * run + (r % 8) * one + r / 8 : blockIdx.x;
+    const unsigned id = block / nrb;
+    x.rb = block - id * nrb;
+    x.s = id / a.Hv;
+    x.h = id - x.s * a.Hv;
+    x.hk = x.h / a.group;
+    x.sp = span_of(a.at, x.s);
+    x.src = state_from(a.p, x.s, x.h);
+    x.dst = state_to(a.p, x.s, x.h);
+    return x.sp.n < a.rec_below && !(x.sp.n == 0 && x.src == x.dst);
+}
+template <int LPR, int NP, int R>
+__device__ __forceinline__ void rec_load(const Packed& p, const RecAt& x, const int (&row)[R], int c, f32x4 (&S)[R][NP]) {
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int col = 4 * (c + LPR * i);
+            S[j][i] = zero4();
+            if (x.src && row[j] < (int)p.dv && col < (int)p.dk)
+                S[j][i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4v*>(x.src + row[j] * (int)p.dk + col));
+        }
+}
+template <int LPR, int NP, int R>
+__device__ __forceinline__ void rec_store(const Packed& p, const RecAt& x, const int (&row)[R], int c, const f32x4 (&S)[R][NP]) {
+    if (!x.dst) return;
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int col = 4 * (c + LPR * i);
+            if (row[j] < (int)p.dv && col < (int)p.dk)
+                __builtin_nontemporal_store((f32x4v)S[j][i], reinterpret_cast<f32x4v*>(x.dst + row[j] * (int)p.dk + col));
+        }
+}
+
+// Single tokens: read straight from memory, in as few registers and no LDS, so
+// that enough workgroups share a compute unit to keep the state's stream
+// going (longer sequences are right, one token after the other).
+template <int DT, int CH, int LPR, int R>
+__global__ __launch_bounds__(kRecThreads) void k_pk_step(Pk a) {
+    constexpr int RPW = 64 / LPR, RB = 4 * RPW * R;
+    const Packed& p = a.p;
+    RecAt x;
+    if (!rec_at<RB>(a, x)) return;
+    const int dk = (int)p.dk, dv = (int)p.dv;
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63, c = l % LPR;
+    const bool dtp = p.order == GDN_DECAY_THEN_PREDICT, on = 4 * c < dk;
+    int row[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) row[j] = x.rb * RB + (j * 4 + w) * RPW + l / LPR;
+    f32x4 S[R][1];
+    rec_load<LPR, 1, R>(p, x, row, c, S);
+    auto one = [&](int64_t t) {
+        f32x4 k[1], q[1], g[1];
+        float v[R], o[R];
+        k[0] = on ? ld4e<DT>(p.k, t * p.k_stride + x.hk * dk + 4 * c) : zero4();
+        q[0] = on ? ld4e<DT>(p.q, t * p.q_stride + x.hk * dk + 4 * c) : zero4();
+        if constexpr (CH != 0) {
+            g[0] = on ? *reinterpret_cast<const f32x4*>(p.alpha + (t * a.Hv + x.h) * dk + 4 * c) : zero4();
+        } else {
+            const float al = p.alpha[t * a.Hv + x.h];
+            g[0] = f32x4{al, al, al, al};
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) v[j] = row[j] < dv ? gdn_ld<DT>(p.v, t * p.v_stride + x.h * dv + row[j]) : 0.f;
+        rec_token<LPR, 1, R>(S, k, q, g, v, p.beta[t * a.Hv + x.h], dtp, p.scale, o);
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (c == 0 && row[j] < dv) st_out<DT>(p.out, (t * a.Hv + x.h) * dv + row[j], o[j]);
+    };
+    if (x.sp.n == 1)
+        one(x.sp.begin);
+    else
+        for (int64_t t = x.sp.begin; t < x.sp.begin + x.sp.n; ++t) one(t);
+    rec_store<LPR, 1, R>(p, x, row, c, S);
+}
+
+template <int DT, int LPR, int NP, int R, bool CH>
 struct RecShared {
     static constexpr int W = 4 * LPR * NP;                 // columns held
     static constexpr int RB = 4 * (64 / LPR) * R;          // rows of a workgroup
-    f32x4 k[2][kStage][W / 4], q[2][kStage][W / 4], a[CH ? 2 : 1][CH ? kStage : 1][W / 4];
+    R4<DT> k[2][kStage][W / 4], q[2][kStage][W / 4];
+    f32x4 a[CH ? 2 : 1][CH ? kStage : 1][W / 4];
     float v[2][kStage][RB], o[2][kStage][RB];
     float sc[2][kStage][2];  // alpha (scalar gate), beta
 };
 
 template <int DT, int CH, int LPR, int NP, int R>
 __global__ __launch_bounds__(kRecThreads) void k_pk_rec(Pk a) {
-    using Sh = RecShared<LPR, NP, R, CH != 0>;
+    using Sh = RecShared<DT, LPR, NP, R, CH != 0>;
     constexpr int RPW = 64 / LPR, RB = Sh::RB;
     __shared__ __attribute__((aligned(16))) Sh sh;
     const Packed& p = a.p;
-    const int dk = (int)p.dk, dv = (int)p.dv;
-    const int nrb = (dv + RB - 1) / RB;
-    const int sh_id = blockIdx.x / nrb, rb = blockIdx.x - sh_id * nrb;
-    const int s = sh_id / a.Hv, h = sh_id - s * a.Hv, hk = h / a.group;
-    const Span sp = span_of(a.at, s);
-    if (sp.n >= a.rec_below) return;
+    RecAt x;
+    if (!rec_at<RB>(a, x)) return;
+    const Span sp = x.sp;
+    const int dk = (int)p.dk, dv = (int)p.dv, rb = x.rb, h = x.h, hk = x.hk;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, c = l % LPR;
     const bool dtp = p.order == GDN_DECAY_THEN_PREDICT;
-    const float* src = state_from(p, s, h);
-    float* dst = state_to(p, s, h);
-    if (sp.n == 0 && src == dst) return;
-
     int row[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) row[j] = rb * RB + (j * 4 + w) * RPW + l / LPR;
     f32x4 S[R][NP];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-        row[j] = rb * RB + (j * 4 + w) * RPW + l / LPR;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int col = 4 * (c + LPR * i);
-            S[j][i] = zero4();
-            if (src && row[j] < dv && col < dk)
-                S[j][i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4v*>(src + (int64_t)row[j] * dk + col));
-        }
-    }
-    // one token: k, q, gate pieces of this lane, value entries of its rows
-    auto token = [&](const f32x4(&k)[NP], const f32x4(&q)[NP], const f32x4(&g)[NP], const float(&v)[R], float beta,
-                     float(&o)[R]) {
-        float pr[R];
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            pr[j] = 0.f;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                if (dtp) S[j][i] *= g[i];
-                pr[j] += dot4e(S[j][i], k[i]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < R; ++j) pr[j] = row_sum<LPR>(pr[j]);
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const float e = beta * (v[j] - pr[j]);
-            o[j] = 0.f;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                S[j][i] = (dtp ? S[j][i] : S[j][i] * g[i]) + e * k[i];
-                o[j] += dot4e(S[j][i], q[i]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < R; ++j) o[j] = p.scale * row_sum<LPR>(o[j]);
-    };
-
-    if (sp.n == 1) {
-        const int64_t t = sp.begin;
-        f32x4 k[NP], q[NP], g[NP];
-        float v[R], o[R];
-        const float al = CH ? 1.f : p.alpha[t * p.Hv + h];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int col = 4 * (c + LPR * i);
-            const bool on = col < dk;
-            k[i] = on ? ld4e<DT>(p.k, t * p.k_stride + hk * dk + col) : zero4();
-            q[i] = on ? ld4e<DT>(p.q, t * p.q_stride + hk * dk + col) : zero4();
-            if constexpr (CH != 0)
-                g[i] = on ? *reinterpret_cast<const f32x4*>(p.alpha + (t * p.Hv + h) * dk + col) : zero4();
-            else
-                g[i] = f32x4{al, al, al, al};
-        }
-#pragma unroll
-        for (int j = 0; j < R; ++j) v[j] = row[j] < dv ? gdn_ld<DT>(p.v, t * p.v_stride + h * dv + row[j]) : 0.f;
-        token(k, q, g, v, p.beta[t * p.Hv + h], o);
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (c == 0 && row[j] < dv) st_out<DT>(p.out, (t * p.Hv + h) * dv + row[j], o[j]);
-    } else if (sp.n > 1) {
+    rec_load<LPR, NP, R>(p, x, row, c, S);
+    if (sp.n > 0) {
         const int pieces = dk / 4;  // of a row
         constexpr int KP = (kStage * Sh::W / 4 + kRecThreads - 1) / kRecThreads;
         constexpr int VP = (kStage * RB + kRecThreads - 1) / kRecThreads;
-        f32x4 kr[KP], qr[KP], ar[CH ? KP : 1];
+        R4<DT> kr[KP], qr[KP];
+        f32x4 ar[CH ? KP : 1];
         float vr[VP], sr = 0.f;
         auto fetch = [&](int64_t t0) {
             const int m = (int)min<int64_t>(kStage, sp.n - t0);
@@ -201,8 +271,8 @@ __global__ __launch_bounds__(kRecThreads) void k_pk_rec(Pk a) {
                 const int e = tid + kRecThreads * i, t = min(e / (Sh::W / 4), m - 1), pc = e % (Sh::W / 4);
                 const bool on = pc < pieces;
                 const int64_t tok = sp.begin + t0 + t;
-                kr[i] = on ? ld4e<DT>(p.k, tok * p.k_stride + hk * dk + 4 * pc) : zero4();
-                qr[i] = on ? ld4e<DT>(p.q, tok * p.q_stride + hk * dk + 4 * pc) : zero4();
+                kr[i] = on ? ldr<DT>(p.k, tok * p.k_stride + hk * dk + 4 * pc) : R4<DT>{};
+                qr[i] = on ? ldr<DT>(p.q, tok * p.q_stride + hk * dk + 4 * pc) : R4<DT>{};
                 if constexpr (CH != 0)
                     ar[i] = on ? *reinterpret_cast<const f32x4*>(p.alpha + (tok * p.Hv + h) * dk + 4 * pc) : zero4();
             }
@@ -248,14 +318,14 @@ __global__ __launch_bounds__(kRecThreads) void k_pk_rec(Pk a) {
                 const float al = sh.sc[b][t][0];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    k[i] = sh.k[b][t][c + LPR * i];
-                    q[i] = sh.q[b][t][c + LPR * i];
+                    k[i] = cvt<DT>(sh.k[b][t][c + LPR * i]);
+                    q[i] = cvt<DT>(sh.q[b][t][c + LPR * i]);
                     if constexpr (CH != 0) g[i] = sh.a[b][t][c + LPR * i];
                     else g[i] = f32x4{al, al, al, al};
                 }
 #pragma unroll
                 for (int j = 0; j < R; ++j) v[j] = sh.v[b][t][row[j] - rb * RB];
-                token(k, q, g, v, sh.sc[b][t][1], o);
+                rec_token<LPR, NP, R>(S, k, q, g, v, sh.sc[b][t][1], dtp, p.scale, o);
 #pragma unroll
                 for (int j = 0; j < R; ++j)
                     if (c == 0) sh.o[b][t][row[j] - rb * RB] = o[j];
@@ -268,16 +338,7 @@ __global__ __launch_bounds__(kRecThreads) void k_pk_rec(Pk a) {
             }
         }
     }
-    if (dst) {
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int col = 4 * (c + LPR * i);
-                if (row[j] < dv && col < dk)
-                    __builtin_nontemporal_store((f32x4v)S[j][i], reinterpret_cast<f32x4v*>(dst + (int64_t)row[j] * dk + col));
-            }
-    }
+    rec_store<LPR, NP, R>(p, x, row, c, S);
 }
 
 template <int DT, int CH, int LPR, int NP, int R>
@@ -287,9 +348,21 @@ hipError_t launch_rec(const Pk& a, hipStream_t st) {
     hipLaunchKernelGGL((k_pk_rec<DT, CH, LPR, NP, R>), dim3((unsigned)blocks), dim3(kRecThreads), 0, st, a);
     return hipGetLastError();
 }
+template <int DT, int CH, int LPR, int R>
+hipError_t launch_step(const Pk& a, hipStream_t st) {
+    constexpr int RB = 4 * (64 / LPR) * R;
+    const int64_t blocks = a.p.S * a.p.Hv * ((a.p.dv + RB - 1) / RB);
+    hipLaunchKernelGGL((k_pk_step<DT, CH, LPR, R>), dim3((unsigned)blocks), dim3(kRecThreads), 0, st, a);
+    return hipGetLastError();
+}
 template <int DT, int CH>
 hipError_t launch_rec_shape(const Pk& a, hipStream_t st) {
     const int64_t pieces = a.p.dk / 4;
+    if (std::min(a.p.max_len, a.p.N) <= 1) {
+        if (pieces <= 8) return launch_step<DT, CH, 8, 4>(a, st);
+        if (pieces <= 16) return launch_step<DT, CH, 16, 4>(a, st);
+        return launch_step<DT, CH, 32, 4>(a, st);
+    }
     if (pieces <= 8) return launch_rec<DT, CH, 8, 1, 2>(a, st);
     if (pieces <= 16) return launch_rec<DT, CH, 16, 1, 2>(a, st);
     return launch_rec<DT, CH, 16, 2, 2>(a, st);
@@ -768,9 +841,9 @@ __global__ __launch_bounds__(seg_threads<D>(), D == 128 ? 2 : 2) void k_pk_seg(P
 
 // Start states of a sequence's segments: X <- S_end(g) + X M(g), sixteen rows
 // of one head a workgroup (rows are independent), wave w the columns 16 w ..;
-// fp32 MFMA, the next matrix in flight while this one multiplies.
+// fp32 MFMA, the next three matrices in flight while one multiplies.
 template <int D>
-__global__ __launch_bounds__(4 * D) void k_pk_chain(Pk a) {
+__global__ __launch_bounds__(4 * D, 2) void k_pk_chain(Pk a) {
     constexpr int NB = D / 16, LDX = D + 4;
     __shared__ __attribute__((aligned(16))) float X[2][16 * LDX];
     const Packed& p = a.p;
@@ -791,36 +864,51 @@ __global__ __launch_bounds__(4 * D) void k_pk_chain(Pk a) {
         return x;
     };
     f32x4 x = rows(at(a.s_end, 0));
-    f32x4 mt[NB], add = zero4();
-    auto fetch = [&](int64_t g) {
+    struct In {
+        f32x4 m[NB], add;
+    };
+    auto fetch = [&](In& in, int64_t g) {
+        g = min(g, ng - 1 > 1 ? ng - 2 : (int64_t)0);
         const float* m = at(a.m_end, g) + (int64_t)col * D;
 #pragma unroll
-        for (int k = 0; k < NB; ++k) mt[k] = *reinterpret_cast<const f32x4*>(m + 16 * k + 4 * g4);
-        add = rows(at(a.s_end, g));
+        for (int k = 0; k < NB; ++k) in.m[k] = ld_g<f32x4>(m + 16 * k + 4 * g4);
+        in.add = rows(at(a.s_end, g));
     };
-    if (ng > 2) fetch(1);
-    for (int64_t g = 1; g < ng; ++g) {
+    // step g: the start state of segment g, then X M(g) + S_end(g)
+    auto step = [&](int64_t g, const In& in) {
         float* dst = at(a.s_start, g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) dst[(int64_t)(16 * rt + 4 * g4 + r) * D + col] = x[r];
-        if (g == ng - 1) break;
         float* Xs = X[g & 1];
 #pragma unroll
         for (int r = 0; r < 4; ++r) Xs[(4 * g4 + r) * LDX + col] = x[r];
         __syncthreads();
-        f32x4 m0[NB];
-        f32x4 acc = add;
-#pragma unroll
-        for (int k = 0; k < NB; ++k) m0[k] = mt[k];
-        if (g + 1 < ng - 1) fetch(g + 1);
-        f32x4 acc2 = zero4();
+        f32x4 acc = in.add, acc2 = zero4();
 #pragma unroll
         for (int k = 0; k < NB; k += 2) {
-            acc = blk(*reinterpret_cast<const f32x4*>(&Xs[c16 * LDX + 16 * k + 4 * g4]), m0[k], acc);
-            acc2 = blk(*reinterpret_cast<const f32x4*>(&Xs[c16 * LDX + 16 * (k + 1) + 4 * g4]), m0[k + 1], acc2);
+            acc = blk(*reinterpret_cast<const f32x4*>(&Xs[c16 * LDX + 16 * k + 4 * g4]), in.m[k], acc);
+            acc2 = blk(*reinterpret_cast<const f32x4*>(&Xs[c16 * LDX + 16 * (k + 1) + 4 * g4]), in.m[k + 1], acc2);
         }
         x = acc + acc2;
+    };
+    if (ng > 2) {
+        // four matrices in flight (each step fetches the one three steps on)
+        In in[4];
+        fetch(in[0], 1);
+        fetch(in[1], 2);
+        fetch(in[2], 3);
+        for (int64_t g = 1; g < ng - 1; g += 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (g + u >= ng - 1) break;
+                fetch(in[(u + 3) & 3], g + u + 3);
+                step(g + u, in[u]);
+            }
+        }
     }
+    float* dst = at(a.s_start, ng - 1);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) dst[(int64_t)(16 * rt + 4 * g4 + r) * D + col] = x[r];
 }
 
 // Tokens of a segment, as a power of two: as many segments as fill the

@@ -52,5 +52,34 @@ __device__ __forceinline__ int64_t seq_of_place(const Offsets& p, int64_t place,
     return lo;
 }
 
+// The sequences by falling length (classes a quarter of an octave of 64-token
+// chunks wide; within a class in no particular order, which no result depends
+// on), so that the kernels that carry a state through a sequence start the
+// longest first.  By one workgroup of `threads`; hist: 2 x kLenClasses ints of
+// LDS.
+constexpr int kLenClasses = 128;
+__device__ __forceinline__ int len_class(int64_t n) {
+    const unsigned c = (unsigned)((n + 63) >> 6) + 1;
+    const int e = 31 - __clz(c);
+    const int key = 4 * e + (e >= 2 ? (c >> (e - 2)) & 3 : (c << (2 - e)) & 3);
+    return max(kLenClasses - 1 - key, 0);
+}
+__device__ __forceinline__ void order_sequences(const Offsets& p, int32_t* order, int* hist, int tid, int threads) {
+    for (int i = tid; i < 2 * kLenClasses; i += threads) hist[i] = 0;
+    __syncthreads();
+    for (int64_t s = tid; s < p.S; s += threads) atomicAdd(&hist[len_class(span_of(p, s).n)], 1);
+    __syncthreads();
+    if (tid == 0) {
+        int at = 0;
+        for (int i = 0; i < kLenClasses; ++i) {
+            hist[kLenClasses + i] = at;
+            at += hist[i];
+        }
+    }
+    __syncthreads();
+    for (int64_t s = tid; s < p.S; s += threads)
+        order[atomicAdd(&hist[kLenClasses + len_class(span_of(p, s).n)], 1)] = (int32_t)s;
+}
+
 }  // namespace
 }  // namespace gdn

@@ -506,30 +506,50 @@ def decode_step(q, k, v, alpha, beta, state=None, *, order=GDN_PREDICT_THEN_DECA
 
 # ---- packed ragged sequences over a pool of states ------------------------------
 
-def _on_device(device, fn, args):
-    """fn(*args, stream) with `device` current, on its current stream."""
+def _enqueue(where, args, device, timer):
+    """Entry point `where` (or its *_timed variant) on the current stream of
+    GPU `device`; raises GdnError."""
     import torch
-    if torch.cuda.current_device() != device.index:
+    C = torch._C
+    fn = getattr(_lib or lib(), where if timer is None else where + "_timed")
+    tail = () if timer is None else (timer.handle,)
+    if C._cuda_getDevice() == device:
+        rc = fn(*args, C._cuda_getCurrentRawStream(device), *tail)
+    else:
         with torch.cuda.device(device):
-            return fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = fn(*args, C._cuda_getCurrentRawStream(device), *tail)
+    if rc != GDN_OK:
+        raise GdnError(rc, where)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _on(t, device, dtype, what):
+    """t (a tensor or None) is contiguous, of dtype and on GPU `device`."""
+    if t is not None:
+        if t.dtype != dtype:
+            raise TypeError(f"{what} must be {dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"{what} must be on the GPU of q")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+
+
 def _packed_check(q, k, v, alpha, beta, cu_seqlens, pools, slots):
     import torch
-    if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[0] != q.shape[0]:
+    f32, i32 = torch.float32, torch.int32
+    shape = q.shape
+    if len(shape) != 3 or k.shape != shape or v.dim() != 3 or v.shape[0] != shape[0]:
         raise ValueError("q, k must be [N,Hk,dk] and v [N,Hv,dv]")
-    N, Hk, dk = q.shape
-    Hv, dv = v.shape[1:]
+    N, Hk, dk = shape
+    _, Hv, dv = v.shape
     dt = q.dtype
     if k.dtype != dt or v.dtype != dt:
         raise TypeError("q, k, v must share a dtype")
     for t, d in ((q, dk), (k, dk), (v, dv)):
-        if t.numel() and (t.stride(2) != 1 or (t.stride(1) != d and t.shape[1] > 1)):
+        if not t.is_contiguous() and (t.stride(2) != 1 or (t.stride(1) != d and t.shape[1] > 1)):
             raise ValueError("the heads and features of a token of q, k, v must be contiguous")
     if alpha.shape == (N, Hv):
         gate = GDN_GATE_SCALAR
@@ -548,20 +568,17 @@ def _packed_check(q, k, v, alpha, beta, cu_seqlens, pools, slots):
     for t in slots:
         if t is not None and t.shape != (S,):
             raise ValueError("slots must be [S]")
-    dev = q.device
-    for t in (cu_seqlens, *slots):
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError("cu_seqlens and slots must be int32")
-    for t in (alpha, beta, *pools):
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError("alpha, beta and states must be float32")
-    for t in (q, k, v, alpha, beta, cu_seqlens, *pools, *slots):
-        if t is not None and (not t.is_cuda or t.device != dev):
-            raise ValueError("all tensors must be on one GPU")
-    for t in (alpha, beta, cu_seqlens, *pools, *slots):
-        if t is not None and not t.is_contiguous():
-            raise ValueError("all tensors but q, k, v must be contiguous")
-    return N, S, Hk, Hv, dk, dv, gate
+    dev = q.get_device()
+    _on(alpha, dev, f32, "alpha")
+    _on(beta, dev, f32, "beta")
+    _on(cu_seqlens, dev, i32, "cu_seqlens")
+    for t in pools:
+        _on(t, dev, f32, "a state pool")
+    for t in slots:
+        _on(t, dev, i32, "slots")
+    if dev < 0 or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k, v must be on one GPU")
+    return N, S, Hk, Hv, dk, dv, gate, dev
 
 
 def _token_strides(q, k, v):
@@ -596,28 +613,29 @@ def packed_fwd(q, k, v, alpha, beta, cu_seqlens, state_in=None, slots_in=None, s
     import torch
     if state_out is None and slots_out is not None:
         raise ValueError("slots_out needs state_out")
-    N, S, Hk, Hv, dk, dv, gate = _packed_check(q, k, v, alpha, beta, cu_seqlens,
-                                               (state_in, state_out), (slots_in, slots_out))
+    N, S, Hk, Hv, dk, dv, gate, dev = _packed_check(q, k, v, alpha, beta, cu_seqlens,
+                                                    (state_in, state_out), (slots_in, slots_out))
     if state_out is None:
-        state_out = torch.empty((S, Hv, dv, dk), dtype=torch.float32, device=q.device)
+        state_out = q.new_empty((S, Hv, dv, dk), dtype=torch.float32)
     if out is None:
-        out = torch.empty((N, Hv, dv), dtype=q.dtype, device=q.device)
-    elif out.shape != (N, Hv, dv) or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
-        raise ValueError("out must be a contiguous [N,Hv,dv] of q's dtype")
+        out = q.new_empty((N, Hv, dv))
+    else:
+        if out.shape != (N, Hv, dv):
+            raise ValueError("out must be [N,Hv,dv]")
+        _on(out, dev, q.dtype, "out")
     if max_len is None:
         max_len = N
     code = _dtype_code(q)
     if workspace is None:
         n = lib().gdn_packed_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, code, gate)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        if n:
+            workspace = q.new_empty((n,), dtype=torch.uint8)
     sq, sk, sv = _token_strides(q, k, v)
     args = (N, S, Hk, Hv, dk, dv, 0 if state_in is None else state_in.shape[0], state_out.shape[0], max_len, code, gate, order, scale,
             _addr(q), sq, _addr(k), sk, _addr(v), sv, _addr(alpha), _addr(beta), _addr(cu_seqlens),
             _addr(state_in), _addr(slots_in), _addr(state_out), _addr(slots_out), _addr(out),
             _addr(workspace), 0 if workspace is None else workspace.numel())
-    rc = _on_device(q.device, lambda *a: _call("gdn_packed_fwd", a, timer), args)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_packed_fwd")
+    _enqueue("gdn_packed_fwd", args, dev, timer)
     return out, state_out
 
 
@@ -630,27 +648,27 @@ def packed_backward(q, k, v, alpha, beta, cu_seqlens, state_in, slots_in, grad_o
     like q, k, v, alpha, beta and the sequences' states [S,Hv,dv,dk] (None when
     not wanted); rows outside every sequence are zero."""
     import torch
-    N, S, Hk, Hv, dk, dv, gate = _packed_check(q, k, v, alpha, beta, cu_seqlens, (state_in,), (slots_in,))
-    dev, f32 = q.device, torch.float32
-    if grad_out.shape != (N, Hv, dv) or grad_out.dtype != q.dtype or grad_out.device != dev or not grad_out.is_contiguous():
-        raise ValueError("grad_out must be a contiguous [N,Hv,dv] of q's dtype")
-    if grad_state_out is not None and (grad_state_out.shape != (S, Hv, dv, dk) or grad_state_out.dtype != f32 or
-                                       grad_state_out.device != dev or not grad_state_out.is_contiguous()):
-        raise ValueError("grad_state_out must be a contiguous float32 [S,Hv,dv,dk]")
-    grads = [torch.empty(t.shape, dtype=f32, device=dev) for t in (q, k, v, alpha, beta)]
-    ds0 = torch.empty((S, Hv, dv, dk), dtype=f32, device=dev) if want_grad_state0 else None
+    N, S, Hk, Hv, dk, dv, gate, dev = _packed_check(q, k, v, alpha, beta, cu_seqlens, (state_in,), (slots_in,))
+    f32 = torch.float32
+    if grad_out.shape != (N, Hv, dv):
+        raise ValueError("grad_out must be [N,Hv,dv]")
+    _on(grad_out, dev, q.dtype, "grad_out")
+    if grad_state_out is not None and grad_state_out.shape != (S, Hv, dv, dk):
+        raise ValueError("grad_state_out must be [S,Hv,dv,dk]")
+    _on(grad_state_out, dev, f32, "grad_state_out")
+    grads = [q.new_empty(t.shape, dtype=f32) for t in (q, k, v, alpha, beta)]
+    ds0 = q.new_empty((S, Hv, dv, dk), dtype=f32) if want_grad_state0 else None
     code = _dtype_code(q)
     if workspace is None:
         n = lib().gdn_packed_backward_workspace_bytes(N, S, Hk, Hv, dk, dv, code, gate)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        if n:
+            workspace = q.new_empty((n,), dtype=torch.uint8)
     sq, sk, sv = _token_strides(q, k, v)
     args = (N, S, Hk, Hv, dk, dv, 0 if state_in is None else state_in.shape[0], code, gate, order, scale,
             _addr(q), sq, _addr(k), sk, _addr(v), sv, _addr(alpha), _addr(beta), _addr(cu_seqlens),
             _addr(state_in), _addr(slots_in), _addr(grad_out), _addr(grad_state_out), *map(_addr, grads), _addr(ds0),
             _addr(workspace), 0 if workspace is None else workspace.numel())
-    rc = _on_device(dev, lambda *a: _call("gdn_packed_backward", a, timer), args)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_packed_backward")
+    _enqueue("gdn_packed_backward", args, dev, timer)
     return (*grads, ds0)
 
 
@@ -667,22 +685,23 @@ def _norm_code(dtype):
 
 def _norm_check(x, params, stats):
     import torch
-    if x.dim() < 1 or not x.is_cuda or not x.is_contiguous():
+    dev = x.get_device()
+    if x.dim() < 1 or dev < 0 or not x.is_contiguous():
         raise ValueError("x must be contiguous and on the GPU")
     n = x.shape[-1]
     if n == 0:
         raise ValueError("rows must hold at least one element")
     rows = x.numel() // n
     for t in params:
-        if t is not None and t.shape != (n,):
-            raise ValueError("weight and bias must be [n]")
+        if t is not None:
+            if t.shape != (n,):
+                raise ValueError("weight and bias must be [n]")
+            _on(t, dev, torch.float32, "weight and bias")
     for t in stats:
-        if t is not None and t.numel() != rows:
+        if t.numel() != rows:
             raise ValueError("mean and rstd must hold one value a row")
-    for t in (*params, *stats):
-        if t is not None and (t.dtype != torch.float32 or t.device != x.device or not t.is_contiguous()):
-            raise ValueError("weight, bias, mean and rstd must be contiguous float32 on x's GPU")
-    return rows, n
+        _on(t, dev, torch.float32, "mean and rstd")
+    return rows, n, dev
 
 
 def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=None, out=None, timer=None):
@@ -691,18 +710,19 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=None, out=N
     Returns (y, mean, rstd), the statistics fp32 and shaped as x without its
     last dimension."""
     import torch
-    rows, n = _norm_check(x, (weight, bias), ())
+    rows, n, dev = _norm_check(x, (weight, bias), ())
+    shape = x.shape
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    elif out.shape != x.shape or out.device != x.device or not out.is_contiguous() or out_dtype not in (None, out.dtype):
-        raise ValueError("out must be contiguous, shaped as x and of out_dtype")
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    args = (rows, n, _norm_code(x.dtype), _norm_code(out.dtype), eps, _addr(x), _addr(weight), _addr(bias),
-            _addr(out), _addr(mean), _addr(rstd))
-    rc = _on_device(x.device, lambda *a: _call("gdn_layer_norm_fwd", a, timer), args)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_layer_norm_fwd")
+        out = x.new_empty(shape, dtype=out_dtype or x.dtype)
+    else:
+        if out.shape != shape:
+            raise ValueError("out must be shaped as x")
+        _on(out, dev, out_dtype or out.dtype, "out")
+    mean = x.new_empty(shape[:-1], dtype=torch.float32)
+    rstd = x.new_empty(shape[:-1], dtype=torch.float32)
+    _enqueue("gdn_layer_norm_fwd", (rows, n, _norm_code(x.dtype), _norm_code(out.dtype), eps, x.data_ptr(),
+                                    _addr(weight), _addr(bias), out.data_ptr(), mean.data_ptr(), rstd.data_ptr()),
+             dev, timer)
     return out, mean, rstd
 
 
@@ -711,19 +731,18 @@ def layer_norm_backward(grad_y, x, weight, mean, rstd, *, want_x=True, want_weig
     """Gradients of layer_norm_fwd: gdn_layer_norm_backward.  Returns (grad_x of
     x's dtype, grad_weight [n], grad_bias [n] fp32), None where not wanted."""
     import torch
-    rows, n = _norm_check(x, (weight,), (mean, rstd))
-    if grad_y.shape != x.shape or grad_y.device != x.device or not grad_y.is_contiguous():
-        raise ValueError("grad_y must be contiguous and shaped as x")
-    dev = x.device
-    dx = torch.empty_like(x) if want_x else None
-    dw = torch.empty(n, dtype=torch.float32, device=dev) if want_weight else None
-    db = torch.empty(n, dtype=torch.float32, device=dev) if want_bias else None
+    rows, n, dev = _norm_check(x, (weight,), (mean, rstd))
+    if grad_y.shape != x.shape:
+        raise ValueError("grad_y must be shaped as x")
+    _on(grad_y, dev, grad_y.dtype, "grad_y")
+    f32 = torch.float32
+    dx = x.new_empty(x.shape) if want_x else None
+    dw = x.new_empty((n,), dtype=f32) if want_weight else None
+    db = x.new_empty((n,), dtype=f32) if want_bias else None
     if workspace is None and (want_weight or want_bias):
-        workspace = torch.empty(lib().gdn_layer_norm_workspace_bytes(rows, n), dtype=torch.uint8, device=dev)
-    args = (rows, n, _norm_code(x.dtype), _norm_code(grad_y.dtype), _addr(grad_y), _addr(x), _addr(weight),
-            _addr(mean), _addr(rstd), _addr(dx), _addr(dw), _addr(db), _addr(workspace),
-            0 if workspace is None else workspace.numel())
-    rc = _on_device(dev, lambda *a: _call("gdn_layer_norm_backward", a, timer), args)
-    if rc != GDN_OK:
-        raise GdnError(rc, "gdn_layer_norm_backward")
+        workspace = x.new_empty((lib().gdn_layer_norm_workspace_bytes(rows, n),), dtype=torch.uint8)
+    _enqueue("gdn_layer_norm_backward", (rows, n, _norm_code(x.dtype), _norm_code(grad_y.dtype), grad_y.data_ptr(),
+                                         x.data_ptr(), _addr(weight), mean.data_ptr(), rstd.data_ptr(), _addr(dx),
+                                         _addr(dw), _addr(db), _addr(workspace),
+                                         0 if workspace is None else workspace.numel()), dev, timer)
     return dx, dw, db

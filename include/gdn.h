@@ -377,8 +377,8 @@ int gdn_packed_path(int64_t dk, int64_t dv, int32_t dtype, int32_t gate);
  *                   not wanted
  *   workspace       gdn_packed_backward_workspace_bytes(...): per value head
  *                   and chunk as gdn_backward, capped at about 8 GiB (more
- *                   heads run in groups), and with shared key heads twice
- *                   4 N Hv dk
+ *                   heads run in groups), 4 S, and with shared key heads
+ *                   twice 4 N Hv dk
  * Alignment: as gdn_packed_fwd; the gradients on 16 bytes, grad_alpha and
  * grad_beta on 4.
  */

@@ -149,7 +149,7 @@ def test_packed_backward_refusals(kw, want):
 
 def test_packed_backward_workspace():
     ws = gdn.gdn_packed_backward_workspace_bytes
-    assert ws(100, 2, 2, 4, 32, 32, 1, 0) == 0 and ws(100, 2, 2, 4, 64, 64, 1, 1) == 0 and ws(0, 2, 2, 4, 64, 64, 1, 0) == 0
+    assert ws(100, 2, 2, 4, 32, 32, 1, 0) == 0 and ws(100, 2, 2, 4, 64, 64, 1, 1) == 0 and ws(0, 0, 2, 4, 64, 64, 1, 0) == 0
     one, shared = ws(1000, 2, 4, 4, 64, 64, 1, 0), ws(1000, 2, 2, 4, 64, 64, 1, 0)
     assert shared == one + 2 * (1000 * 4 * 64 * 4)
     assert ws(1 << 20, 1, 64, 64, 128, 128, 1, 0) <= (8 << 30) + (1 << 20)  # heads in groups
