@@ -10,8 +10,12 @@ namespace {
 bool aligned(const void* ptr, uintptr_t a) { return (uintptr_t)ptr % a == 0; }
 int finish(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_E_HIP; }
 bool dim_ok(int64_t d) { return d >= 16 && d <= 128 && d % 16 == 0; }
-constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+// A launch holds fewer than 2^32 threads.  The most a call asks for: 4 x 256 a
+// sequence and head token by token; 8 x 512 a sequence and head and, beside
+// those, 8 x 512 a head and 2048 tokens or 256 a head and 64 tokens in chunks.
+constexpr int64_t kMaxStates = (int64_t)1 << 21, kMaxChunkStates = (int64_t)1 << 19, kMaxChunkRows = (int64_t)1 << 28;
 constexpr int64_t kMaxCols = 16384;
+constexpr int64_t kMaxStride = (int64_t)1 << 23;
 
 int packed_check(const Packed& p) {
     if (p.dtype != GDN_F32 && p.dtype != GDN_BF16) return GDN_E_ARG;
@@ -20,12 +24,23 @@ int packed_check(const Packed& p) {
     if (p.N < 0 || p.S < 0 || p.Hk < 0 || p.Hv < 0 || p.dk <= 0 || p.dv <= 0 || p.n_in < 0 || p.n_out < 0 || p.max_len < 0)
         return GDN_E_SHAPE;
     if (p.Hk == 0 ? p.Hv != 0 : p.Hv % p.Hk != 0) return GDN_E_SHAPE;
-    // offsets into the sequences are 32-bit integers; places (at most one a
-    // sequence and one a 64 tokens) and heads map onto one grid dimension
+    // offsets into the sequences are 32-bit integers
     if (p.N > INT32_MAX || p.S > INT32_MAX || p.Hv > 65535) return GDN_E_SHAPE;
     if (!dim_ok(p.dk) || !dim_ok(p.dv)) return GDN_E_UNSUPPORTED;
-    if ((p.N / 64 + p.S) * p.Hv * 16 > kMaxGrid) return GDN_E_SHAPE;
+    if (p.S * p.Hv > kMaxStates) return GDN_E_SHAPE;
     return GDN_OK;
+}
+int chunk_check(const Packed& p) {
+    return p.S * p.Hv > kMaxChunkStates || p.N * p.Hv > kMaxChunkRows ? GDN_E_SHAPE : GDN_OK;
+}
+int packed_fwd_check(const Packed& p) {
+    const int s = packed_check(p);
+    return s == GDN_OK && packed_in_chunks(p) ? chunk_check(p) : s;
+}
+int packed_bwd_check(const Packed& p) {
+    const int s = packed_check(p);
+    if (s != GDN_OK) return s;
+    return chunked_backward_supported(p.dk, p.dv, p.gate) ? chunk_check(p) : GDN_E_UNSUPPORTED;
 }
 
 Packed packed_sizes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in,
@@ -41,7 +56,8 @@ Packed packed_sizes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, in
 int packed_inputs(const Packed& p) {
     const int64_t e = p.dtype == GDN_BF16 ? 2 : 4;
     if (p.q_stride < p.Hk * p.dk || p.k_stride < p.Hk * p.dk || p.v_stride < p.Hv * p.dv) return GDN_E_SHAPE;
-    if (p.q_stride > kMaxGrid || p.k_stride > kMaxGrid || p.v_stride > kMaxGrid) return GDN_E_SHAPE;
+    // (a chunk's rows are addressed with 32-bit offsets)
+    if (p.q_stride > kMaxStride || p.k_stride > kMaxStride || p.v_stride > kMaxStride) return GDN_E_SHAPE;
     if ((p.q_stride * e | p.k_stride * e | p.v_stride * e) % 16 != 0) return GDN_E_ARG;
     if (p.N > 0 && (!p.q || !p.k || !p.v || !p.alpha || !p.beta)) return GDN_E_ARG;
     if (!p.cu) return GDN_E_ARG;
@@ -61,7 +77,7 @@ int packed_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int6
                   const int32_t* slots_out, void* out, void* workspace, size_t workspace_bytes, void* stream,
                   gdn_timer* timer) {
     Packed p = packed_sizes(N, S, Hk, Hv, dk, dv, n_in, n_out, max_len, dtype, gate, order);
-    int s = packed_check(p);
+    int s = packed_fwd_check(p);
     if (s != GDN_OK) return s;
     if (S * Hv == 0) return GDN_OK;
     p.scale = scale;
@@ -89,9 +105,8 @@ int packed_bwd_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, 
     PackedBwd b{};
     Packed& p = b.p;
     p = packed_sizes(N, S, Hk, Hv, dk, dv, n_in, 0, N, dtype, gate, order);
-    int s = packed_check(p);
+    int s = packed_bwd_check(p);
     if (s != GDN_OK) return s;
-    if (!chunked_backward_supported(dk, dv, gate)) return GDN_E_UNSUPPORTED;
     if (S * Hv == 0) return GDN_OK;
     p.scale = scale;
     p.q = q; p.k = k; p.v = v;
@@ -193,7 +208,7 @@ int gdn_packed_fwd_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t d
 size_t gdn_packed_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t max_len,
                                   int32_t dtype, int32_t gate) {
     const Packed p = packed_sizes(N, S, Hk, Hv, dk, dv, 0, 0, max_len, dtype, gate, GDN_PREDICT_THEN_DECAY);
-    return packed_check(p) != GDN_OK || S * Hv == 0 ? 0 : packed_workspace(p);
+    return packed_fwd_check(p) != GDN_OK || S * Hv == 0 ? 0 : packed_workspace(p);
 }
 
 int gdn_packed_path(int64_t dk, int64_t dv, int32_t dtype, int32_t gate) {
@@ -230,7 +245,7 @@ int gdn_packed_backward_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int6
 size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
                                            int32_t dtype, int32_t gate) {
     const Packed p = packed_sizes(N, S, Hk, Hv, dk, dv, 0, 0, N, dtype, gate, GDN_PREDICT_THEN_DECAY);
-    return packed_check(p) != GDN_OK || !chunked_backward_supported(dk, dv, gate) ? 0 : packed_backward_workspace(p);
+    return packed_bwd_check(p) != GDN_OK ? 0 : packed_backward_workspace(p);
 }
 
 int gdn_layer_norm_fwd(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps, const void* x,

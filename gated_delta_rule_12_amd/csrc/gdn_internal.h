@@ -153,7 +153,8 @@ struct Packed {
     gdn_timer* timer;
 };
 // Whether the chunk kernels serve these shapes, and the bytes they need.
-bool packed_chunked(const Packed& p);
+bool packed_chunked(const Packed& p);    // its shapes have chunk kernels
+bool packed_in_chunks(const Packed& p);  // and max_len says that they are worth it
 size_t packed_workspace(const Packed& p);
 hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st);
 

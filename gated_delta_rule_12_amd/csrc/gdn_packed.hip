@@ -11,8 +11,9 @@
 // notes' GDN and KDA paragraphs).
 //
 // Two forms serve one call, each sequence taking one of them by its length:
-//   k_pk_rec, token by token, the state in registers: steps of a generation,
-//     drafted tokens, short prompts, and every shape without chunk kernels;
+//   token by token, the state in registers (k_pk_step, k_pk_rec): steps of a
+//     generation, drafted tokens, short prompts, and every shape without chunk
+//     kernels;
 //   the chunk form (scalar gate, bf16, dk = dv = D in {64, 128}, sequences of
 //     at least kChunkMin tokens), C = 64 tokens a chunk (notes, WY/UT section):
 //       T'    = (I + diag(beta) L)^{-1} diag(beta),  L_tj = e^{g'_t - g_j} k_t.k_j (j < t)
@@ -24,8 +25,11 @@
 //     than a segment run as a state pass (every segment but the last, from
 //     zero, with the matrix M its start state is multiplied by), the chain of
 //     start states (k_pk_chain: S_start(g + 1) = S_end(g) + S_start(g) M(g),
-//     the sequence-parallel notes' increment and correction) and the output
-//     pass from the true start states.
+//     the sequence-parallel notes' increment and correction, as a two-level
+//     scan where it is long) and the output pass from the true start states.
+// Measured (bf16, D = 128): 8 sequences of 1 to 8192 tokens, 16384 together,
+// 16 value heads, 332 us (prep 61, state pass 80, chain 30, outputs 158; bytes
+// alone 47 us); one of 65531, 4 heads, 405 us (46, 115, 101, 149).
 // Chunks and segments have their places by rule (gdn_packed_common.h).  Slots
 // outside the pool read as zero states and are not written.
 #include <type_traits>
@@ -38,22 +42,31 @@
 namespace gdn {
 namespace {
 
-// Sequences of fewer tokens go token by token where there is a choice.
+// Sequences of fewer tokens go token by token.  Token by token, and in chunks:
+// 256 sequences x 16 heads of 128, 24 tokens 385 and 351 us, 32 tokens 508 and
+// 359, 64 tokens 932 and 413; 16 sequences, 24 tokens 31 and 38 us, 32 tokens
+// 40 and 38; heads of 64, 256 sequences, 32 tokens 166 and 184 us, 48 tokens
+// 235 and 188.
 constexpr int kChunkMin = 32;
 
 struct Pk {
     Packed p;
     Offsets at;
     int Hv, group;   // value heads; value heads per key head
-    int rec_below;   // k_pk_rec takes sequences of fewer tokens
+    int rec_below;   // sequences of fewer tokens go token by token
     int seg_shift;   // a segment holds 2^seg_shift tokens
     int64_t nslot;   // places for chunks
     int64_t nseg;    // places for segments
-    float* T;        // [place, head][10 blocks of 16 x 16]: T' (lower blocks, row by row)
+    int32_t* order;  // sequences by falling length
+    int32_t* first;  // [S + 1]: segments before each rank of that order
+    u16x8* T;        // [place, head][kTfrag]: T' as A operands
     float* G;        // [place, head][kGate]
     float* s_end;    // [place, head][D][D]: end states of the state pass
     float* m_end;    // [place, head][D][D]: M transposed
     float* s_start;  // [place, head][D][D]: start states of the output pass
+    bool two_level;  // long chains of start states run as a two-level scan:
+    float* q_blk;    // [block place, head][D][D]: a block of maps as one: addend
+    float* p_blk;    // [block place, head][D][D]: and matrix, transposed
 };
 
 __device__ __forceinline__ const float* state_from(const Packed& p, int64_t s, int64_t h) {
@@ -78,6 +91,7 @@ __device__ __forceinline__ float* state_to(const Packed& p, int64_t s, int64_t h
 // LDS, the next stage's rows in flight while the current one is worked off.
 constexpr int kRecThreads = 256;
 constexpr int kStage = 8;
+constexpr int kRecLPR = 16, kRecR = 2;
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
 // four consecutive input-typed elements, as loaded and as fp32
@@ -147,12 +161,12 @@ struct RecAt {
     float* dst;
 };
 template <int RB>
-__device__ __forceinline__ bool rec_at(const Pk& a, RecAt& x) {
+__device__ __forceinline__ bool rec_at(const Pk& a, unsigned blocks, RecAt& x) {
     // workgroups go to the eight XCDs in turn: each XCD takes a run of
     // sequences of its own
     const unsigned nrb = ((unsigned)a.p.dv + RB - 1) / RB, one = nrb * a.Hv, run = 8 * one;
     const unsigned g = blockIdx.x / run, r = blockIdx.x - g * run;
-    const unsigned block = (g + 1) * run <= gridDim.x ? g * run + (r % 8) * one + r / 8 : blockIdx.x;
+    const unsigned block = (g + 1) * run <= blocks ? g * run + (r % 8) * one + r / 8 : blockIdx.x;
     const unsigned id = block / nrb;
     x.rb = block - id * nrb;
     x.s = id / a.Hv;
@@ -196,7 +210,7 @@ __global__ __launch_bounds__(kRecThreads) void k_pk_step(Pk a) {
     constexpr int RPW = 64 / LPR, RB = 4 * RPW * R;
     const Packed& p = a.p;
     RecAt x;
-    if (!rec_at<RB>(a, x)) return;
+    if (!rec_at<RB>(a, gridDim.x, x)) return;
     const int dk = (int)p.dk, dv = (int)p.dv;
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63, c = l % LPR;
     const bool dtp = p.order == GDN_DECAY_THEN_PREDICT, on = 4 * c < dk;
@@ -240,14 +254,14 @@ struct RecShared {
     float sc[2][kStage][2];  // alpha (scalar gate), beta
 };
 
+// the work of the first `blocks` workgroups of a launch
 template <int DT, int CH, int LPR, int NP, int R>
-__global__ __launch_bounds__(kRecThreads) void k_pk_rec(Pk a) {
+__device__ __forceinline__ void rec_block(const Pk& a, unsigned blocks, RecShared<DT, LPR, NP, R, CH != 0>& sh) {
     using Sh = RecShared<DT, LPR, NP, R, CH != 0>;
     constexpr int RPW = 64 / LPR, RB = Sh::RB;
-    __shared__ __attribute__((aligned(16))) Sh sh;
     const Packed& p = a.p;
     RecAt x;
-    if (!rec_at<RB>(a, x)) return;
+    if (!rec_at<RB>(a, blocks, x)) return;
     const Span sp = x.sp;
     const int dk = (int)p.dk, dv = (int)p.dv, rb = x.rb, h = x.h, hk = x.hk;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, c = l % LPR;
@@ -342,6 +356,12 @@ __global__ __launch_bounds__(kRecThreads) void k_pk_rec(Pk a) {
 }
 
 template <int DT, int CH, int LPR, int NP, int R>
+__global__ __launch_bounds__(kRecThreads) void k_pk_rec(Pk a) {
+    __shared__ __attribute__((aligned(16))) RecShared<DT, LPR, NP, R, CH != 0> sh;
+    rec_block<DT, CH, LPR, NP, R>(a, gridDim.x, sh);
+}
+
+template <int DT, int CH, int LPR, int NP, int R>
 hipError_t launch_rec(const Pk& a, hipStream_t st) {
     constexpr int RB = 4 * (64 / LPR) * R;
     const int64_t blocks = a.p.S * a.p.Hv * ((a.p.dv + RB - 1) / RB);
@@ -363,70 +383,152 @@ hipError_t launch_rec_shape(const Pk& a, hipStream_t st) {
         if (pieces <= 16) return launch_step<DT, CH, 16, 4>(a, st);
         return launch_step<DT, CH, 32, 4>(a, st);
     }
-    if (pieces <= 8) return launch_rec<DT, CH, 8, 1, 2>(a, st);
-    if (pieces <= 16) return launch_rec<DT, CH, 16, 1, 2>(a, st);
-    return launch_rec<DT, CH, 16, 2, 2>(a, st);
+    if (pieces <= 8) return launch_rec<DT, CH, 8, 1, kRecR>(a, st);
+    if (pieces <= 16) return launch_rec<DT, CH, kRecLPR, 1, kRecR>(a, st);
+    return launch_rec<DT, CH, kRecLPR, 2, kRecR>(a, st);
 }
 
 // ---------------------------------------------------------------------------
 // chunk form
 // ---------------------------------------------------------------------------
-// Gate rows of a chunk (floats): gamma, gamma', gamma_C / gamma, the log
-// prefix as hi + lo, gamma_C.
-constexpr int kGgam = 0, kGgamp = 64, kGtail = 128, kGhi = 192, kGlo = 256, kGlast = 320, kGate = 324;
+// Rows of a chunk's factors (floats), t a token: scale gamma_t / xq,
+// gamma'_t / xk, gamma_C / (gamma_t xk), the log prefix as hi + lo; then
+// gamma_C, 1 / xT, scale / (xq xk), xk, xq (xk, xq, xT: powers of two, below).
+constexpr int kGgam = 0, kGgamp = 64, kGtail = 128, kGhi = 192, kGlo = 256, kGlast = 320, kGit = 321, kGip = 322, kGxk = 323,
+              kGxq = 324, kGate = 328;
 constexpr int kGatePieces = kGate / 4;
-constexpr int kTblk = 10 * 256;  // floats of T' per chunk: lower blocks (m, j), j <= m
+// T' of a chunk as A operands of 32 x 32 x 16 products: lower blocks (0, 0),
+// (1, 0), (1, 1) of 32 x 32, two steps of 16 columns each, two terms
+constexpr int kTfrag = 3 * 2 * 2 * 64;
+// ... and of scale P, two terms
+constexpr int kPfrag = 3 * 2 * 2 * 64;
 constexpr int LDA = C + 4;
-__device__ __forceinline__ constexpr int tblk(int m, int j) { return m * (m + 1) / 2 + j; }
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// D += A B on a 32 x 32 x 16 bf16 tile: lane l = 32 g + c supplies A[c][8 g ..]
+// and B[8 g ..][c]; the accumulator holds D[8 (i / 4) + 4 g + i % 4][c] in
+// element i.  Elements 8 j .. 8 j + 7 of an accumulator tile are thus the B
+// operand of a step of 16 of its rows as they stand, if the other operand
+// takes its columns in that order: 16 j + 4 g + {0 .. 3}, 16 j + 8 + 4 g + {0 .. 3}.
+__device__ __forceinline__ f32x16 mfma32(const u16x8& a, const u16x8& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+// The same on fp16.
+//
+// Operands of the state's own products are fp16 in two terms, x = hi + lo to
+// 2^-23 of x (bf16 takes three for that, and half as many instructions again),
+// with a power of two taken out first, which puts the largest value of a
+// column of S, U or Delta, or of a chunk's K, Q or T', between 2^13 and 2^14:
+// no scale of the inputs over- or underflows, k and q (bf16) stay exact to
+// 2^-38 of the chunk's largest, and a column with an infinity spoils no other.
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ f32x16 mfma32h(const u16x8& a, const u16x8& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+struct Pow2 {
+    float x, inv;  // m x in [2^13, 2^14); 1 / x
+};
+__device__ __forceinline__ Pow2 pow2_for(float m) {
+    const int e = max(min((int)(__float_as_uint(m) >> 23), 254), 14);
+    return {__uint_as_float((uint32_t)(267 - e) << 23), __uint_as_float((uint32_t)(e - 13) << 23)};
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
+    return x;
+}
+__device__ __forceinline__ float max4(const float* x) { return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])); }
+// over the two lanes of a column of a 32 x 32 tile
+__device__ __forceinline__ float column_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+struct Half2 {
+    u16x8 h, l;
+};
+// eight consecutive elements times x, as operands
+template <int N>
+__device__ __forceinline__ Half2 split_f16(const float (&v)[N], int at, float x) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = v[at + 2 * i], b = v[at + 2 * i + 1];
+        h[i] = pack_f16(a * x, b * x);
+        const f16x2 t = __builtin_bit_cast(f16x2, h[i]);
+        l[i] = pack_f16(__builtin_fmaf(a, x, -(float)t[0]), __builtin_fmaf(b, x, -(float)t[1]));
+    }
+    return {__builtin_bit_cast(u16x8, u32x4{h[0], h[1], h[2], h[3]}), __builtin_bit_cast(u16x8, u32x4{l[0], l[1], l[2], l[3]})};
+}
+// eight bf16 times x, as fp16
+__device__ __forceinline__ u32x4 bf16_to_f16(const u32x4& v, float x) {
+    u32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = pack_f16(__uint_as_float(v[i] << 16) * x, __uint_as_float(v[i] & 0xFFFF0000u) * x);
+    return y;
+}
+__device__ __forceinline__ float max_abs8(const u32x4& v) {  // of eight bf16
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(v[i] << 16)), fabsf(__uint_as_float(v[i] & 0xFFFF0000u))));
+    return m;
+}
+// Four 16-bit elements of a column: in each group of 16 lanes, lane i points
+// at row i / 4, columns 4 (i % 4) .. of a 4 x 16 block and gets column i.
+__device__ __forceinline__ u16x4 lds_column4(const unsigned short* p) {
+    return __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) s16x4*)const_cast<unsigned short*>(p)));
+}
 
 // A log gate of a zero gate: low enough that every product over it is zero
 // in fp32, finite so that the prefix of the tokens behind it stays exact (it
 // is a compensated pair; their ratios cancel it)
 constexpr float kLogZero = -256.f;
 
-// x = hi + mid + lo, bf16 each, to the last bit of fp32: both remainders are
-// exact (as in split2), so a product with an exact bf16 operand in three
-// instructions keeps fp32's accuracy.  (Two terms leave 2^-18 of each
-// element, 2e-6 of the state on a long sequence where fp32 arithmetic
-// leaves 3e-7.)
-__device__ __forceinline__ void split3_2(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    const bf16x2_t m0 = {(__bf16)-1.f, (__bf16)-0.f}, m1 = {(__bf16)-0.f, (__bf16)-1.f};
-    hi = pack_bf16(a, b);
-    const bf16x2_t h = __builtin_bit_cast(bf16x2_t, hi);
-    const float ra = __builtin_amdgcn_fdot2_f32_bf16(h, m0, a, false), rb = __builtin_amdgcn_fdot2_f32_bf16(h, m1, b, false);
-    mid = pack_bf16(ra, rb);
-    const bf16x2_t m = __builtin_bit_cast(bf16x2_t, mid);
-    lo = pack_bf16(__builtin_amdgcn_fdot2_f32_bf16(m, m0, ra, false), __builtin_amdgcn_fdot2_f32_bf16(m, m1, rb, false));
-}
-struct Split3 {
-    u16x4 h, m, l;
+struct Split2 {
+    u16x8 h, l;
 };
-__device__ __forceinline__ Split3 split3(const f32x4& x) {
-    uint32_t h0, m0, l0, h1, m1, l1;
-    split3_2(x[0], x[1], h0, m0, l0);
-    split3_2(x[2], x[3], h1, m1, l1);
-    return {__builtin_bit_cast(u16x4, uint2{h0, h1}), __builtin_bit_cast(u16x4, uint2{m0, m1}),
-            __builtin_bit_cast(u16x4, uint2{l0, l1})};
-}
-// acc += A B over a 16 x 16 x 16 fp32 block (a: row c16, four consecutive
-// contraction indices; b: an accumulator tile as it stands)
-__device__ __forceinline__ f32x4 blk(const f32x4& a, const f32x4& b, f32x4 acc) {
+template <int N>
+__device__ __forceinline__ Split2 split2_8(const float (&x)[N], int at) {
+    uint32_t h[4], l[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc = mfma_f32(a[q], b[q], acc);
-    return acc;
+    for (int i = 0; i < 4; ++i) split2(x[at + 2 * i], x[at + 2 * i + 1], h[i], l[i]);
+    return {__builtin_bit_cast(u16x8, u32x4{h[0], h[1], h[2], h[3]}), __builtin_bit_cast(u16x8, u32x4{l[0], l[1], l[2], l[3]})};
 }
 
 // Per chunk and value head: the gate rows and T'.  One workgroup of four
-// waves each; K K^T on bf16 MFMA (exact operands), the inverse in fp32.
+// waves each; K K^T on bf16 MFMA (exact operands), the inverse in fp32.  The
+// launch's first `recs` workgroups take the short sequences token by token:
+// they wait for memory and for their own sums, the chunks keep the compute
+// units busy beside them.
 template <int D>
-__global__ __launch_bounds__(kThreads) void k_pk_prep(Pk a) {
+__global__ __launch_bounds__(kThreads, 7) void k_pk_prep(Pk a, unsigned recs) {
     constexpr int LDK = D + 8, PPR = D / 8, KP = C * PPR / kThreads;
     static_assert(C * LDK * 2 <= C * LDA * 4, "K rows fit the tile");
+    using Rec = RecShared<GDN_BF16, kRecLPR, D / 64, kRecR, false>;
+    static_assert(kThreads == kRecThreads && sizeof(Rec) <= C * LDA * 4, "one workgroup serves either");
     __shared__ __attribute__((aligned(16))) float AT[C * LDA];
-    __shared__ __attribute__((aligned(16))) float ghi[C], glo[C], gphi[C], gplo[C], gbeta[C];
+    __shared__ __attribute__((aligned(16))) float ghi[C], glo[C], gphi[C], gplo[C], gbeta[C], mx[3][4];
     const Packed& p = a.p;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g4 = l >> 4, c16 = l & 15;
-    const int place = blockIdx.x / a.Hv, h = blockIdx.x - place * a.Hv, hk = h / a.group;
+    if (blockIdx.x == gridDim.x - 1) {  // one workgroup more: the segments' order
+        order_sequences(a.at, a.order, reinterpret_cast<int*>(AT), tid, kThreads);
+        __syncthreads();
+        count_segments(a.at, a.order, a.seg_shift, kChunkMin, a.first, reinterpret_cast<int*>(AT), tid, kThreads);
+        return;
+    }
+    if (blockIdx.x < recs) {
+        rec_block<GDN_BF16, 0, kRecLPR, D / 64, kRecR>(a, recs, *reinterpret_cast<Rec*>(AT));
+        return;
+    }
+    const unsigned id = blockIdx.x - recs;
+    const int place = id / a.Hv, h = id - place * a.Hv, hk = h / a.group;
     const int64_t s = seq_of_place(a.at, place, 6, l);
     const Span sp = span_of(a.at, s);
     const int64_t c = place - ((sp.begin >> 6) + s);
@@ -435,11 +537,21 @@ __global__ __launch_bounds__(kThreads) void k_pk_prep(Pk a) {
     const int nt = (int)min<int64_t>(C, sp.n - c * C);
     const uint16_t* kin = static_cast<const uint16_t*>(p.k) + hk * D;
     uint16_t* Ks = reinterpret_cast<uint16_t*>(AT);
+    const uint16_t* qin = static_cast<const uint16_t*>(p.q) + hk * D;
     u32x4 kv[KP];
+    float xk = 0.f, xq = 0.f;
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
         const int e = tid + kThreads * i, t = min(e / PPR, nt - 1), c8 = e % PPR;
         kv[i] = ld_g<u32x4>(kin + (t0 + t) * p.k_stride + c8 * 8);
+        xk = fmaxf(xk, max_abs8(kv[i]));
+        xq = fmaxf(xq, max_abs8(ld_g<u32x4>(qin + (t0 + t) * p.q_stride + c8 * 8)));
+    }
+    xk = wave_max(xk);
+    xq = wave_max(xq);
+    if (l == 0) {
+        mx[0][w] = xk;
+        mx[1][w] = xq;
     }
     if (w == 0) {
         const int64_t r = (t0 + min(l, nt - 1)) * p.Hv + h;
@@ -459,14 +571,20 @@ __global__ __launch_bounds__(kThreads) void k_pk_prep(Pk a) {
         *reinterpret_cast<u32x4*>(&Ks[t * LDK + c8 * 8]) = t < nt ? kv[i] : u32x4{0, 0, 0, 0};
     }
     __syncthreads();
+    float* const G = a.G + (int64_t)id * kGate;
     if (w == 0) {
-        float* G = a.G + (int64_t)blockIdx.x * kGate;
-        G[kGgam + l] = __expf(ghi[l] + glo[l]);
-        G[kGgamp + l] = __expf(gphi[l] + gplo[l]);
-        G[kGtail + l] = ratio(ghi[C - 1], glo[C - 1], ghi[l], glo[l]);
+        const Pow2 xk = pow2_for(max4(mx[0])), xq = pow2_for(max4(mx[1]));
+        G[kGgam + l] = p.scale * __expf(ghi[l] + glo[l]) * xq.inv;
+        G[kGgamp + l] = __expf(gphi[l] + gplo[l]) * xk.inv;
+        G[kGtail + l] = ratio(ghi[C - 1], glo[C - 1], ghi[l], glo[l]) * xk.inv;
         G[kGhi + l] = ghi[l];
         G[kGlo + l] = glo[l];
-        if (l < 4) G[kGlast + l] = __expf(ghi[C - 1] + glo[C - 1]);
+        if (l == 0) {
+            G[kGlast] = __expf(ghi[C - 1] + glo[C - 1]);
+            G[kGip] = p.scale * (xk.inv * xq.inv);
+            G[kGxk] = xk.x;
+            G[kGxq] = xq.x;
+        }
     }
     auto krow = [&](int m, int k) { return *reinterpret_cast<const u16x8*>(&Ks[(16 * m + c16) * LDK + 32 * k + 8 * g4]); };
     // Gram blocks (m, n), n <= m, dealt 3, 3, 2, 2 over the waves
@@ -503,417 +621,623 @@ __global__ __launch_bounds__(kThreads) void k_pk_prep(Pk a) {
     }
     __syncthreads();
     ut_inverse_lds(AT, tid);
-    float* T = a.T + (int64_t)blockIdx.x * kTblk;
-    for (int e = tid; e < kTblk / 4; e += kThreads) {
-        const int b = e >> 6, i = (e & 63) >> 2, j4 = 4 * (e & 3);
-        const int m = b >= 6 ? 3 : b >= 3 ? 2 : b >= 1 ? 1 : 0, nb = b - m * (m + 1) / 2;
-        const f32x4 x = *reinterpret_cast<const f32x4*>(&AT[(16 * m + i) * LDA + 16 * nb + j4]) *
-                        *reinterpret_cast<const f32x4*>(&gbeta[16 * nb + j4]);
-        st_g(T + 4 * e, x);
+    // T' = T diag(beta); blocks above the diagonal (the tile holds A there) zero
+    u16x8* T = a.T + (int64_t)id * kTfrag;
+    float x[2][8], m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = tid + kThreads * k;
+        if (e >= 3 * 2 * 64) continue;
+        const int ln = e & 63, st = (e >> 6) & 1, b = e >> 7;
+        const int t = 32 * (b > 0) + (ln & 31), j0 = 32 * (b > 1) + 16 * st + 4 * (ln >> 5);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int j = j0 + 8 * hf;
+            const f32x4 v = *reinterpret_cast<const f32x4*>(&AT[t * LDA + j]) * *reinterpret_cast<const f32x4*>(&gbeta[j]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                x[k][4 * hf + r] = (j >> 4) > (t >> 4) ? 0.f : v[r];
+                m = fmaxf(m, fabsf(x[k][4 * hf + r]));
+            }
+        }
+    }
+    m = wave_max(m);
+    if (l == 0) mx[2][w] = m;
+    __syncthreads();
+    const Pow2 xt = pow2_for(max4(mx[2]));
+    if (tid == 0) G[kGit] = xt.inv;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = tid + kThreads * k;
+        if (e >= 3 * 2 * 64) continue;
+        const Half2 y = split_f16(x[k], 0, xt.x);
+        u16x8* d = T + (e >> 6) * 2 * 64 + (e & 63);
+        st_g(d, y.h);
+        st_g(d + 64, y.l);
     }
 }
 
-// LDS of a segment's workgroup.  K and Q rows are kept with the columns of
-// every 32-column block permuted, 16 h + 4 g + r -> 8 g + 4 h + r, so that the
-// eight key slots of lane group g in the order two accumulator tiles supply
-// them are 16 contiguous bytes.
+// A segment's workgroup in LDS (74 KiB at D = 128 with outputs: two a compute
+// unit).  K and Q rows: 16-byte pieces of eight keys in the operands' order,
+// keys 16 b + 4 g + {0 .. 3} and + 8 in piece 2 b + g, at piece ^ (row mod
+// pieces), so that neither the operands' reads (a row a lane) nor K's columns
+// (lds_column4) meet in a bank.  V and the outputs: a wave's own 32 columns of
+// 64 rows each, V until it is used and then the outputs.
 template <int D, bool OUT>
 struct SegShared {
-    static constexpr int LDK = D + 8;
-    unsigned short K[C * LDK];
-    unsigned short V[C * LDK];
-    u16x8 KtF[D / 16][2][64];  // K^T as A operands: [key tile][32 tokens][lane]
-    f32x4 T[kTblk / 4];
+    unsigned short K[C * D];
+    unsigned short V[C * D];
+    u16x8 T[kTfrag];
     float G[kGate];
-    unsigned short Q[OUT ? C * LDK : 8];
-    u16x8 Pf[OUT ? 4 : 1][2][2][64];  // P as A operands, hi and lo
-    unsigned short O[OUT ? C * LDK : 8];
+    unsigned short Q[OUT ? C * D : 8];
+    u16x8 P[OUT ? kPfrag : 1];
 };
 template <int D>
-constexpr int seg_threads() { return 4 * D; }
+constexpr int seg_threads() { return 2 * D; }
+// x, as if it had just been computed
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+template <int D>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+    return row * D + 8 * (piece ^ (row & (D / 8 - 1)));
+}
 
-// One segment of one value head.  Wave w holds value columns 16 w .. of S^T
+// One segment of one value head.  Wave w holds value columns 32 w .. of S^T
 // for every key (accumulator tiles; they serve as the next product's operand
-// as they stand), so nothing but the staged chunk is shared between waves.
+// as they stand), so nothing but the staged chunk and P crosses waves.
 // OUT: from the segment's start state, with outputs; the last segment writes
-// the end state.  Otherwise the state pass: from zero (segment 0: from the
-// sequence's start state, which it also copies for the output pass, so that
-// the end state may go where the start state was), beside the same columns
-// of M from I (the recurrence with V = 0); end values only.
+// the end state.  Otherwise the state pass, end values only: S from zero
+// (segment 0: from the sequence's start state, which it also copies for the
+// output pass, so that the end state may go where the start state was) or, by
+// a workgroup of its own, M from I (the recurrence with V = 0).
 template <int D, bool OUT>
-__global__ __launch_bounds__(seg_threads<D>(), D == 128 ? 2 : 2) void k_pk_seg(Pk a) {
-    constexpr int NV = OUT ? 1 : 2;  // states a wave carries: S, M
-    constexpr int NW = D / 16, NT = 64 * NW, LDK = SegShared<D, OUT>::LDK;
-    constexpr int KS = D / 32, TPW = D / 16, PPR = D / 8, KP = C * PPR / NT;
-    constexpr int TP = (kTblk / 4 + NT - 1) / NT;
-    static_assert(C * PPR % NT == 0 && kGatePieces <= NT && (2 * TPW) % NW == 0, "staging split");
+__global__ __launch_bounds__(seg_threads<D>(), D == 128 ? 2 : 1) void k_pk_seg(Pk a) {
+    constexpr int NT = seg_threads<D>(), KT = D / 32, PPR = D / 8, KP = C * PPR / NT;
+    constexpr int GP = (kGatePieces + NT - 1) / NT;
+    static_assert(C * PPR % NT == 0, "staging split");
     __shared__ __attribute__((aligned(16))) SegShared<D, OUT> sh;
     const Packed& p = a.p;
-    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g4 = l >> 4, c16 = l & 15;
-    const int place = blockIdx.x / a.Hv, h = blockIdx.x - place * a.Hv, hk = h / a.group;
-    const int64_t s = seq_of_place(a.at, place, a.seg_shift, l);
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g = l >> 5, c = l & 31;
+    const int place_h = OUT ? blockIdx.x : blockIdx.x >> 1;
+    const bool is_m = !OUT && (blockIdx.x & 1);
+    const int i_seg = place_h / a.Hv, h = place_h - i_seg * a.Hv, hk = h / a.group;
+    if (i_seg >= a.first[p.S]) return;
+    const int64_t rank = rank_of_segment(a.first, p.S, i_seg, l), s = a.order[rank];
     const Span sp = span_of(a.at, s);
-    const int64_t base = (sp.begin >> a.seg_shift) + s;  // the sequence's first place
-    const int64_t gi = place - base, ng = (sp.n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
-    if (sp.n < kChunkMin || gi < 0 || gi >= ng || (!OUT && gi == ng - 1)) return;
-    const int64_t per = (int64_t)1 << (a.seg_shift - 6);  // chunks of a segment
+    const int64_t gi = i_seg - a.first[rank], ng = (sp.n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
+    if (!OUT && (gi == ng - 1 || (is_m && gi == 0))) return;
+    const int64_t place = (sp.begin >> a.seg_shift) + s + gi;  // of the segment's states
+    const int64_t per = (int64_t)1 << (a.seg_shift - 6);       // chunks of a segment
     const int64_t i_begin = gi * per, i_end = min<int64_t>((sp.n + C - 1) / C, i_begin + per);
     const int64_t cplace = (sp.begin >> 6) + s;  // the sequence's first chunk place
     const uint16_t* kin = static_cast<const uint16_t*>(p.k) + hk * D;
     const uint16_t* qin = static_cast<const uint16_t*>(p.q) + hk * D;
-    const uint16_t* vin = static_cast<const uint16_t*>(p.v) + h * D;
-    auto in_ws = [&](float* pool, int64_t pl) { return pool + (pl * p.Hv + h) * D * D; };
+    const uint16_t* vin = static_cast<const uint16_t*>(p.v) + h * D + 32 * w;
+    auto in_ws = [&](float* pool) { return pool + (place * p.Hv + h) * D * D; };
+    const int v = 32 * w + c;  // this lane's value column
 
-    const int v = 16 * w + c16;  // this lane's value column
-    f32x4 Sacc[NV][TPW];         // [state][key tile]: rows 16 u + 4 g4 + r of column v
+    // key tile u, element i: key 32 u + 8 (i / 4) + 4 g + i % 4; times a power of
+    // two, 1 / unit (the last update's)
+    float S[KT][16], unit = 1.f;
     {
-        const float* src = OUT && ng > 1 ? in_ws(a.s_start, place) : gi == 0 ? state_from(p, s, h) : nullptr;
+        const float* src = OUT && ng > 1 ? in_ws(a.s_start) : gi == 0 ? state_from(p, s, h) : nullptr;
 #pragma unroll
-        for (int u = 0; u < TPW; ++u) {
-            const int a0 = 16 * u + 4 * g4;
-            Sacc[0][u] = src ? *reinterpret_cast<const f32x4*>(src + (int64_t)v * D + a0) : zero4();
-            if constexpr (!OUT) {
-                if (gi == 0) *reinterpret_cast<f32x4*>(in_ws(a.s_start, place) + (int64_t)v * D + a0) = Sacc[0][u];
+        for (int u = 0; u < KT; ++u)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) Sacc[NV - 1][u][r] = v == a0 + r ? 1.f : 0.f;
+            for (int i = 0; i < 4; ++i) {
+                const int key = 32 * u + 8 * i + 4 * g;
+                f32x4 x = zero4();
+                if (is_m) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[r] = v == key + r ? 1.f : 0.f;
+                } else if (src) {
+                    x = ld_g<f32x4>(src + v * D + key);
+                }
+                if (!OUT && !is_m && gi == 0) st_g(in_ws(a.s_start) + v * D + key, x);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[u][4 * i + r] = x[r];
             }
-        }
     }
 
-    // staging: the next chunk in registers while this one is worked off
-    u32x4 kr[KP], vr[KP], qr[OUT ? KP : 1];
-    f32x4 tr[TP], gr;
-    auto issue = [&](int64_t i, int parts) {  // 1: K, V; 2: Q, T', gate rows
+    // staging: the next chunk's K and Q in registers from the state update on,
+    // its T' and V straight into LDS once this chunk's are used (addresses: a
+    // uniform base and 32 bits a lane)
+    u32x4 kr[KP], qr[OUT ? KP : 1];
+    float xk, xq;
+    f32x4 gr[GP];
+    const int t_st = tid / PPR, pc_st = tid % PPR;  // a thread stages rows t_st + 16 k
+    constexpr int TS = NT / PPR;
+    static_assert(TS == 16, "rows of a staging round keep their place in the swizzle");
+    auto at32 = [](const uint16_t* base, uint32_t off) {
+        return ld_g<u32x4>(reinterpret_cast<const char*>(base) + off);
+    };
+    auto issue = [&](int64_t i) {
         const int64_t t0 = sp.begin + i * C;
         const int nt = (int)min<int64_t>(C, sp.n - i * C);
+        const uint16_t *kc = kin + t0 * p.k_stride, *qc = qin + t0 * p.q_stride;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            const int e = tid + NT * k, t = min(e / PPR, nt - 1), c8 = e % PPR;
-            if (parts & 1) {
-                kr[k] = ld_g<u32x4>(kin + (t0 + t) * p.k_stride + c8 * 8);
-                vr[k] = ld_g<u32x4>(vin + (t0 + t) * p.v_stride + c8 * 8);
-            }
-            if (OUT && (parts & 2)) qr[k] = ld_g<u32x4>(qin + (t0 + t) * p.q_stride + c8 * 8);
+            const uint32_t t = min(t_st + TS * k, nt - 1);
+            kr[k] = at32(kc, t * (uint32_t)(2 * p.k_stride) + 16 * pc_st);
+            if (OUT) qr[k] = at32(qc, t * (uint32_t)(2 * p.q_stride) + 16 * pc_st);
         }
-        if (parts & 2) {
-            const int64_t ch = (cplace + i) * p.Hv + h;
+        const float* gc = a.G + ((cplace + i) * p.Hv + h) * kGate;
+        xk = gc[kGxk];
+        xq = gc[kGxq];
 #pragma unroll
-            for (int k = 0; k < TP; ++k) tr[k] = ld_g<f32x4>(a.T + ch * kTblk + 4 * min(tid + NT * k, kTblk / 4 - 1));
-            gr = ld_g<f32x4>(a.G + ch * kGate + 4 * min(tid, kGatePieces - 1));
+        for (int k = 0; k < GP; ++k) gr[k] = ld_g<f32x4>(gc + 4 * min(tid + NT * k, kGatePieces - 1));
+    };
+    auto to_lds = [](const void* from, void* to) {  // 16 bytes a lane, to `to` (uniform) + 16 l
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
+                                         (__attribute__((address_space(3))) uint32_t*)to, 16, 0, 0);
+    };
+    auto fetch_T = [&](int64_t i) {
+        const u16x8* tc = a.T + ((cplace + i) * p.Hv + h) * kTfrag;
+#pragma unroll
+        for (int k = 0; k < kTfrag / NT; ++k) to_lds(tc + NT * k + tid, &sh.T[NT * k + 64 * w]);
+    };
+    // (rows past the end repeat the last: T' has nothing for them)
+    auto fetch_V = [&](int64_t i) {
+        const int nt = (int)min<int64_t>(C, sp.n - i * C);
+        const uint16_t* vc = vin + (sp.begin + i * C) * p.v_stride;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t t = min((l >> 2) + 16 * k, nt - 1);
+            to_lds(reinterpret_cast<const char*>(vc) + (t * (uint32_t)(2 * p.v_stride) + 16 * (l & 3)),
+                   &sh.V[w * C * 32 + 512 * k]);
         }
     };
     auto store = [&](int64_t i) {
         const int nt = (int)min<int64_t>(C, sp.n - i * C);
         const u32x4 z = u32x4{0, 0, 0, 0};
+        // keys 8 pc .. + 3 and + 4 .. + 7: halves of pieces 2 (pc / 2) and that + 1
+        const int p0 = opaque(piece_at<D>(t_st, pc_st & ~1) + 4 * (pc_st & 1)), p1 = p0 ^ 8;
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
-            const int e = tid + NT * k, t = e / PPR, c8 = e % PPR;
-            const bool ok = t < nt;
-            *reinterpret_cast<u32x4*>(&sh.V[t * LDK + c8 * 8]) = ok ? vr[k] : z;
-            const int p0 = t * LDK + 32 * (c8 >> 2) + 16 * (c8 & 1) + 4 * ((c8 >> 1) & 1);
-            const u32x4 kk = ok ? kr[k] : z;
-            *reinterpret_cast<u32x2*>(&sh.K[p0]) = u32x2{kk[0], kk[1]};
-            *reinterpret_cast<u32x2*>(&sh.K[p0 + 8]) = u32x2{kk[2], kk[3]};
+            const bool ok = t_st + TS * k < nt;
+            const u32x4 x = ok ? bf16_to_f16(kr[k], xk) : z;
+            *reinterpret_cast<u32x2*>(&sh.K[p0 + TS * D * k]) = u32x2{x[0], x[1]};
+            *reinterpret_cast<u32x2*>(&sh.K[p1 + TS * D * k]) = u32x2{x[2], x[3]};
             if (OUT) {
-                const u32x4 qq = ok ? qr[k] : z;
-                *reinterpret_cast<u32x2*>(&sh.Q[p0]) = u32x2{qq[0], qq[1]};
-                *reinterpret_cast<u32x2*>(&sh.Q[p0 + 8]) = u32x2{qq[2], qq[3]};
+                const u32x4 y = ok ? bf16_to_f16(qr[k], xq) : z;
+                *reinterpret_cast<u32x2*>(&sh.Q[p0 + TS * D * k]) = u32x2{y[0], y[1]};
+                *reinterpret_cast<u32x2*>(&sh.Q[p1 + TS * D * k]) = u32x2{y[2], y[3]};
             }
         }
 #pragma unroll
-        for (int k = 0; k < TP; ++k)
-            if (kTblk / 4 % NT == 0 || tid + NT * k < kTblk / 4) sh.T[tid + NT * k] = tr[k];
-        if (tid < kGatePieces) *reinterpret_cast<f32x4*>(&sh.G[4 * tid]) = gr;
+        for (int k = 0; k < GP; ++k)
+            if (tid + NT * k < kGatePieces) *reinterpret_cast<f32x4*>(&sh.G[4 * (tid + NT * k)]) = gr[k];
     };
-    // P blocks (m, c), c <= m, dealt over the waves: rows j of tile c, columns
-    // t of tile m, so that two blocks form an A operand as they stand
-    auto scores = [&]() {
-        for (int bi = w; bi < 10; bi += NW) {
-            const int m = bi >= 6 ? 3 : bi >= 3 ? 2 : bi >= 1 ? 1 : 0, c = bi - m * (m + 1) / 2, t = 16 * m + c16;
-            f32x4 acc = zero4();
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const u16x8 ka = *reinterpret_cast<const u16x8*>(&sh.K[(16 * c + c16) * LDK + 32 * k + 8 * g4]);
-                const u16x8 qb = *reinterpret_cast<const u16x8*>(&sh.Q[t * LDK + 32 * k + 8 * g4]);
-                acc = mfma(ka, qb, acc);
-            }
-            const float th = sh.G[kGhi + t], tl = sh.G[kGlo + t];
-            const f32x4 jh = *reinterpret_cast<const f32x4*>(&sh.G[kGhi + 16 * c + 4 * g4]);
-            const f32x4 jl = *reinterpret_cast<const f32x4*>(&sh.G[kGlo + 16 * c + 4 * g4]);
-            f32x4 pt;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                pt[r] = 16 * c + 4 * g4 + r <= t ? acc[r] * ratio(th, tl, jh[r], jl[r]) : 0.f;
-            u16x4 hi, lo;
-            split4(pt, hi, lo);
-            reinterpret_cast<u16x4*>(&sh.Pf[m][c >> 1][0][l])[c & 1] = hi;
-            reinterpret_cast<u16x4*>(&sh.Pf[m][c >> 1][1][l])[c & 1] = lo;
-        }
+    auto grow = [&](int row, int m, int i) {  // four gate entries of tokens 32 m + 8 i + 4 g ..
+        return *reinterpret_cast<const f32x4*>(&sh.G[row + 32 * m + 8 * i + 4 * g]);
     };
-    if constexpr (OUT) {
-        // the halves of P's operands above the diagonal, never written again
-        if (w == 0) {
-            const u16x4 z = u16x4{0, 0, 0, 0};
-#pragma unroll
-            for (int hl = 0; hl < 2; ++hl) {
-                reinterpret_cast<u16x4*>(&sh.Pf[0][0][hl][l])[1] = z;
-                reinterpret_cast<u16x4*>(&sh.Pf[2][1][hl][l])[1] = z;
-            }
-        }
-    }
-    auto flush = [&](int64_t i) {  // the output tile of chunk i, rows past the end dropped
-        const int64_t t0 = sp.begin + i * C;
-        const int nt = (int)min<int64_t>(C, sp.n - i * C);
-        uint16_t* ob = static_cast<uint16_t*>(p.out) + h * D;
-#pragma unroll
-        for (int k = 0; k < KP; ++k) {
-            const int e = tid + NT * k, t = e / PPR, c8 = e % PPR;
-            if (t < nt)
-                __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(&sh.O[t * LDK + 8 * c8]),
-                                            reinterpret_cast<u32x4*>(ob + (t0 + t) * p.Hv * D + 8 * c8));
-        }
+    unsigned short* const Vw = &sh.V[w * C * 32];
+    // column c of rows 8 i + 4 g .. + 3 of token tile m of the wave's V
+    auto v4 = [&](int m, int i) {
+        return lds_column4(&Vw[(32 * m + 8 * i + 4 * g + (l & 15) / 4) * 32 + 16 * ((l >> 4) & 1) + 4 * (l & 3)]);
     };
-    // an identity operand: lane (column c16) is one where the slot holds key
-    // 16 hh + c16 of the 32-key block
-    auto idfrag = [&](int hh) {
-        u16x8 f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            f[e] = ((e >> 2) == hh && 4 * g4 + (e & 3) == c16) ? (unsigned short)0x3F80 : (unsigned short)0;
-        return f;
+    // LDS places are formed from one base each where they are used (rows and
+    // pieces differ in bits of their own): kept in registers over the loop
+    // they would not leave room for the state
+    // row 32 m + c of K or Q, keys of step b (16 b ..): base ^ 16 b, + 32 D m
+    auto row = [&](const unsigned short* x, int base, int m, int b) {
+        return *reinterpret_cast<const u16x8*>(&x[(base ^ (16 * b)) + 32 * D * m]);
+    };
+    const int row_base = piece_at<D>(c, g);
+    // K^T: keys 32 u + c, tokens of step j of tile m, as an A operand.  A lane
+    // points at row 4 g + (l % 16) / 4 (and that + 8) of the step, four keys:
+    // group l % 4 of 16-key block 2 u + (l / 16) % 2
+    const int kc_base = piece_at<D>(4 * g + (l & 15) / 4, 2 * ((l >> 4) & 1) + (l & 1)) + 4 * ((l & 3) >> 1);
+    auto kcol = [&](int base, int u, int m, int j) {
+        const int at = (base ^ (32 * u)) + (32 * m + 16 * j) * D;
+        const int at8 = ((base ^ (32 * u)) ^ (64 & (D - 1))) + (32 * m + 16 * j + 8) * D;
+        return cat(lds_column4(&sh.K[at]), lds_column4(&sh.K[at8]));
     };
 
-    issue(i_begin, 3);
+    issue(i_begin);
+    fetch_T(i_begin);
+    if (!is_m) fetch_V(i_begin);
     store(i_begin);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     for (int64_t i = i_begin; i < i_end; ++i) {
         __syncthreads();  // chunk i staged
-        const bool more = i + 1 < i_end;
-        if (OUT && more) issue(i + 1, 1);
-        if constexpr (OUT) scores();
-        // K^T as A operands, by exact products with the identity
+        const int rb = opaque(row_base);
+        // scale P^T = K Q^T of the lower blocks, dealt over the waves: rows j,
+        // column t, so that eight elements are P's A operand as they stand
+        if constexpr (OUT) {
+            for (int b = w; b < 3; b += NT / 64) {
+                const int jb = b > 1, tb = b > 0;
+                f32x16 acc = {};
 #pragma unroll
-        for (int jj = 0; jj < 2 * TPW / NW; ++jj) {
-            const int job = w + NW * jj, tp = job & 1, u = job >> 1;
-            u16x4 half[2];
+                for (int k = 0; k < D / 16; ++k) acc = mfma32h(row(sh.K, rb, jb, k), row(sh.Q, rb, tb, k), acc);
+                const int t = 32 * tb + c;
+                const float th = sh.G[kGhi + t], tl = sh.G[kGlo + t], ip = sh.G[kGip];
+                float x[16];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const u16x8 ka = *reinterpret_cast<const u16x8*>(&sh.K[(16 * (2 * tp + q) + c16) * LDK + 32 * (u >> 1) + 8 * g4]);
-                const f32x4 d = mfma(ka, idfrag(u & 1), zero4());
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    const f32x4 jh = grow(kGhi, jb, i4), jl = grow(kGlo, jb, i4);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) half[q][r] = (unsigned short)(__float_as_uint(d[r]) >> 16);
-            }
-            sh.KtF[u][tp][l] = cat(half[0], half[1]);
-        }
-        // X = K S^T, S in three terms; Z = Q S^T, S in two (its error, 2^-18,
-        // is far below the bf16 rounding of the output)
-        f32x4 X[NV][4], Z[OUT ? 4 : 1];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-#pragma unroll
-            for (int n = 0; n < NV; ++n) X[n][m] = zero4();
-            if constexpr (OUT) Z[m] = zero4();
-        }
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            u16x8 bh[NV], bm[NV], bl[NV];
-#pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const Split3 x = split3(Sacc[n][2 * k]), y = split3(Sacc[n][2 * k + 1]);
-                bh[n] = cat(x.h, y.h);
-                bm[n] = cat(x.m, y.m);
-                bl[n] = cat(x.l, y.l);
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const u16x8 ra = *reinterpret_cast<const u16x8*>(&sh.K[(16 * m + c16) * LDK + 32 * k + 8 * g4]);
-#pragma unroll
-                for (int n = 0; n < NV; ++n) {
-                    X[n][m] = mfma(ra, bl[n], X[n][m]);
-                    X[n][m] = mfma(ra, bm[n], X[n][m]);
-                    X[n][m] = mfma(ra, bh[n], X[n][m]);
+                    for (int r = 0; r < 4; ++r)
+                        x[4 * i4 + r] = 32 * jb + 8 * i4 + 4 * g + r <= t ? ip * acc[4 * i4 + r] * ratio(th, tl, jh[r], jl[r]) : 0.f;
                 }
-                if constexpr (OUT) {
-                    const u16x8 qa = *reinterpret_cast<const u16x8*>(&sh.Q[(16 * m + c16) * LDK + 32 * k + 8 * g4]);
-                    Z[m] = mfma(qa, bm[0], Z[m]);
-                    Z[m] = mfma(qa, bh[0], Z[m]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const Split2 y = split2_8(x, 8 * j);
+                    sh.P[(b * 2 + j) * 128 + l] = y.h;
+                    sh.P[(b * 2 + j) * 128 + 64 + l] = y.l;
                 }
             }
         }
-        if (more) issue(i + 1, OUT ? 2 : 3);
-        // U = V - diag(gamma') X
+        __builtin_amdgcn_sched_barrier(0);
+        // X = K S^T
+        float m = 0.f;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4 gp = *reinterpret_cast<const f32x4*>(&sh.G[kGgamp + 16 * m + 4 * g4]);
+        for (int u = 0; u < KT; ++u)
 #pragma unroll
-            for (int n = 0; n < NV; ++n)
+            for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(S[u][e]));
+        const float ms = column_max(m);
+        const Pow2 xs = pow2_for(ms);
+        const float s_inv = xs.inv * unit;
+        f32x16 X[2] = {};
+#pragma unroll
+        for (int b = 0; b < D / 16; ++b) {
+            const Half2 y = split_f16(S[b >> 1], 8 * (b & 1), xs.x);
+            const u16x8 k0 = row(sh.K, rb, 0, b), k1 = row(sh.K, rb, 1, b);
+            X[0] = mfma32h(k0, y.l, X[0]);
+            X[1] = mfma32h(k1, y.l, X[1]);
+            X[0] = mfma32h(k0, y.h, X[0]);
+            X[1] = mfma32h(k1, y.h, X[1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // U = V - diag(gamma') X (V has arrived in LDS)
+        if (OUT) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");  // (all but the last outputs' stores)
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        float mu = 0.f;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+                const f32x4 gp = s_inv * grow(kGgamp, m, i4);
+                u16x4 vv = u16x4{0, 0, 0, 0};
+                if (!is_m) vv = v4(m, i4);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float vv = n == 1 ? 0.f : gdn_bf16_to_f32(sh.V[(16 * m + 4 * g4 + r) * LDK + v]);
-                    X[n][m][r] = vv - gp[r] * X[n][m][r];
-                }
-        }
-        if constexpr (OUT)
-            if (i > i_begin) flush(i - 1);
-        // Delta = T' U in fp32; its two terms for the output, and
-        // diag(gamma_C / gamma) Delta in three for the state
-        u16x4 dh[OUT ? 4 : 1], dl[OUT ? 4 : 1];
-        Split3 db[NV][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            f32x4 d[NV];
-#pragma unroll
-            for (int n = 0; n < NV; ++n) d[n] = zero4();
-#pragma unroll
-            for (int j = 0; j <= m; ++j) {
-                const f32x4 ta = sh.T[tblk(m, j) * 64 + c16 * 4 + g4];
-#pragma unroll
-                for (int n = 0; n < NV; ++n) d[n] = blk(ta, X[n][j], d[n]);
-            }
-            const f32x4 tail = *reinterpret_cast<const f32x4*>(&sh.G[kGtail + 16 * m + 4 * g4]);
-            if constexpr (OUT) split4(d[0], dh[m], dl[m]);
-#pragma unroll
-            for (int n = 0; n < NV; ++n) db[n][m] = split3(tail * d[n]);
-        }
-        __syncthreads();  // the operands of K^T and P are whole
-        const float gC = sh.G[kGlast];
-#pragma unroll
-        for (int u = 0; u < TPW; ++u) {
-            f32x4 acc[NV];
-#pragma unroll
-            for (int n = 0; n < NV; ++n) acc[n] = gC * Sacc[n][u];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const u16x8 ka = sh.KtF[u][k][l];
-#pragma unroll
-                for (int n = 0; n < NV; ++n) {
-                    acc[n] = mfma(ka, cat(db[n][2 * k].l, db[n][2 * k + 1].l), acc[n]);
-                    acc[n] = mfma(ka, cat(db[n][2 * k].m, db[n][2 * k + 1].m), acc[n]);
-                    acc[n] = mfma(ka, cat(db[n][2 * k].h, db[n][2 * k + 1].h), acc[n]);
+                    X[m][4 * i4 + r] = gdn_bf16_to_f32(vv[r]) - gp[r] * X[m][4 * i4 + r];
+                    mu = fmaxf(mu, fabsf(X[m][4 * i4 + r]));
                 }
             }
+        const Pow2 xu = pow2_for(column_max(mu));
+        __builtin_amdgcn_sched_barrier(0);
+        // Delta = T' U
+        f32x16 dl[2] = {};
 #pragma unroll
-            for (int n = 0; n < NV; ++n) Sacc[n][u] = acc[n];
+        for (int jb = 0; jb < 2; ++jb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = X[jb][8 * j + e];
+                const Half2 y = split_f16(u, 0, xu.x);
+                u16x8 th[2], tl[2];
+#pragma unroll
+                for (int tb = jb; tb < 2; ++tb) {
+                    const u16x8* ta = &sh.T[((tb + jb) * 2 + j) * 128 + l];
+                    th[tb] = ta[0], tl[tb] = ta[64];
+                }
+#pragma unroll
+                for (int tb = jb; tb < 2; ++tb) dl[tb] = mfma32h(tl[tb], y.h, dl[tb]);
+#pragma unroll
+                for (int tb = jb; tb < 2; ++tb) dl[tb] = mfma32h(th[tb], y.l, dl[tb]);
+#pragma unroll
+                for (int tb = jb; tb < 2; ++tb) dl[tb] = mfma32h(th[tb], y.h, dl[tb]);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        const float unscale = xu.inv * sh.G[kGit];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) dl[m][e] *= unscale;
+        const bool more = i + 1 < i_end;
+        __syncthreads();  // T' is used, P whole
+        if (more) fetch_T(i + 1);
+        if constexpr (OUT) {
+            // O = diag(scale gamma) Q S^T + scale P Delta, P and Delta in two bf16
+            // terms, rounded once to bf16, over V (S is split again: X's phase has
+            // no registers for Q S^T)
+            f32x16 Z[2] = {};
+            const int qb = opaque(row_base);
+#pragma unroll
+            for (int b = 0; b < D / 16; ++b) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(S[b >> 1][8 * (b & 1) + e]));  // (not X's terms, kept)
+                const Half2 y = split_f16(S[b >> 1], 8 * (b & 1), xs.x);
+                const u16x8 q0 = row(sh.Q, qb, 0, b), q1 = row(sh.Q, qb, 1, b);
+                Z[0] = mfma32h(q0, y.l, Z[0]);
+                Z[1] = mfma32h(q1, y.l, Z[1]);
+                Z[0] = mfma32h(q0, y.h, Z[0]);
+                Z[1] = mfma32h(q1, y.h, Z[1]);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    const f32x4 gam = s_inv * grow(kGgam, m, i4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) Z[m][4 * i4 + r] *= gam[r];
+                }
+#pragma unroll
+            for (int jb = 0; jb < 2; ++jb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = dl[jb][8 * j + e];
+                    const Split2 y = split2_8(x, 0);
+                    u16x8 ph[2], pl[2];
+#pragma unroll
+                    for (int m = jb; m < 2; ++m) {
+                        const u16x8* pa = &sh.P[((m + jb) * 2 + j) * 128 + l];
+                        ph[m] = pa[0], pl[m] = pa[64];
+                    }
+#pragma unroll
+                    for (int m = jb; m < 2; ++m) Z[m] = mfma32(pl[m], y.h, Z[m]);
+#pragma unroll
+                    for (int m = jb; m < 2; ++m) Z[m] = mfma32(ph[m], y.l, Z[m]);
+#pragma unroll
+                    for (int m = jb; m < 2; ++m) Z[m] = mfma32(ph[m], y.h, Z[m]);
+                }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i2 = 0; i2 < 8; ++i2) {
+                    const uint32_t y = pack_bf16(Z[m][2 * i2], Z[m][2 * i2 + 1]);
+                    const int t = 32 * m + 8 * (i2 >> 1) + 4 * g + 2 * (i2 & 1);
+                    Vw[t * 32 + c] = (unsigned short)y;
+                    Vw[(t + 1) * 32 + c] = (unsigned short)(y >> 16);
+                }
         }
-        // O = scale (diag(gamma) Z + P Delta), rounded once to bf16
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) issue(i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        // S^T <- gamma_C S^T + K^T diag(gamma_C / gamma) Delta, summed in the scale
+        // of the larger of the two (the decayed state, not the one before it: a
+        // small Delta behind a strong decay keeps its bits)
+        float md = 0.f;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+                const f32x4 tail = grow(kGtail, m, i4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    dl[m][4 * i4 + r] *= tail[r];
+                    md = fmaxf(md, fabsf(dl[m][4 * i4 + r]));
+                }
+            }
+        const float g_unit = sh.G[kGlast] * unit;
+        const Pow2 xd = pow2_for(fmaxf(column_max(md), ms * g_unit));
+        const float gC = ms > 0.f ? g_unit * xd.x : 0.f;  // (a zero state leaves the scale anywhere)
+        unit = xd.inv;
+        const int kb = opaque(kc_base);
+        f32x16 acc[KT];
+#pragma unroll
+        for (int u = 0; u < KT; ++u)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[u][e] = gC * S[u][e];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = dl[m][8 * j + e];
+                const Half2 y = split_f16(x, 0, xd.x);
+#pragma unroll
+                for (int u = 0; u < KT; u += 2) {
+                    const u16x8 k0 = kcol(kb, u, m, j), k1 = kcol(kb, u + 1, m, j);
+                    acc[u] = mfma32h(k0, y.l, acc[u]);
+                    acc[u + 1] = mfma32h(k1, y.l, acc[u + 1]);
+                    acc[u] = mfma32h(k0, y.h, acc[u]);
+                    acc[u + 1] = mfma32h(k1, y.h, acc[u + 1]);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < KT; ++u)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) S[u][e] = acc[u][e];
+        // T' has arrived in LDS (and the rows in registers); waited for in front of
+        // the output's stores, which the counter counts too
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // the wave's columns of the output tile, rows past the end dropped; the
+        // next V takes their place in LDS, asked for before the stores
+        u32x4 o[OUT ? 4 : 1];
         if constexpr (OUT) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 o = zero4();
+            for (int k = 0; k < 4; ++k) o[k] = *reinterpret_cast<const u32x4*>(&Vw[8 * (l + 64 * k)]);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        if (more && !is_m) fetch_V(i + 1);
+        if constexpr (OUT) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int nt = (int)min<int64_t>(C, sp.n - i * C);
+            uint16_t* ob = static_cast<uint16_t*>(p.out) + (sp.begin + i * C) * p.Hv * D + h * D + 32 * w;
 #pragma unroll
-                for (int k = 0; k <= (m >> 1); ++k) {
-                    const u16x8 ph = sh.Pf[m][k][0][l], pl = sh.Pf[m][k][1][l];
-                    const u16x8 xh = cat(dh[2 * k], dh[2 * k + 1]), xl = cat(dl[2 * k], dl[2 * k + 1]);
-                    o = mfma(pl, xh, o);
-                    o = mfma(ph, xl, o);
-                    o = mfma(ph, xh, o);
-                }
-                const f32x4 gam = *reinterpret_cast<const f32x4*>(&sh.G[kGgam + 16 * m + 4 * g4]);
-                const f32x4 y = p.scale * (gam * Z[m] + o);
-                const uint32_t y01 = pack_bf16(y[0], y[1]), y23 = pack_bf16(y[2], y[3]);
-                sh.O[(16 * m + 4 * g4 + 0) * LDK + v] = (unsigned short)y01;
-                sh.O[(16 * m + 4 * g4 + 1) * LDK + v] = (unsigned short)(y01 >> 16);
-                sh.O[(16 * m + 4 * g4 + 2) * LDK + v] = (unsigned short)y23;
-                sh.O[(16 * m + 4 * g4 + 3) * LDK + v] = (unsigned short)(y23 >> 16);
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t t = (l >> 2) + 16 * k;
+                if ((int)t < nt)
+                    __builtin_nontemporal_store(o[k], reinterpret_cast<u32x4*>(reinterpret_cast<char*>(ob) +
+                                                                               (t * (uint32_t)(2 * D * a.Hv) + 16 * (l & 3))));
             }
         }
-        __syncthreads();  // chunk i is worked off, its output tile whole
+        __syncthreads();  // chunk i is worked off
         if (more) store(i + 1);
     }
-    if constexpr (OUT) {
-        flush(i_end - 1);
-        float* dst = gi == ng - 1 ? state_to(p, s, h) : nullptr;
-        if (dst) {
 #pragma unroll
-            for (int u = 0; u < TPW; ++u)
-                *reinterpret_cast<f32x4*>(dst + (int64_t)v * D + 16 * u + 4 * g4) = Sacc[0][u];
+    for (int u = 0; u < KT; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[u][e] *= unit;
+    float* dst = OUT ? (gi == ng - 1 ? state_to(p, s, h) : nullptr) : is_m ? nullptr : in_ws(a.s_end);
+    float* mt = is_m ? in_ws(a.m_end) : nullptr;  // M^T: row key (of the end state), column v
+#pragma unroll
+    for (int u = 0; u < KT; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = 32 * u + 8 * i + 4 * g;
+            if (dst) st_g(dst + v * D + key, f32x4{S[u][4 * i], S[u][4 * i + 1], S[u][4 * i + 2], S[u][4 * i + 3]});
+            if (mt) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) mt[(key + r) * D + v] = S[u][4 * i + r];
+            }
         }
-    } else {
-        float* dst = in_ws(a.s_end, place);
-        float* mt = in_ws(a.m_end, place);  // M^T: row key (of the end state), column v
-#pragma unroll
-        for (int u = 0; u < TPW; ++u) {
-            *reinterpret_cast<f32x4*>(dst + (int64_t)v * D + 16 * u + 4 * g4) = Sacc[0][u];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) mt[(16 * u + 4 * g4 + r) * D + v] = Sacc[NV - 1][u][r];
-        }
-    }
 }
 
-// Start states of a sequence's segments: X <- S_end(g) + X M(g), sixteen rows
-// of one head a workgroup (rows are independent), wave w the columns 16 w ..;
-// fp32 MFMA, the next three matrices in flight while one multiplies.
-template <int D>
+// Start states of a sequence's segments: X(g + 1) = S_end(g) + X(g) M(g), from
+// X(1) = S_end(0).  The maps compose, so a long chain runs as a two-level scan
+// (about 3 sqrt of the steps): blocks of 2^kChainShift maps side by side into
+// one map each (kCompose: P = M(a) ... M(e - 1) and the addend Q), the blocks'
+// start states one after the other (kBlocks), and every block's own from its
+// start (kExpand, which alone does the whole of a short chain).
+// Sixteen rows of one head a workgroup (rows are independent), wave w the
+// columns 16 w ..; fp32 MFMA, the next three matrices in flight while one
+// multiplies (a step takes 2.4 us: 64 KiB into the compute unit, then LDS
+// exchange and products one behind the other).
+constexpr int kChainShift = 3, kChainLong = 16;  // maps a block; the fewest that go two-level
+enum { kCompose, kBlocks, kExpand };
+template <int D, int MODE, int R>
 __global__ __launch_bounds__(4 * D, 2) void k_pk_chain(Pk a) {
     constexpr int NB = D / 16, LDX = D + 4;
-    __shared__ __attribute__((aligned(16))) float X[2][16 * LDX];
+    constexpr int TILES = NB / R, WGS = MODE == kCompose ? 2 * TILES : TILES;  // row tiles of Q (and P)
+    __shared__ __attribute__((aligned(16))) float X[2][16 * R * LDX];
     const Packed& p = a.p;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g4 = l >> 4, c16 = l & 15;
-    const int rt = blockIdx.x % NB;
-    const int sh_id = blockIdx.x / NB, s = sh_id / a.Hv, h = sh_id - s * a.Hv;
+    // workgroups go to the eight XCDs in turn: those that read the same
+    // matrices share one and its L2
+    const int j = blockIdx.x / 8, tile = j % WGS, id = (j / WGS) * 8 + blockIdx.x % 8;
+    const int rt = tile % TILES * R;
+    const bool is_p = MODE == kCompose && tile >= TILES;
+    const int64_t bshift = a.seg_shift + kChainShift;
+    const int64_t units = MODE == kBlocks ? p.S : (p.N >> bshift) + p.S;
+    const int place = id / a.Hv, h = id - place * a.Hv;
+    if (place >= units) return;
+    const int64_t s = MODE == kBlocks ? place : seq_of_place(a.at, place, (int)bshift, l);
     const Span sp = span_of(a.at, s);
     const int64_t ng = (sp.n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
     if (sp.n < kChunkMin || ng < 2) return;
-    const int64_t base = (sp.begin >> a.seg_shift) + s;
+    const int64_t base = (sp.begin >> a.seg_shift) + s, bbase = (sp.begin >> bshift) + s;
+    const bool two = a.two_level && ng - 2 >= kChainLong;
+    const int64_t nblk = two ? (ng - 2 + (1 << kChainShift) - 1) >> kChainShift : 1;
+    const int64_t blk = MODE == kBlocks ? 0 : place - bbase;
+    if (blk < 0 || blk >= nblk || (MODE != kExpand && !two)) return;
     auto at = [&](float* pool, int64_t g) { return pool + ((base + g) * p.Hv + h) * D * D; };
-    // rows 4 g4 + r of the sixteen, column 16 w + c16
-    const int col = 16 * w + c16;
+    auto at_blk = [&](float* pool, int64_t b) { return pool + ((bbase + b) * p.Hv + h) * D * D; };
+    // steps g0 .. g1 - 1: maps, or blocks of them
+    const int64_t g0 = MODE == kBlocks ? 0 : 1 + (blk << kChainShift);
+    const int64_t g1 = MODE == kBlocks ? nblk - 1 : two ? min(ng - 1, g0 + (1 << kChainShift)) : ng - 1;
+    const int col = 16 * w + c16;  // rows 4 g4 + r of the sixteen
+    struct Rows {
+        f32x4 t[R];
+    };
     auto rows = [&](const float* m) {
-        f32x4 x;
+        Rows x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = m[(int64_t)(16 * rt + 4 * g4 + r) * D + col];
+        for (int t = 0; t < R; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x.t[t][r] = m[(16 * (rt + t) + 4 * g4 + r) * D + col];
         return x;
     };
-    f32x4 x = rows(at(a.s_end, 0));
-    struct In {
-        f32x4 m[NB], add;
+    auto put = [&](float* m, const Rows& x) {
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m[(16 * (rt + t) + 4 * g4 + r) * D + col] = x.t[t][r];
     };
+    constexpr int AHEAD = 4 - R;
+    struct In {
+        f32x4 m[NB];
+        Rows add;
+    };
+    const int64_t first = MODE == kCompose ? g0 + 1 : g0;  // (the first map of a block is where P and Q start)
+    // (in program order, so that a step waits for its own matrix alone)
     auto fetch = [&](In& in, int64_t g) {
-        g = min(g, ng - 1 > 1 ? ng - 2 : (int64_t)0);
-        const float* m = at(a.m_end, g) + (int64_t)col * D;
+        g = max(min(g, g1 - 1), first);
+        const float* m = (MODE == kBlocks ? at_blk(a.p_blk, g) : at(a.m_end, g)) + col * D;
 #pragma unroll
         for (int k = 0; k < NB; ++k) in.m[k] = ld_g<f32x4>(m + 16 * k + 4 * g4);
-        in.add = rows(at(a.s_end, g));
-    };
-    // step g: the start state of segment g, then X M(g) + S_end(g)
-    auto step = [&](int64_t g, const In& in) {
-        float* dst = at(a.s_start, g);
+        if (!is_p) in.add = rows(MODE == kBlocks ? at_blk(a.q_blk, g) : at(a.s_end, g));
+        else
 #pragma unroll
-        for (int r = 0; r < 4; ++r) dst[(int64_t)(16 * rt + 4 * g4 + r) * D + col] = x[r];
+            for (int t = 0; t < R; ++t) in.add.t[t] = zero4();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    Rows x;
+    if (MODE == kCompose) {
+        if (!is_p) x = rows(at(a.s_end, g0));
+        else
+#pragma unroll
+            for (int t = 0; t < R; ++t) x.t[t] = ld_g<f32x4>(at(a.m_end, g0) + col * D + 16 * (rt + t) + 4 * g4);
+    } else {
+        x = MODE == kExpand && blk > 0 ? rows(at(a.s_start, g0)) : rows(at(a.s_end, 0));
+        if (MODE == kExpand && blk == 0) put(at(a.s_start, 1), x);
+    }
+    auto step = [&](int64_t g, const In& in) {
         float* Xs = X[g & 1];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) Xs[(4 * g4 + r) * LDX + col] = x[r];
+        for (int t = 0; t < R; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) Xs[(16 * t + 4 * g4 + r) * LDX + col] = x.t[t][r];
         __syncthreads();
-        f32x4 acc = in.add, acc2 = zero4();
+        Rows y;
 #pragma unroll
-        for (int k = 0; k < NB; k += 2) {
-            acc = blk(*reinterpret_cast<const f32x4*>(&Xs[c16 * LDX + 16 * k + 4 * g4]), in.m[k], acc);
-            acc2 = blk(*reinterpret_cast<const f32x4*>(&Xs[c16 * LDX + 16 * (k + 1) + 4 * g4]), in.m[k + 1], acc2);
+        for (int t = 0; t < R; ++t) {
+            f32x4 xa[NB], acc[4] = {in.add.t[t], zero4(), zero4(), zero4()};
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+                xa[k] = *reinterpret_cast<const f32x4*>(&Xs[(16 * t + c16) * LDX + 16 * k + 4 * g4]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < NB; k += 4)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = mfma_f32(xa[k + e][q], in.m[k + e][q], acc[e]);
+            y.t[t] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         }
-        x = acc + acc2;
+        if (g < g1) {
+            x = y;
+            // (the start of the next segment; of the next block's first)
+            if (MODE == kExpand && (g + 1 < g1 || blk == nblk - 1)) put(at(a.s_start, g + 1), x);
+            if (MODE == kBlocks) put(at(a.s_start, 1 + ((g + 1) << kChainShift)), x);
+        }
     };
-    if (ng > 2) {
-        // four matrices in flight (each step fetches the one three steps on)
-        In in[4];
-        fetch(in[0], 1);
-        fetch(in[1], 2);
-        fetch(in[2], 3);
-        for (int64_t g = 1; g < ng - 1; g += 4) {
+    if (first < g1) {
+        In in[AHEAD + 1];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (g + u >= ng - 1) break;
-                fetch(in[(u + 3) & 3], g + u + 3);
+        for (int u = 0; u < AHEAD; ++u) fetch(in[u], first + u);
+        for (int64_t g = first; g < g1; g += AHEAD + 1) {
+#pragma unroll
+            for (int u = 0; u <= AHEAD; ++u) {
+                fetch(in[(u + AHEAD) % (AHEAD + 1)], g + u + AHEAD);
                 step(g + u, in[u]);
             }
         }
     }
-    float* dst = at(a.s_start, ng - 1);
+    if (MODE == kCompose) {
+        if (!is_p) put(at_blk(a.q_blk, blk), x);
+        else
 #pragma unroll
-    for (int r = 0; r < 4; ++r) dst[(int64_t)(16 * rt + 4 * g4 + r) * D + col] = x[r];
+            for (int t = 0; t < R; ++t) st_g(at_blk(a.p_blk, blk) + col * D + 16 * (rt + t) + 4 * g4, x.t[t]);
+    }
 }
 
-// Tokens of a segment, as a power of two: as many segments as fill the
-// compute units once over all heads, at least kSegMin chunks each.
-constexpr int kSegMinShift = 6 + 3;
+// Tokens of a segment, as a power of two: as many segments as there are
+// compute units over all heads, at least four chunks each.  Twice as many run
+// the output pass two workgroups a compute unit (one of 65531 tokens, 4 heads:
+// outputs 116 instead of 149 us), but have twice the matrices to multiply
+// through the chain (153 instead of 101 us); mixed batch of 16384, 16 heads:
+// state pass, chain and outputs 105, 56, 144 instead of 80, 30, 158 us.
+constexpr int kSegMinShift = 6 + 2;
 constexpr int kWhole = 31;  // a sequence's tokens are fewer than 2^31
 int seg_shift_for(const Packed& p) {
     const int64_t want = std::max<int64_t>(1, p.N * p.Hv / 256);  // tokens a workgroup
@@ -923,12 +1247,15 @@ int seg_shift_for(const Packed& p) {
 }
 int64_t longest(const Packed& p) { return std::min(p.N, p.max_len); }
 
+// whether a sequence may have a chain that is worth two levels
+bool two_level(const Packed& p, int shift) { return longest(p) > (int64_t)(kChainLong + 1) << shift; }
+
 struct PkLayout {
-    size_t T, G, s_end, m_end, s_start, total;
+    size_t T, G, order, first, s_end, m_end, s_start, q_blk, p_blk, total;
 };
 PkLayout layout(const Packed& p) {
     PkLayout L{};
-    if (!packed_chunked(p) || longest(p) < kChunkMin) return L;
+    if (!packed_in_chunks(p)) return L;
     const size_t chunks = (size_t)(p.N / C + p.S) * (size_t)p.Hv;
     size_t off = 0;
     auto take = [&](size_t floats) {
@@ -936,14 +1263,21 @@ PkLayout layout(const Packed& p) {
         off += align256(floats * sizeof(float));
         return at;
     };
-    L.T = take(chunks * kTblk);
+    L.T = take(chunks * kTfrag * 4);
     L.G = take(chunks * kGate);
+    L.order = take((size_t)p.S);
+    L.first = take((size_t)p.S + 1);
     const int sh = seg_shift_for(p);
     if (longest(p) > ((int64_t)1 << sh)) {
         const size_t states = (size_t)((p.N >> sh) + p.S) * (size_t)p.Hv * (size_t)(p.dk * p.dk);
         L.s_end = take(states);
         L.m_end = take(states);
         L.s_start = take(states);
+        if (two_level(p, sh)) {
+            const size_t blocks = (size_t)((p.N >> (sh + kChainShift)) + p.S) * (size_t)p.Hv * (size_t)(p.dk * p.dk);
+            L.q_blk = take(blocks);
+            L.p_blk = take(blocks);
+        }
     }
     L.total = off;
     return L;
@@ -953,18 +1287,28 @@ template <int D>
 hipError_t launch_chunks(const Pk& a, bool segments, hipStream_t st) {
     const Packed& p = a.p;
     prof_begin(p.timer, "k_pk_prep", st);
-    hipLaunchKernelGGL(k_pk_prep<D>, dim3((unsigned)(a.nslot * p.Hv)), dim3(kThreads), 0, st, a);
+    const unsigned recs = (unsigned)(p.S * p.Hv * (D / RecShared<GDN_BF16, kRecLPR, D / 64, kRecR, false>::RB));
+    hipLaunchKernelGGL(k_pk_prep<D>, dim3(recs + (unsigned)(a.nslot * p.Hv) + 1), dim3(kThreads), 0, st, a, recs);
     prof_end(p.timer, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(a.nseg * p.Hv)), block(seg_threads<D>());
+    const dim3 grid((unsigned)(a.nseg * p.Hv)), states((unsigned)(2 * a.nseg * p.Hv)), block(seg_threads<D>());
     if (segments) {
         prof_begin(p.timer, "k_pk_state", st);
-        hipLaunchKernelGGL((k_pk_seg<D, false>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((k_pk_seg<D, false>), states, block, 0, st, a);
         prof_end(p.timer, st);
         if ((e = hipGetLastError()) != hipSuccess) return e;
+        // eight workgroup-sets at a time, for the eight XCDs
+        const int64_t blocks = ((p.N >> (a.seg_shift + kChainShift)) + p.S) * p.Hv;
+        auto sets = [](int64_t n, int per) { return dim3((unsigned)((n + 7) / 8 * 8 * per)); };
         prof_begin(p.timer, "k_pk_chain", st);
-        hipLaunchKernelGGL(k_pk_chain<D>, dim3((unsigned)(p.S * p.Hv * (D / 16))), dim3(4 * D), 0, st, a);
+        if (a.two_level) {
+            hipLaunchKernelGGL((k_pk_chain<D, kCompose, 2>), sets(blocks, D / 16), dim3(4 * D), 0, st, a);
+            hipLaunchKernelGGL((k_pk_chain<D, kBlocks, 1>), sets(p.S * p.Hv, D / 16), dim3(4 * D), 0, st, a);
+            hipLaunchKernelGGL((k_pk_chain<D, kExpand, 2>), sets(blocks, D / 32), dim3(4 * D), 0, st, a);
+        } else {
+            hipLaunchKernelGGL((k_pk_chain<D, kExpand, 1>), sets(blocks, D / 16), dim3(4 * D), 0, st, a);
+        }
         prof_end(p.timer, st);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
@@ -980,6 +1324,8 @@ bool packed_chunked(const Packed& p) {
     return p.dtype == GDN_BF16 && p.gate == GDN_GATE_SCALAR && p.dk == p.dv && (p.dk == 64 || p.dk == 128);
 }
 
+bool packed_in_chunks(const Packed& p) { return packed_chunked(p) && longest(p) >= kChunkMin; }
+
 size_t packed_workspace(const Packed& p) { return layout(p).total; }
 
 hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st) {
@@ -991,14 +1337,16 @@ hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st) {
     const PkLayout L = layout(p);
     const bool chunks = L.total > 0;
     a.rec_below = chunks ? kChunkMin : INT32_MAX;
-    prof_begin(p.timer, "k_pk_rec", st);
-    hipError_t e;
-    if (p.dtype == GDN_BF16)
-        e = p.gate == GDN_GATE_CHANNEL ? launch_rec_shape<GDN_BF16, 1>(a, st) : launch_rec_shape<GDN_BF16, 0>(a, st);
-    else
-        e = p.gate == GDN_GATE_CHANNEL ? launch_rec_shape<GDN_F32, 1>(a, st) : launch_rec_shape<GDN_F32, 0>(a, st);
-    prof_end(p.timer, st);
-    if (e != hipSuccess || !chunks) return e;
+    if (!chunks) {
+        prof_begin(p.timer, "k_pk_rec", st);
+        hipError_t e;
+        if (p.dtype == GDN_BF16)
+            e = p.gate == GDN_GATE_CHANNEL ? launch_rec_shape<GDN_BF16, 1>(a, st) : launch_rec_shape<GDN_BF16, 0>(a, st);
+        else
+            e = p.gate == GDN_GATE_CHANNEL ? launch_rec_shape<GDN_F32, 1>(a, st) : launch_rec_shape<GDN_F32, 0>(a, st);
+        prof_end(p.timer, st);
+        return e;
+    }
     char* base = static_cast<char*>(ws);
     // without segments every sequence is one, whatever its length (max_len
     // is the caller's word, the lengths are the device's)
@@ -1006,11 +1354,16 @@ hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st) {
     a.seg_shift = segments ? seg_shift_for(p) : kWhole;
     a.nslot = p.N / C + p.S;
     a.nseg = (p.N >> a.seg_shift) + p.S;
-    a.T = reinterpret_cast<float*>(base + L.T);
+    a.T = reinterpret_cast<u16x8*>(base + L.T);
+    a.order = reinterpret_cast<int32_t*>(base + L.order);
+    a.first = reinterpret_cast<int32_t*>(base + L.first);
     a.G = reinterpret_cast<float*>(base + L.G);
     a.s_end = reinterpret_cast<float*>(base + L.s_end);
     a.m_end = reinterpret_cast<float*>(base + L.m_end);
     a.s_start = reinterpret_cast<float*>(base + L.s_start);
+    a.two_level = segments && two_level(p, a.seg_shift);
+    a.q_blk = reinterpret_cast<float*>(base + L.q_blk);
+    a.p_blk = reinterpret_cast<float*>(base + L.p_blk);
     return p.dk == 64 ? launch_chunks<64>(a, segments, st) : launch_chunks<128>(a, segments, st);
 }
 

@@ -80,6 +80,49 @@ __device__ __forceinline__ void order_sequences(const Offsets& p, int32_t* order
     for (int64_t s = tid; s < p.S; s += threads)
         order[atomicAdd(&hist[kLenClasses + len_class(span_of(p, s).n)], 1)] = (int32_t)s;
 }
+// Segments of 2^shift tokens of sequences of at least min_len tokens, counted
+// over the sequences in that order: first[r] those before rank r, first[S] all
+// of them.  By the workgroup that ordered them; sums: `threads` ints of LDS.
+__device__ __forceinline__ void count_segments(const Offsets& p, const int32_t* order, int shift, int64_t min_len,
+                                               int32_t* first, int* sums, int tid, int threads) {
+    const int64_t run = (p.S + threads - 1) / threads, r0 = tid * run, r1 = min(r0 + run, p.S);
+    auto segments = [&](int64_t r) {
+        const int64_t n = span_of(p, order[r]).n;
+        return n < min_len ? 0 : (int)((n + ((int64_t)1 << shift) - 1) >> shift);
+    };
+    int mine = 0;
+    for (int64_t r = r0; r < r1; ++r) mine += segments(r);
+    sums[tid] = mine;
+    __syncthreads();
+    if (tid == 0) {
+        int at = 0;
+        for (int i = 0; i < threads; ++i) {
+            const int x = sums[i];
+            sums[i] = at;
+            at += x;
+        }
+        first[p.S] = at;
+    }
+    __syncthreads();
+    int at = sums[tid];
+    for (int64_t r = r0; r < r1; ++r) {
+        first[r] = at;
+        at += segments(r);
+    }
+}
+// The rank whose segments hold the i-th (i < first[S]), by a whole wave.
+__device__ __forceinline__ int64_t rank_of_segment(const int32_t* first, int64_t S, int i, int lane) {
+    int64_t lo = 0, cnt = S;
+    while (cnt > 1) {
+        const int64_t step = (cnt + 63) >> 6;
+        const bool le = lane * step < cnt && first[lo + lane * step] <= i;
+        const int hits = (int)__popcll(__ballot(le));
+        const int64_t k = hits > 0 ? hits - 1 : 0;
+        lo += k * step;
+        cnt = min(step, cnt - k * step);
+    }
+    return lo;
+}
 
 }  // namespace
 }  // namespace gdn

@@ -332,15 +332,19 @@ int gdn_seqpar_fwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv,
  * the other tokens of its chunk (64), nothing of other sequences or heads.
  * An empty sequence copies its start state.  Values of cu_seqlens out of
  * order or range are clamped, so they never lead out of the buffers.
- * Sequences of 64 tokens or more run in chunks on the matrix cores for
+ * Sequences of 32 tokens or more run in chunks on the matrix cores for
  * bf16, scalar gates, dk = dv in {64, 128} (gdn_packed_path); everything
- * else runs token by token.  Both hold states and sums in fp32.  No call
+ * else runs token by token.  Both hold states and sums in fp32; in chunks,
+ * q and k are exact to 2^-38 of the largest of their chunk and head, states
+ * and values to that of the largest of their value feature in it.  No call
  * synchronises; all of them can be captured into a graph.
  * Alignment: q, k, v, out, the pools, a channel alpha and the workspace on
  * 16 bytes, token strides multiples of 16 bytes; the rest on 4; else
  * GDN_E_ARG.  dk, dv as for gdn_chunk_fwd.  GDN_E_SHAPE: negative sizes, Hv
- * not a multiple of Hk, strides shorter than a row, a pool without indices
- * smaller than S, N or S of 2^31 or more, (N / 64 + S) Hv of 2^27 or more.
+ * not a multiple of Hk, strides shorter than a row or over 2^23, a pool
+ * without indices smaller than S, N or S of 2^31 or more, S Hv over 2^21; for
+ * calls with chunk kernels (max_len and N of 32 or more) also S Hv over 2^19
+ * or N Hv over 2^28.
  */
 int gdn_packed_fwd(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
                    int64_t n_in, int64_t n_out, int64_t max_len, int32_t dtype, int32_t gate, int32_t order,

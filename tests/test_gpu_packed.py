@@ -91,6 +91,9 @@ CASES = [
     Packed((512, 511, 1537), 2, 2, 64, 64, order=DTP, fresh=(2,)),
     Packed((2600,), 1, 1, 128, 128, alpha_mean=6.0),   # long memory
     Packed((900, 700), 1, 2, 128, 128, alpha_mean=-4.0),  # strong decay
+    # many segments: the chain of start states in two levels, and in one beside it
+    Packed((9000, 1300, 7, 4700), 1, 1, 64, 64, slots=1, alpha_mean=5.0),
+    Packed((5377, 6144), 1, 2, 128, 128, order=DTP, alpha_mean=5.0),
 ]
 
 
@@ -127,6 +130,69 @@ def test_zero_gates_reset_the_state():
             return c
         c.make = with_zeros
         check(c, *run(c))
+
+
+@pytest.mark.parametrize("q,k,v,state", [(40, 0, 0, 0), (-60, 0, 0, 0), (0, -20, 0, 0), (0, -45, 0, -45), (0, 0, 60, 60),
+                                         (0, 0, -80, -80), (20, -30, -10, 35), (0, 0, 0, 40), (0, 0, 40, 0), (-30, 1, 30, 30)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_any_scale(d, q, k, v, state):
+    """Inputs and states times powers of two: as near to the exact results as
+    without (every scale a factor of the results, which are compared by their
+    largest; two times the keys with a quarter of beta keeps the state bounded)."""
+    c = Packed((70, 700, 3), 1, 2, d, d, seed=31)
+    make = c.make
+
+    def scaled():
+        make()
+        for n, e in (("q", q), ("k", k), ("v", v), ("pool", state)):
+            c.a[n] = (c.a[n] * np.float32(2.0**e)).astype(np.float32)
+        if k > 0:
+            c.a["beta"] /= np.float32(4.0**k)
+        return c
+    c.make = scaled
+    check(c, *run(c))
+
+
+def test_tokens_and_features_of_different_sizes():
+    """Value features over twelve decades, tokens that grow over a chunk border,
+    one chunk of zeros: held to each feature's own largest value."""
+    c = Packed((400, 90), 1, 2, 128, 128, seed=32, fresh=(0, 1))
+    make = c.make
+
+    def sized():
+        make()
+        c.a["v"] *= (2.0 ** np.linspace(-20, 20, 128).round()).astype(np.float32)
+        c.a["v"][64:128] = 0
+        c.a["v"][192:256] *= 2.0**12
+        c.a["q"][256:320] = 0
+        c.a["k"][320:330] = 0
+        return c
+    c.make = sized
+    out, pool = run(c)
+    ref, ends = c.forward()
+    for lo, hi in ((0, 400), (400, 490)):
+        top = np.abs(ref[lo:hi]).max(0)
+        assert (np.abs(out[lo:hi] - ref[lo:hi]) <= 2.0**-8 * np.abs(ref[lo:hi]) + 2.0**-14 * top).all()
+    got = pool[c.a["slots_out"]]
+    assert (np.abs(got - ends) <= 1e-5 * np.abs(ends).max(-1, keepdims=True)).all()
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0**40, 2.0**100, 0.0])
+def test_a_large_state_is_forgotten(size):
+    """A gate of zero takes a state of any size away; values follow chunks later."""
+    c = Packed((330, 50), 1, 2, 64, 64, seed=33)
+    make = c.make
+
+    def forgetful():
+        make()
+        c.a["pool"] *= np.float32(size)
+        c.a["alpha"][[0, 330]] = 0.0
+        c.a["v"][:200] = 0
+        c.a["k"][0] = c.a["k"][330] = 0  # the first prediction would still read the state
+        c.a["q"][[0, 330]] = 0
+        return c
+    c.make = forgetful
+    check(c, *run(c))
 
 
 def test_nan_stays_in_its_sequence():
@@ -330,4 +396,4 @@ def test_timer_names_the_kernels():
     tm = gdn.Timer()
     o, _ = gdn.packed_fwd(*(c.cuda(n) for n in ("q", "k", "v", "alpha", "beta", "cu", "pool")), timer=tm)
     torch.cuda.synchronize()
-    assert set(tm.read()) == {"k_pk_rec", "k_pk_prep", "k_pk_state", "k_pk_chain", "k_pk_out"}
+    assert set(tm.read()) == {"k_pk_prep", "k_pk_state", "k_pk_chain", "k_pk_out"}

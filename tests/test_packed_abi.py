@@ -29,7 +29,11 @@ ODD = ctypes.c_void_p(0x10002)
     (dict(max_len=-1), SHAPE), (dict(n_in=-1), SHAPE), (dict(N=2**31), SHAPE), (dict(S=2**31), SHAPE),
     (dict(S=2**25, Hv=8, n_in=2**25, n_out=2**25), SHAPE),     # more workgroups than a grid holds
     (dict(dk=72), UNSUP), (dict(dv=144), UNSUP), (dict(dk=8), UNSUP),
+    (dict(S=2**18, Hv=16, n_in=2**18, n_out=2**18), SHAPE),
+    (dict(S=2**16, Hv=16, n_in=2**16, n_out=2**16, max_len=64, dk=64, dv=64, sv=1024), SHAPE),  # fewer with chunk kernels
+    (dict(N=2**25, Hv=16, max_len=2**25, dk=64, dv=64, sv=1024), SHAPE),
     (dict(sq=127), SHAPE), (dict(sv=255), SHAPE), (dict(sk=2**31), SHAPE),
+    (dict(sq=2**23 + 8), SHAPE), (dict(sk=2**23 + 8), SHAPE), (dict(sv=2**23 + 8), SHAPE),  # 32-bit offsets in a chunk
     (dict(sq=132), ARG), (dict(sk=129), ARG), (dict(sv=258, dtype=0), ARG),   # strides of whole 16-byte pieces
     (dict(q=NUL), ARG), (dict(k=NUL), ARG), (dict(v=NUL), ARG), (dict(alpha=NUL), ARG), (dict(beta=NUL), ARG),
     (dict(cu=NUL), ARG), (dict(out=NUL), ARG),
@@ -137,7 +141,8 @@ def bwd(N=100, S=2, Hk=2, Hv=4, dk=64, dv=64, n_in=2, dtype=1, gate=0, order=0, 
 @pytest.mark.parametrize("kw,want", [
     (dict(dtype=2), ARG), (dict(gate=2), ARG), (dict(order=2), ARG), (dict(N=-1), SHAPE), (dict(Hk=3), SHAPE),
     (dict(gate=1), UNSUP), (dict(dk=128), UNSUP), (dict(dk=32, dv=32), UNSUP), (dict(dk=60), UNSUP),
-    (dict(sq=100), SHAPE), (dict(sq=129), ARG), (dict(n_in=1), SHAPE),
+    (dict(sq=100), SHAPE), (dict(sq=129), ARG), (dict(n_in=1), SHAPE), (dict(sv=2**23 + 8), SHAPE),
+    (dict(S=2**18, n_in=2**18), SHAPE), (dict(N=2**27), SHAPE),
     (dict(q=NUL), ARG), (dict(cu=NUL), ARG), (dict(g=NUL), ARG), (dict(dq=NUL), ARG), (dict(dkk=NUL), ARG), (dict(dvv=NUL), ARG),
     (dict(da=NUL), ARG), (dict(db=NUL), ARG), (dict(g=ODD), ARG), (dict(dq=ctypes.c_void_p(0x10004)), ARG), (dict(da=ODD), ARG),
     (dict(ds=ctypes.c_void_p(0x10008)), ARG), (dict(gs=ODD), ARG), (dict(ws=NUL), WS), (dict(wsb=1000), WS), (dict(ws=ODD), ARG),
