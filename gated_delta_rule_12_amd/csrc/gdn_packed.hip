@@ -693,7 +693,7 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 // output pass, so that the end state may go where the start state was) or, by
 // a workgroup of its own, M from I (the recurrence with V = 0).
 template <int D, bool OUT>
-__global__ __launch_bounds__(seg_threads<D>(), D == 128 ? 2 : 1) void k_pk_seg(Pk a) {
+__global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
     constexpr int NT = seg_threads<D>(), KT = D / 32, PPR = D / 8, KP = C * PPR / NT;
     constexpr int GP = (kGatePieces + NT - 1) / NT;
     static_assert(C * PPR % NT == 0, "staging split");
@@ -1103,7 +1103,7 @@ __global__ __launch_bounds__(seg_threads<D>(), D == 128 ? 2 : 1) void k_pk_seg(P
 // columns 16 w ..; fp32 MFMA, the next three matrices in flight while one
 // multiplies (a step takes 2.4 us: 64 KiB into the compute unit, then LDS
 // exchange and products one behind the other).
-constexpr int kChainShift = 3, kChainLong = 16;  // maps a block; the fewest that go two-level
+constexpr int kChainShift = 3, kChainLong = 32;  // maps a block; the fewest that go two-level
 enum { kCompose, kBlocks, kExpand };
 template <int D, int MODE, int R>
 __global__ __launch_bounds__(4 * D, 2) void k_pk_chain(Pk a) {
@@ -1237,11 +1237,14 @@ __global__ __launch_bounds__(4 * D, 2) void k_pk_chain(Pk a) {
 // outputs 116 instead of 149 us), but have twice the matrices to multiply
 // through the chain (153 instead of 101 us); mixed batch of 16384, 16 heads:
 // state pass, chain and outputs 105, 56, 144 instead of 80, 30, 158 us.
-constexpr int kSegMinShift = 6 + 2;
+// Heads of 64 have workgroups of two waves, so twice as many, of at least two
+// chunks (8 sequences of 2048, 16 heads: 240 us with one a compute unit, 174
+// with two; 4 of 500, 4 heads: 63 us with four chunks, 44 with two; heads of
+// 128: 92 and 81 us for 4 of 1000, but 118 and 135 us for one of 4096).
 constexpr int kWhole = 31;  // a sequence's tokens are fewer than 2^31
 int seg_shift_for(const Packed& p) {
-    const int64_t want = std::max<int64_t>(1, p.N * p.Hv / 256);  // tokens a workgroup
-    int sh = kSegMinShift;
+    const int64_t want = p.N * p.Hv / (p.dk == 64 ? 512 : 256);  // tokens a workgroup
+    int sh = p.dk == 64 ? 7 : 8;
     while (((int64_t)1 << sh) < want && sh < 30) ++sh;
     return sh;
 }

@@ -86,7 +86,7 @@ CASES = [
     Packed((0, 200, 1, 0, 128, 66, 0), 2, 4, 128, 128, slots=2, tail=5),
     Packed((129, 1, 300), 1, 3, 128, 128, order=DTP, fresh=(0, 2), slots=1),
     Packed((191, 250), 4, 4, 64, 64, order=DTP, scale=0.125),
-    # segments: 512 tokens each at these sizes
+    # segments
     Packed((1100, 30, 513), 1, 2, 128, 128, slots=1),
     Packed((512, 511, 1537), 2, 2, 64, 64, order=DTP, fresh=(2,)),
     Packed((2600,), 1, 1, 128, 128, alpha_mean=6.0),   # long memory
@@ -94,6 +94,7 @@ CASES = [
     # many segments: the chain of start states in two levels, and in one beside it
     Packed((9000, 1300, 7, 4700), 1, 1, 64, 64, slots=1, alpha_mean=5.0),
     Packed((5377, 6144), 1, 2, 128, 128, order=DTP, alpha_mean=5.0),
+    Packed((4000, 9100), 1, 1, 128, 128, slots=1, alpha_mean=5.0),
 ]
 
 
