@@ -47,6 +47,13 @@
 //     its 16 rows in registers; wave w owns key tiles of it, the token tiles
 //     of the chunk products are dealt over the waves and exchanged in LDS.
 //   k_bgrad, one workgroup per chunk: everything else from the stored pieces.
+// Over packed sequences (gdn_packed_backward) the same kernels run with
+// PackedGeo: chunks at their places by rule, the chains longest first; the
+// gradients of a shared key head are summed over its value heads by k_bfold in
+// a fixed order, and k_bclear zeroes the rows outside the sequences.  7
+// sequences, 16384 tokens, 16 heads of 128, bf16: 235 + 794 + 784 + 5 us; the
+// chains are bound by the latency of their steps (6 us for three phases, at
+// half the matrix cores' rate), the gradients by their fp32 products and LDS.
 #include <type_traits>
 
 #include "gdn_internal.h"

@@ -21,6 +21,11 @@
 // workgroup adds its row groups in LDS and writes one partial row; k_ln_params
 // adds the partial rows.  Every sum has a fixed order (no atomics), so
 // repeated calls give identical results.
+//
+// Bound by memory: 262144 x 128 (fp32 in, bf16 out) forward 39 us for 203 MB
+// (5.2 TB/s; 31.5 us where the input is still in the last-level cache),
+// backward 63 us for 338 MB (5 of them k_ln_params); 16381 x 2048 bf16
+// backward 45 us for 201 MB.
 #include "gdn_internal.h"
 #include "../../include/gdn.h"
 

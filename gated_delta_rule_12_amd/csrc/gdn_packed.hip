@@ -27,9 +27,10 @@
 //     start states (k_pk_chain: S_start(g + 1) = S_end(g) + S_start(g) M(g),
 //     the sequence-parallel notes' increment and correction, as a two-level
 //     scan where it is long) and the output pass from the true start states.
-// Measured (bf16, D = 128): 8 sequences of 1 to 8192 tokens, 16384 together,
-// 16 value heads, 332 us (prep 61, state pass 80, chain 30, outputs 158; bytes
-// alone 47 us); one of 65531, 4 heads, 405 us (46, 115, 101, 149).
+// Measured (bf16, D = 128): 40 sequences of very different lengths, 16384
+// tokens, 16 value heads, 337 us (prep 62, state pass 78, chain 28, outputs
+// 155; the bytes alone 47 us); one of 65531, 4 heads, 405 us (46, 118, 101,
+// 149; bytes 45 us).
 // Chunks and segments have their places by rule (gdn_packed_common.h).  Slots
 // outside the pool read as zero states and are not written.
 #include <type_traits>
@@ -87,8 +88,11 @@ __device__ __forceinline__ float* state_to(const Packed& p, int64_t s, int64_t h
 // lane c at columns 4 (c + LPR i)), R rows a thread; the two dot products are
 // summed over the row's lanes by vector-ALU butterflies.  A single token is a
 // stream over the state (8 dk dv bytes a head; non-temporal, each byte is
-// touched once): k_pk_step.  k_pk_rec stages more of them kStage at a time in
-// LDS, the next stage's rows in flight while the current one is worked off.
+// touched once): k_pk_step, 256 x 16 states of 128 x 128 in 97 us (bytes: 89).
+// k_pk_rec stages more of them kStage at a time in LDS, the next stage's rows
+// in flight while the current one is worked off: 48 x 5 tokens, channel gate,
+// 29 us (bytes: 18; bound by the states' stream and then by the tokens' sums,
+// one behind the other).
 constexpr int kRecThreads = 256;
 constexpr int kStage = 8;
 constexpr int kRecLPR = 16, kRecR = 2;
@@ -684,7 +688,12 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
     return row * D + 8 * (piece ^ (row & (D / 8 - 1)));
 }
 
-// One segment of one value head.  Wave w holds value columns 32 w .. of S^T
+// One segment of one value head.  Bound by the vector ALU (counted at D = 128,
+// two workgroups a compute unit: 57 % of the time against 29 % of the matrix
+// cores': splits of S, U and Delta into two terms, scaling, gates).  Waves of
+// 32 columns read each K and Q operand half as often as waves of 16, and fp16
+// pairs take two products a term where bf16 takes three for the same bits: the
+// outputs of the batch above 205 -> 155 us.  Wave w holds value columns 32 w .. of S^T
 // for every key (accumulator tiles; they serve as the next product's operand
 // as they stand), so nothing but the staged chunk and P crosses waves.
 // OUT: from the segment's start state, with outputs; the last segment writes
@@ -707,6 +716,8 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
     const int64_t rank = rank_of_segment(a.first, p.S, i_seg, l), s = a.order[rank];
     const Span sp = span_of(a.at, s);
     const int64_t gi = i_seg - a.first[rank], ng = (sp.n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
+    // (counted apart from the lengths, which offsets out of order can overflow)
+    if (gi < 0 || gi >= ng) return;
     if (!OUT && (gi == ng - 1 || (is_m && gi == 0))) return;
     const int64_t place = (sp.begin >> a.seg_shift) + s + gi;  // of the segment's states
     const int64_t per = (int64_t)1 << (a.seg_shift - 6);       // chunks of a segment
@@ -1101,8 +1112,12 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
 // start (kExpand, which alone does the whole of a short chain).
 // Sixteen rows of one head a workgroup (rows are independent), wave w the
 // columns 16 w ..; fp32 MFMA, the next three matrices in flight while one
-// multiplies (a step takes 2.4 us: 64 KiB into the compute unit, then LDS
-// exchange and products one behind the other).
+// multiplies (a step takes 2.4 us at D = 128: 64 KiB into the compute unit,
+// then LDS exchange and products one behind the other).  The two-level scan's
+// outer kernels take R = 2 sixteens of rows a workgroup: half the matrices'
+// loads, and a round of workgroups instead of two (190 -> 153 us at 127 maps
+// of 4 heads).  One level and two: 64 maps, D = 128, 150 and 101 us; at most
+// 25 maps, D = 64, 23 and 34 us.
 constexpr int kChainShift = 3, kChainLong = 32;  // maps a block; the fewest that go two-level
 enum { kCompose, kBlocks, kExpand };
 template <int D, int MODE, int R>

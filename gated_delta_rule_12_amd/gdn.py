@@ -626,6 +626,7 @@ def packed_fwd(q, k, v, alpha, beta, cu_seqlens, state_in=None, slots_in=None, s
     if max_len is None:
         max_len = N
     code = _dtype_code(q)
+    _on(workspace, dev, torch.uint8, "workspace")
     if workspace is None:
         n = lib().gdn_packed_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, code, gate)
         if n:
@@ -659,6 +660,7 @@ def packed_backward(q, k, v, alpha, beta, cu_seqlens, state_in, slots_in, grad_o
     grads = [q.new_empty(t.shape, dtype=f32) for t in (q, k, v, alpha, beta)]
     ds0 = q.new_empty((S, Hv, dv, dk), dtype=f32) if want_grad_state0 else None
     code = _dtype_code(q)
+    _on(workspace, dev, torch.uint8, "workspace")
     if workspace is None:
         n = lib().gdn_packed_backward_workspace_bytes(N, S, Hk, Hv, dk, dv, code, gate)
         if n:
@@ -739,6 +741,7 @@ def layer_norm_backward(grad_y, x, weight, mean, rstd, *, want_x=True, want_weig
     dx = x.new_empty(x.shape) if want_x else None
     dw = x.new_empty((n,), dtype=f32) if want_weight else None
     db = x.new_empty((n,), dtype=f32) if want_bias else None
+    _on(workspace, dev, torch.uint8, "workspace")
     if workspace is None and (want_weight or want_bias):
         workspace = x.new_empty((lib().gdn_layer_norm_workspace_bytes(rows, n),), dtype=torch.uint8)
     _enqueue("gdn_layer_norm_backward", (rows, n, _norm_code(x.dtype), _norm_code(grad_y.dtype), grad_y.data_ptr(),

@@ -162,6 +162,31 @@ def test_unaligned_views_and_aliases():
     assert torch.equal(inplace, ref)
 
 
+def test_large_offsets():
+    """More than 2^31 elements: the last rows, and the weight's gradient of
+    gradients that are zero but there."""
+    import torch
+    rows, n = 2**31 // 256 + 999, 256
+    x = torch.full((rows, n), 2.0, dtype=torch.bfloat16, device="cuda")
+    tail, dy, w, b = make(500, n, "bf16", "bf16", 9)
+    x[-500:] = tail
+    y, mean, rstd = gdn.layer_norm_fwd(x, w, b)
+    small = gdn.layer_norm_fwd(tail, w, b)
+    torch.cuda.synchronize()
+    assert torch.equal(y[-500:], small[0]) and torch.equal(mean[-500:], small[1]) and torch.equal(rstd[-500:], small[2])
+    g = torch.zeros_like(x)
+    g[-500:] = dy
+    dx, dw, db = gdn.layer_norm_backward(g, x, w, mean, rstd)
+    sx, sw, sb = gdn.layer_norm_backward(dy, tail, w, *small[1:])
+    torch.cuda.synchronize()
+    assert torch.equal(dx[-500:], sx)
+    # the same 500 terms in another order: either sum within 500 roundings of
+    # partial sums that the terms' magnitudes bound
+    xhat = (tail.double() - small[1].double()[:, None]) * small[2].double()[:, None]
+    for a, r, terms in ((dw, sw, dy.double() * xhat), (db, sb, dy.double())):
+        assert ((a - r).double().abs() <= 2 * 500 * 2.0**-24 * terms.abs().sum(0)).all()
+
+
 def test_empty_and_deterministic_and_replayed():
     import torch
     x = torch.empty((0, 64), device="cuda")

@@ -234,6 +234,19 @@ def test_slices_of_one_projection():
     check(c, *run(c, tensors=parts))
 
 
+@pytest.mark.parametrize("d,gate", [(64, "scalar"), (128, "scalar"), (128, "channel")])
+def test_far_tokens(d, gate):
+    """Token strides up to the limit: elements past 2^31, bytes past 2^32 (in
+    chunks, rows of one chunk a gigabyte apart)."""
+    import torch
+    c = Packed((270, 30, 1), 1, 2, d, d, gate=gate, seed=34).make()
+    far = torch.empty((301, 2**23), dtype=torch.bfloat16, device="cuda")
+    far[:, :d], far[:, d:2 * d] = c.cuda("q")[:, 0], c.cuda("k")[:, 0]
+    far[:, -2 * d:] = c.cuda("v").view(301, 2 * d)
+    check(c, *run(c, tensors={"q": far[:, :d].view(301, 1, d), "k": far[:, d:2 * d].view(301, 1, d),
+                              "v": far[:, -2 * d:].view(301, 2, d)}))
+
+
 def test_two_sequences_start_from_one_slot():
     c = Packed((70, 70, 3), 1, 2, 64, 64, seed=12, slots=1)
     make = c.make

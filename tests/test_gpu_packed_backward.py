@@ -158,6 +158,19 @@ def test_slices_of_one_projection():
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_far_tokens(d):
+    """Token strides up to the limit: elements past 2^31, bytes past 2^32."""
+    import torch
+    c = Packed((270, 31), 1, 2, d, d, seed=36).make()
+    far = torch.empty((301, 2**23), dtype=torch.bfloat16, device="cuda")
+    far[:, :d], far[:, d:2 * d] = c.cuda("q")[:, 0], c.cuda("k")[:, 0]
+    far[:, -2 * d:] = c.cuda("v").view(301, 2 * d)
+    t = tensors(c)
+    t.update(q=far[:, :d].view(301, 1, d), k=far[:, d:2 * d].view(301, 1, d), v=far[:, -2 * d:].view(301, 2, d))
+    check(c, run(c, t))
+
+
 def test_bad_offsets_stay_in_bounds():
     """Falling, negative and far offsets and slots (the values are not defined)."""
     import torch
