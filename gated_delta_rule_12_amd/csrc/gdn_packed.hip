@@ -387,8 +387,20 @@ hipError_t launch_rec_shape(const Pk& a, hipStream_t st) {
         if (pieces <= 16) return launch_step<DT, CH, 16, 4>(a, st);
         return launch_step<DT, CH, 32, 4>(a, st);
     }
-    if (pieces <= 8) return launch_rec<DT, CH, 8, 1, kRecR>(a, st);
-    if (pieces <= 16) return launch_rec<DT, CH, kRecLPR, 1, kRecR>(a, st);
+    // With few states a token's latency counts, and fewer elements a thread take
+    // less of it; with many, the lanes' sums cost more than they hide.  fp32, heads
+    // of 128, lanes a row x rows a thread 32 x 1, 16 x 1, 16 x 2: 16 states, 1000
+    // tokens 233, 269, 391 us; 256 states, 100 tokens 125, 102, 107 us; 4096, 8
+    // tokens 201, 167, 155 us.  Heads of 64, 16 x 1 and 16 x 2: 16 states 231 and
+    // 294 us, 1024 of 30 tokens 39 and 43, 4096 of 8 tokens 50 and 46.
+    const int64_t states = a.p.S * a.p.Hv;
+    if (pieces <= 16) {
+        if (states <= 1024)
+            return pieces <= 8 ? launch_rec<DT, CH, 8, 1, 1>(a, st) : launch_rec<DT, CH, kRecLPR, 1, 1>(a, st);
+        return pieces <= 8 ? launch_rec<DT, CH, 8, 1, kRecR>(a, st) : launch_rec<DT, CH, kRecLPR, 1, kRecR>(a, st);
+    }
+    if (states <= 32) return launch_rec<DT, CH, 32, 1, 1>(a, st);
+    if (states <= 512) return launch_rec<DT, CH, kRecLPR, 2, 1>(a, st);
     return launch_rec<DT, CH, kRecLPR, 2, kRecR>(a, st);
 }
 

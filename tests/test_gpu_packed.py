@@ -105,6 +105,16 @@ def test_forward(i):
     check(c, *run(c))
 
 
+@pytest.mark.parametrize("dtype,gate", [("f32", "scalar"), ("bf16", "channel"), ("f32", "channel")])
+@pytest.mark.parametrize("dk,dv", [(32, 32), (64, 48), (128, 128)])
+@pytest.mark.parametrize("S,hv", [(3, 2), (20, 4), (140, 4), (300, 4)])
+def test_token_form_over_few_and_many_states(S, hv, dk, dv, dtype, gate):
+    """The token-by-token kernels by number of states: 1 to 12 tokens each."""
+    lengths = tuple(1 + (7 * s) % 12 for s in range(S))
+    c = Packed(lengths, 2, hv, dk, dv, dtype=dtype, gate=gate, order=S % 2, seed=37)
+    check(c, *run(c))
+
+
 @pytest.mark.parametrize("lengths,d", [((1, 1, 1), 128), ((3, 90, 1200), 128), ((5, 600), 64)])
 def test_in_place(lengths, d):
     c = Packed(lengths, 2, 4, d, d, slots=2, seed=7)
