@@ -475,7 +475,8 @@ __device__ __forceinline__ Half2 split_f16(const float (&v)[N], int at, float x)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float a = v[at + 2 * i], b = v[at + 2 * i + 1];
-        h[i] = pack_f16(a * x, b * x);
+        h[i] = pack_f16(__builtin_fmaf(a, x, 0.f), __builtin_fmaf(b, x, 0.f));
+        asm("" : "+v"(h[i]));  // (taken as packed by what follows, not formed again element by element)
         const f16x2 t = __builtin_bit_cast(f16x2, h[i]);
         l[i] = pack_f16(__builtin_fmaf(a, x, -(float)t[0]), __builtin_fmaf(b, x, -(float)t[1]));
     }
@@ -485,7 +486,8 @@ __device__ __forceinline__ Half2 split_f16(const float (&v)[N], int at, float x)
 __device__ __forceinline__ u32x4 bf16_to_f16(const u32x4& v, float x) {
     u32x4 y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = pack_f16(__uint_as_float(v[i] << 16) * x, __uint_as_float(v[i] & 0xFFFF0000u) * x);
+    for (int i = 0; i < 4; ++i)
+        y[i] = pack_f16(__builtin_fmaf(__uint_as_float(v[i] << 16), x, 0.f), __builtin_fmaf(__uint_as_float(v[i] & 0xFFFF0000u), x, 0.f));
     return y;
 }
 __device__ __forceinline__ float max_abs8(const u32x4& v) {  // of eight bf16
