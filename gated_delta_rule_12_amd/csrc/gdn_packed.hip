@@ -28,9 +28,9 @@
 //     the sequence-parallel notes' increment and correction, as a two-level
 //     scan where it is long) and the output pass from the true start states.
 // Measured (bf16, D = 128): 40 sequences of very different lengths, 16384
-// tokens, 16 value heads, 337 us (prep 62, state pass 78, chain 28, outputs
-// 155; the bytes alone 47 us); one of 65531, 4 heads, 405 us (46, 118, 101,
-// 149; bytes 45 us).
+// tokens, 16 value heads, 310 us (prep 62, state pass 80, chain 28, outputs
+// 150; the bytes alone 47 us); one of 65531, 4 heads, 395 us (46, 114, 101,
+// 138; bytes 45 us).
 // Chunks and segments have their places by rule (gdn_packed_common.h).  Slots
 // outside the pool read as zero states and are not written.
 #include <type_traits>
@@ -707,7 +707,10 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 // cores': splits of S, U and Delta into two terms, scaling, gates).  Waves of
 // 32 columns read each K and Q operand half as often as waves of 16, and fp16
 // pairs take two products a term where bf16 takes three for the same bits: the
-// outputs of the batch above 205 -> 155 us.  Wave w holds value columns 32 w .. of S^T
+// outputs of the batch above 205 -> 158 us.  The next chunk's rows are asked for
+// in front of the outputs instead of behind them (158 -> 150 us; 148 -> 138 us
+// for the long sequence, where no second workgroup covers the wait); asked for
+// in front of Delta: 155 and 135 us.  Wave w holds value columns 32 w .. of S^T
 // for every key (accumulator tiles; they serve as the next product's operand
 // as they stand), so nothing but the staged chunk and P crosses waves.
 // OUT: from the segment's start state, with outputs; the last segment writes
@@ -766,7 +769,7 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
             }
     }
 
-    // staging: the next chunk's K and Q in registers from the state update on,
+    // staging: the next chunk's K and Q in registers from the outputs on,
     // its T' and V straight into LDS once this chunk's are used (addresses: a
     // uniform base and 32 bits a lane)
     u32x4 kr[KP], qr[OUT ? KP : 1];
@@ -967,6 +970,8 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
         const bool more = i + 1 < i_end;
         __syncthreads();  // T' is used, P whole
         if (more) fetch_T(i + 1);
+        if (more) issue(i + 1);
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (OUT) {
             // O = diag(scale gamma) Q S^T + scale P Delta, P and Delta in two bf16
             // terms, rounded once to bf16, over V (S is split again: X's phase has
@@ -1023,8 +1028,6 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
                     Vw[(t + 1) * 32 + c] = (unsigned short)(y >> 16);
                 }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) issue(i + 1);
         __builtin_amdgcn_sched_barrier(0);
         // S^T <- gamma_C S^T + K^T diag(gamma_C / gamma) Delta, summed in the scale
         // of the larger of the two (the decayed state, not the one before it: a
@@ -1263,13 +1266,13 @@ __global__ __launch_bounds__(4 * D, 2) void k_pk_chain(Pk a) {
 // Tokens of a segment, as a power of two: as many segments as there are
 // compute units over all heads, at least four chunks each.  Twice as many run
 // the output pass two workgroups a compute unit (one of 65531 tokens, 4 heads:
-// outputs 116 instead of 149 us), but have twice the matrices to multiply
+// outputs 113 instead of 139 us), but have twice the matrices to multiply
 // through the chain (153 instead of 101 us); mixed batch of 16384, 16 heads:
-// state pass, chain and outputs 105, 56, 144 instead of 80, 30, 158 us.
+// state pass, chain and outputs 106, 56, 140 instead of 82, 30, 154 us.
 // Heads of 64 have workgroups of two waves, so twice as many, of at least two
-// chunks (8 sequences of 2048, 16 heads: 240 us with one a compute unit, 174
-// with two; 4 of 500, 4 heads: 63 us with four chunks, 44 with two; heads of
-// 128: 92 and 81 us for 4 of 1000, but 118 and 135 us for one of 4096).
+// chunks (8 sequences of 2048, 16 heads: 222 us with one a compute unit and
+// four chunks, 170 so; 4 of 500, 4 heads: 58 and 44 us; heads of 128, four
+// chunks and two: 117 and 135 us for one of 4096, 91 and 80 for 4 of 1000).
 constexpr int kWhole = 31;  // a sequence's tokens are fewer than 2^31
 int seg_shift_for(const Packed& p) {
     const int64_t want = p.N * p.Hv / (p.dk == 64 ? 512 : 256);  // tokens a workgroup
