@@ -61,7 +61,8 @@ def test_packed_workspace_and_path():
     assert ws(5000, 3, 4, 4, 128, 128, 5000, 1, 1) == 0
     assert ws(5000, 3, 4, 3, 128, 128, 5000, 1, 0) == 0      # refused
     small, large = ws(5000, 3, 4, 4, 128, 128, 400, 1, 0), ws(5000, 3, 4, 4, 128, 128, 5000, 1, 0)
-    assert 0 < small < large and large % 256 == 0
+    one = ws(5000, 3, 4, 4, 128, 128, 100, 1, 0)  # a segment each: no states of segments
+    assert 0 < one < small <= large and large % 256 == 0
 
 
 def norm_fwd(rows=4, n=64, xt=0, yt=1, x=F, w=F, b=F, y=F, m=F, r=F):
