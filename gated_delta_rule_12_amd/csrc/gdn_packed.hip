@@ -70,6 +70,15 @@ struct Pk {
     float* p_blk;    // [block place, head][D][D]: and matrix, transposed
 };
 
+// Workgroups go to the eight XCDs in turn.  The work of workgroup b of n, so
+// that `set` consecutive pieces of work fall to one XCD and meet in its L2
+// (a step's states of 256 sequences 108 -> 97 us with a sequence a set; a state
+// pass with S and M of two value heads a set 82 -> 79 us).
+__device__ __forceinline__ unsigned on_one_xcd(unsigned b, unsigned n, unsigned set) {
+    const unsigned run = 8 * set, i = b / run, r = b - i * run;
+    return (i + 1) * run <= n ? i * run + (r % 8) * set + r / 8 : b;
+}
+
 __device__ __forceinline__ const float* state_from(const Packed& p, int64_t s, int64_t h) {
     const int64_t slot = p.slots_in ? (int64_t)p.slots_in[s] : s;
     if (!p.s_in || slot < 0 || slot >= p.n_in) return nullptr;
@@ -166,11 +175,9 @@ struct RecAt {
 };
 template <int RB>
 __device__ __forceinline__ bool rec_at(const Pk& a, unsigned blocks, RecAt& x) {
-    // workgroups go to the eight XCDs in turn: each XCD takes a run of
-    // sequences of its own
-    const unsigned nrb = ((unsigned)a.p.dv + RB - 1) / RB, one = nrb * a.Hv, run = 8 * one;
-    const unsigned g = blockIdx.x / run, r = blockIdx.x - g * run;
-    const unsigned block = (g + 1) * run <= blocks ? g * run + (r % 8) * one + r / 8 : blockIdx.x;
+    // each XCD takes whole sequences
+    const unsigned nrb = ((unsigned)a.p.dv + RB - 1) / RB, one = nrb * a.Hv;
+    const unsigned block = on_one_xcd(blockIdx.x, blocks, one);
     const unsigned id = block / nrb;
     x.rb = block - id * nrb;
     x.s = id / a.Hv;
@@ -545,7 +552,7 @@ __global__ __launch_bounds__(kThreads, 7) void k_pk_prep(Pk a, unsigned recs) {
         rec_block<GDN_BF16, 0, kRecLPR, D / 64, kRecR>(a, recs, *reinterpret_cast<Rec*>(AT));
         return;
     }
-    const unsigned id = blockIdx.x - recs;
+    const unsigned id = on_one_xcd(blockIdx.x - recs, gridDim.x - 1 - recs, a.group);
     const int place = id / a.Hv, h = id - place * a.Hv, hk = h / a.group;
     const int64_t s = seq_of_place(a.at, place, 6, l);
     const Span sp = span_of(a.at, s);
@@ -726,8 +733,10 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
     __shared__ __attribute__((aligned(16))) SegShared<D, OUT> sh;
     const Packed& p = a.p;
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g = l >> 5, c = l & 31;
-    const int place_h = OUT ? blockIdx.x : blockIdx.x >> 1;
-    const bool is_m = !OUT && (blockIdx.x & 1);
+    // workgroups that read the same K (and Q) rows: a key head's value heads, S and M
+    const unsigned block = on_one_xcd(blockIdx.x, gridDim.x, (OUT ? 1 : 2) * a.group);
+    const int place_h = OUT ? block : block >> 1;
+    const bool is_m = !OUT && (block & 1);
     const int i_seg = place_h / a.Hv, h = place_h - i_seg * a.Hv, hk = h / a.group;
     if (i_seg >= a.first[p.S]) return;
     const int64_t rank = rank_of_segment(a.first, p.S, i_seg, l), s = a.order[rank];
