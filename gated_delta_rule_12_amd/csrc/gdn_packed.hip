@@ -28,9 +28,9 @@
 //     the sequence-parallel notes' increment and correction, as a two-level
 //     scan where it is long) and the output pass from the true start states.
 // Measured (bf16, D = 128): 40 sequences of very different lengths, 16384
-// tokens, 16 value heads, 310 us (prep 62, state pass 80, chain 28, outputs
-// 150; the bytes alone 47 us); one of 65531, 4 heads, 395 us (46, 114, 101,
-// 138; bytes 45 us).
+// tokens, 16 value heads, 309 us (prep 62, state pass 76, chain 28, outputs
+// 140 to 150; the bytes alone 47 us); one of 65531, 4 heads, 391 us (46, 112,
+// 101, 139; bytes 45 us).
 // Chunks and segments have their places by rule (gdn_packed_common.h).  Slots
 // outside the pool read as zero states and are not written.
 #include <type_traits>
@@ -73,7 +73,7 @@ struct Pk {
 // Workgroups go to the eight XCDs in turn.  The work of workgroup b of n, so
 // that `set` consecutive pieces of work fall to one XCD and meet in its L2
 // (a step's states of 256 sequences 108 -> 97 us with a sequence a set; a state
-// pass with S and M of two value heads a set 82 -> 79 us).
+// pass with S and M of two value heads a set 82 -> 76 us).
 __device__ __forceinline__ unsigned on_one_xcd(unsigned b, unsigned n, unsigned set) {
     const unsigned run = 8 * set, i = b / run, r = b - i * run;
     return (i + 1) * run <= n ? i * run + (r % 8) * set + r / 8 : b;
