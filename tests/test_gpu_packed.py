@@ -4,10 +4,10 @@ Tolerances, derived before the first run.  bf16 outputs: one rounding of at
 most 2^-8 of the value (half a step), plus the kernel's own error, fp32
 sums of at most 128 terms and two-term bf16 splits (2^-17 of the largest
 value): 2^-8 |o| + 2^-14 max |o| leaves a factor of eight on the latter.
-States and fp32 outputs: fp32 throughout (three-term splits lose nothing), a
-128-term sum is off by at most 128 2^-24 = 7.6e-6 of its terms' sizes, and gates
-below one keep a token's error from growing: 1e-5 of the largest value, the
-library's bound for fp32.
+States and fp32 outputs: fp32 throughout (operands split into terms that keep
+them to 2^-23 of their column's largest), a 128-term sum is off by at most 128
+2^-24 = 7.6e-6 of its terms' sizes, and gates below one keep a token's error from
+growing: 1e-5 of the largest value, the library's bound for fp32.
 """
 from __future__ import annotations
 
