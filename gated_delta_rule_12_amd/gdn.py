@@ -657,7 +657,9 @@ def packed_backward(q, k, v, alpha, beta, cu_seqlens, state_in, slots_in, grad_o
     if grad_state_out is not None and grad_state_out.shape != (S, Hv, dv, dk):
         raise ValueError("grad_state_out must be [S,Hv,dv,dk]")
     _on(grad_state_out, dev, f32, "grad_state_out")
-    grads = [q.new_empty(t.shape, dtype=f32) for t in (q, k, v, alpha, beta)]
+    # (without sequences the entry point enqueues nothing, and every row is outside them)
+    new = q.new_empty if S * Hv else q.new_zeros
+    grads = [new(t.shape, dtype=f32) for t in (q, k, v, alpha, beta)]
     ds0 = q.new_empty((S, Hv, dv, dk), dtype=f32) if want_grad_state0 else None
     code = _dtype_code(q)
     _on(workspace, dev, torch.uint8, "workspace")

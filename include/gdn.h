@@ -375,7 +375,8 @@ int gdn_packed_path(int64_t dk, int64_t dv, int32_t dtype, int32_t gate);
  *                   their end states; NULL: zero
  *   grad_q, grad_k  [N, Hk, dk] fp32, summed over the value heads of a key
  *                   head;  grad_v [N, Hv, dv], grad_alpha, grad_beta [N, Hv]
- *                   fp32; rows outside every sequence are set to zero
+ *                   fp32; rows outside every sequence are set to zero (S Hv = 0:
+ *                   nothing is enqueued, the gradients are left as they were)
  *   grad_state0     [S, Hv, dv, dk] fp32: dL/d of each sequence's start state
  *                   (sequences that share a slot each have their own); NULL:
  *                   not wanted

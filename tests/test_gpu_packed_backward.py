@@ -289,3 +289,26 @@ def test_a_training_step_of_a_block():
     # fp32 all the way: each of the six kernels adds its 1e-5
     for got, ref in ((dx, X.grad), (dw0, W0.grad), (dw1, W1.grad), (da, A.grad), (db, B.grad)):
         assert (got.double().cpu() - ref).abs().max() <= 6e-5 * ref.abs().max()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_without_sequences_every_row_is_zero(d):
+    """cu_seqlens of one entry: no sequence, so every row is outside them."""
+    import torch
+    c = Packed((70,), 1, 2, d, d, seed=51).make()
+    t = tensors(c)
+    t.update(cu=t["cu"][:1], slots_in=t["slots_in"][:0], dstate=t["dstate"][:0])
+    # (memory that the gradients may get back is not zero)
+    dirty = [torch.full((70, 2, d), 7.0, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    del dirty
+    got = run(c, t)
+    for name, x in zip(NAMES[:5], got):
+        assert (x == 0).all(), name
+    assert got[5].shape == (0, 2, d, d)
+    # no value heads: q and k have gradients of zero all the same
+    dq, dkk, dvv, *_ = gdn.packed_backward(t["q"], t["k"], t["v"][:, :0], t["alpha"][:, :0].contiguous(),
+                                           t["beta"][:, :0].contiguous(), c.cuda("cu"), None, None,
+                                           t["dout"][:, :0].contiguous())
+    torch.cuda.synchronize()
+    assert (dq == 0).all() and (dkk == 0).all() and dvv.shape == (70, 0, d)
