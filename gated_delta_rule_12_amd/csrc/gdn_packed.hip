@@ -458,6 +458,23 @@ __device__ __forceinline__ Pow2 pow2_for(float m) {
     const int e = max(min((int)(__float_as_uint(m) >> 23), 254), 14);
     return {__uint_as_float((uint32_t)(267 - e) << 23), __uint_as_float((uint32_t)(e - 13) << 23)};
 }
+// m, the largest magnitude of x's TILES tiles of 16 (NaN never is), or without
+// the infinities among them
+constexpr float kInf = __builtin_huge_valf();
+template <int TILES, class A>
+__device__ __forceinline__ float finite_max(float m, const A& x) {
+    if (m == kInf) {
+        m = 0.f;
+#pragma unroll
+        for (int u = 0; u < TILES; ++u)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float y = fabsf(x[u][e]);
+                m = y < kInf ? fmaxf(m, y) : m;
+            }
+    }
+    return m;
+}
 __device__ __forceinline__ float wave_max(float x) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
@@ -502,6 +519,14 @@ __device__ __forceinline__ float max_abs8(const u32x4& v) {  // of eight bf16
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         m = fmaxf(m, fmaxf(fabsf(__uint_as_float(v[i] << 16)), fabsf(__uint_as_float(v[i] & 0xFFFF0000u))));
+    return m;
+}
+__device__ __forceinline__ float finite_max8(float m, const u32x4& v) {  // of m and the finite ones of eight bf16
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float y = fabsf(__uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16));
+        m = y < kInf ? fmaxf(m, y) : m;
+    }
     return m;
 }
 // Four 16-bit elements of a column: in each group of 16 lanes, lane i points
@@ -571,6 +596,15 @@ __global__ __launch_bounds__(kThreads, 7) void k_pk_prep(Pk a, unsigned recs) {
         kv[i] = ld_g<u32x4>(kin + (t0 + t) * p.k_stride + c8 * 8);
         xk = fmaxf(xk, max_abs8(kv[i]));
         xq = fmaxf(xq, max_abs8(ld_g<u32x4>(qin + (t0 + t) * p.q_stride + c8 * 8)));
+    }
+    if (fmaxf(xk, xq) == kInf) {
+        xk = xq = 0.f;
+#pragma unroll 1
+        for (int e = tid; e < C * PPR; e += kThreads) {
+            const int t = min(e / PPR, nt - 1), c8 = e % PPR;
+            xk = finite_max8(xk, ld_g<u32x4>(kin + (t0 + t) * p.k_stride + c8 * 8));
+            xq = finite_max8(xq, ld_g<u32x4>(qin + (t0 + t) * p.q_stride + c8 * 8));
+        }
     }
     xk = wave_max(xk);
     xq = wave_max(xq);
@@ -662,7 +696,8 @@ __global__ __launch_bounds__(kThreads, 7) void k_pk_prep(Pk a, unsigned recs) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 x[k][4 * hf + r] = (j >> 4) > (t >> 4) ? 0.f : v[r];
-                m = fmaxf(m, fabsf(x[k][4 * hf + r]));
+                const float y = fabsf(x[k][4 * hf + r]);
+                m = y < kInf ? fmaxf(m, y) : m;
             }
         }
     }
@@ -914,7 +949,7 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
         for (int u = 0; u < KT; ++u)
 #pragma unroll
             for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(S[u][e]));
-        const float ms = column_max(m);
+        const float ms = column_max(finite_max<KT>(m, S));
         const Pow2 xs = pow2_for(ms);
         const float s_inv = xs.inv * unit;
         f32x16 X[2] = {};
@@ -945,7 +980,7 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
                     mu = fmaxf(mu, fabsf(X[m][4 * i4 + r]));
                 }
             }
-        const Pow2 xu = pow2_for(column_max(mu));
+        const Pow2 xu = pow2_for(column_max(finite_max<2>(mu, X)));
         __builtin_amdgcn_sched_barrier(0);
         // Delta = T' U
         f32x16 dl[2] = {};
@@ -1054,7 +1089,7 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
                 }
             }
         const float g_unit = sh.G[kGlast] * unit;
-        const Pow2 xd = pow2_for(fmaxf(column_max(md), ms * g_unit));
+        const Pow2 xd = pow2_for(fmaxf(column_max(finite_max<2>(md, dl)), ms * g_unit));
         const float gC = ms > 0.f ? g_unit * xd.x : 0.f;  // (a zero state leaves the scale anywhere)
         unit = xd.inv;
         const int kb = opaque(kc_base);

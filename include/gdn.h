@@ -328,8 +328,11 @@ int gdn_seqpar_fwd(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv,
  *               same.  1 for single tokens; N where nothing is known
  *   workspace   gdn_packed_workspace_bytes(...) bytes (0 without chunk
  *               kernels); two calls that may overlap need two
- * A NaN or an infinity in v reaches the later tokens of its value feature and
- * the other tokens of its chunk (64), nothing of other sequences or heads.
+ * NaN and infinities propagate as in the formula, to nothing of other
+ * sequences.  In the chunk form an infinity becomes a NaN, and beyond the
+ * formula one may reach the other tokens of its chunk (64): in v those of its
+ * value feature, in alpha or beta of its value head, in k of its key head; one
+ * in q reaches its own token alone.  What stays finite is right.
  * An empty sequence copies its start state.  Values of cu_seqlens out of
  * order or range are clamped, so they never lead out of the buffers.
  * Sequences of 32 tokens or more run in chunks on the matrix cores for

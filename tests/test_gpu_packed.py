@@ -421,3 +421,58 @@ def test_timer_names_the_kernels():
     o, _ = gdn.packed_fwd(*(c.cuda(n) for n in ("q", "k", "v", "alpha", "beta", "cu", "pool")), timer=tm)
     torch.cuda.synchronize()
     assert set(tm.read()) == {"k_pk_prep", "k_pk_state", "k_pk_chain", "k_pk_out"}
+
+
+@pytest.mark.parametrize("d,order", [(64, PTD), (128, DTP)])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("what", ["v", "q", "k", "alpha", "beta", "pool"])
+def test_non_finite_inputs_propagate(what, value, d, order):
+    """One infinity or NaN: what the formulas make non-finite is so, and every
+    finite output is the right one.  Beyond the formulas it may reach (as NaN)
+    the tokens of its own chunk of 64: in v those of its value feature, in a gate
+    or beta of its head, in k of every head that reads it; in q nothing but its
+    own token."""
+    c = Packed((40, 700, 33), 1, 2, d, d, order=order, seed=41)
+    c.make()
+    t, lo = 40 + 300, 40 + 256   # the token, its chunk's first
+    free = np.zeros((773, 2, d), bool)
+    if what == "v":
+        c.a["v"][t, 1, 5] = value
+        free[lo:lo + 64, 1, 5] = True
+    elif what == "q":
+        c.a["q"][t, 0, 5] = value
+    elif what == "k":
+        c.a["k"][t, 0, 5] = value
+        free[lo:lo + 64] = True
+    elif what == "pool":
+        c.a["pool"][c.a["slots_in"][1], 1, 5, 7] = value
+    else:
+        c.a[what][t, 1] = value
+        free[lo:lo + 64, 1] = True
+    c.make = lambda: c
+    out, pool = run(c)
+    ref, ends = c.forward()
+    bad = ~np.isfinite(ref)
+    assert bad.any() and not np.isfinite(out[bad]).any()
+    assert np.isfinite(out[~bad & ~free]).all()
+    ok = ~bad & np.isfinite(out)
+    out_ok(out[ok], ref[ok], "bf16")
+    got = pool[c.a["slots_out"]]
+    bad = ~np.isfinite(ends)
+    assert not np.isfinite(got[bad]).any() and np.isfinite(got[~bad]).all()
+    assert (np.abs(got - ends)[~bad] <= 1e-5 * np.abs(ends[~bad]).max()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["scalar", "channel"])
+@pytest.mark.parametrize("dk,dv", [(32, 32), (48, 16), (96, 128), (64, 64), (128, 128), (16, 112)])
+def test_single_tokens(dk, dv, gate, dtype):
+    """A step of one token a sequence in every type, gate and row layout, in both
+    orders, into another pool and in place; an empty sequence among them."""
+    lengths = (1, 1, 0, 1, 1, 1, 1)
+    for order in (PTD, DTP):
+        c = Packed(lengths, 2, 6, dk, dv, dtype=dtype, gate=gate, order=order, slots=2, fresh=(3,), tail=2, seed=42)
+        check(c, *run(c, max_len=1))
+        c.fresh = ()
+        out, pool = run(c, max_len=1, inplace=True)
+        check(c, out, pool, inplace=True)
