@@ -452,29 +452,15 @@ __device__ __forceinline__ f32x16 mfma32h(const u16x8& a, const u16x8& b, const 
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 struct Pow2 {
-    float x, inv;  // m x in [2^13, 2^14); 1 / x
+    float x, inv;  // m x in [2^13, 2^14), NaN for an infinite m; 1 / x
 };
 __device__ __forceinline__ Pow2 pow2_for(float m) {
     const int e = max(min((int)(__float_as_uint(m) >> 23), 254), 14);
-    return {__uint_as_float((uint32_t)(267 - e) << 23), __uint_as_float((uint32_t)(e - 13) << 23)};
+    // (a column with an infinity times NaN: scaled to it, what else the column
+    // holds would be zero, finite and wrong)
+    return {__builtin_fmaf(m, 0.f, __uint_as_float((uint32_t)(267 - e) << 23)), __uint_as_float((uint32_t)(e - 13) << 23)};
 }
-// m, the largest magnitude of x's TILES tiles of 16 (NaN never is), or without
-// the infinities among them
 constexpr float kInf = __builtin_huge_valf();
-template <int TILES, class A>
-__device__ __forceinline__ float finite_max(float m, const A& x) {
-    if (m == kInf) {
-        m = 0.f;
-#pragma unroll
-        for (int u = 0; u < TILES; ++u)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float y = fabsf(x[u][e]);
-                m = y < kInf ? fmaxf(m, y) : m;
-            }
-    }
-    return m;
-}
 __device__ __forceinline__ float wave_max(float x) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
@@ -949,7 +935,7 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
         for (int u = 0; u < KT; ++u)
 #pragma unroll
             for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(S[u][e]));
-        const float ms = column_max(finite_max<KT>(m, S));
+        const float ms = column_max(m);
         const Pow2 xs = pow2_for(ms);
         const float s_inv = xs.inv * unit;
         f32x16 X[2] = {};
@@ -980,7 +966,7 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
                     mu = fmaxf(mu, fabsf(X[m][4 * i4 + r]));
                 }
             }
-        const Pow2 xu = pow2_for(column_max(finite_max<2>(mu, X)));
+        const Pow2 xu = pow2_for(column_max(mu));
         __builtin_amdgcn_sched_barrier(0);
         // Delta = T' U
         f32x16 dl[2] = {};
@@ -1089,7 +1075,7 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
                 }
             }
         const float g_unit = sh.G[kGlast] * unit;
-        const Pow2 xd = pow2_for(fmaxf(column_max(finite_max<2>(md, dl)), ms * g_unit));
+        const Pow2 xd = pow2_for(fmaxf(column_max(md), ms * g_unit));
         const float gC = ms > 0.f ? g_unit * xd.x : 0.f;  // (a zero state leaves the scale anywhere)
         unit = xd.inv;
         const int kb = opaque(kc_base);
