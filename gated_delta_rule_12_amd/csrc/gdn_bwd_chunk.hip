@@ -214,7 +214,7 @@ struct PackedGeo {
         Head x;
         x.begin = sp.begin;
         x.n = sp.n;
-        x.place = (sp.begin >> 6) + s;
+        x.place = chunk_places().first(sp.begin, s);
         x.hl = hl;
         x.NC = (int)((sp.n + C - 1) / C);
         x.state = s * Hv + h0 + hl;
@@ -246,7 +246,7 @@ struct PackedGeo {
     }
     __device__ bool chunk(int64_t block, int lane, ChunkAt& x) const {
         const int place = (int)block / nh, hl = (int)block - place * nh;
-        const Head hd = head_of(seq_of_place(off, place, 6, lane), hl);
+        const Head hd = head_of(seq_of_place(off, place, chunk_places(), lane), hl);
         const int64_t c = place - hd.place;
         if (c < 0 || c >= hd.NC) return false;
         x = at(hd, (int)c);
@@ -1360,9 +1360,9 @@ hipError_t launch_chunked(const BwdProblem& a, const CbWs& ws, const Geo& geo, i
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_bfold(PackedGeo<D> geo, const float* sq, const float* sk, float* dq, float* dk) {
     const int nk = geo.nh / geo.group, place = blockIdx.x / nk, hkl = blockIdx.x - place * nk;
-    const int64_t s = seq_of_place(geo.off, place, 6, threadIdx.x & 63);
+    const int64_t s = seq_of_place(geo.off, place, chunk_places(), threadIdx.x & 63);
     const Span sp = span_of(geo.off, s);
-    const int64_t c = place - ((sp.begin >> 6) + s);
+    const int64_t c = place - chunk_places().first(sp.begin, s);
     if (c < 0 || c * C >= sp.n) return;
     const int nt = (int)min<int64_t>(C, sp.n - c * C);
     const int64_t t0 = sp.begin + c * C;

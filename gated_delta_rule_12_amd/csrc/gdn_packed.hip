@@ -31,8 +31,10 @@
 // tokens, 16 value heads, 309 us (prep 62, state pass 76, chain 28, outputs
 // 140 to 150; the bytes alone 47 us); one of 65531, 4 heads, 391 us (46, 112,
 // 101, 139; bytes 45 us).
-// Chunks and segments have their places by rule (gdn_packed_common.h).  Slots
-// outside the pool read as zero states and are not written.
+// Chunks have their places by rule (gdn_packed_common.h), segments theirs by
+// counts that the preparation's launch makes: only sequences longer than a
+// segment have states of segments, so that short ones cost no workspace.
+// Slots outside the pool read as zero states and are not written.
 #include <type_traits>
 
 #include "gdn_internal.h"
@@ -49,6 +51,7 @@ namespace {
 // 40 and 38; heads of 64, 256 sequences, 32 tokens 166 and 184 us, 48 tokens
 // 235 and 188.
 constexpr int kChunkMin = 32;
+static_assert(kChunkMin == 1 << 5, "a place every 32 tokens serves every sequence in chunks");
 
 struct Pk {
     Packed p;
@@ -56,13 +59,18 @@ struct Pk {
     int Hv, group;   // value heads; value heads per key head
     int rec_below;   // sequences of fewer tokens go token by token
     int seg_shift;   // a segment holds 2^seg_shift tokens
-    int64_t nslot;   // places for chunks
-    int64_t nseg;    // places for segments
+    Places places;   // of the chunks
+    int64_t nslot;   // so many of them
+    int64_t nseg;    // the most segments, of sequences in chunks
+    int64_t nstate;  // the most of sequences of two segments or more
+    int64_t nunit;   // the most workgroup-sets of their chains
     int32_t* order;  // sequences by falling length
     int32_t* first;  // [S + 1]: segments before each rank of that order
+    int32_t* sfirst; // [S + 1]: ... of sequences of two or more: their places
+    int32_t* ufirst; // [S + 1]: chain units before each rank: the blocks' places
     u16x8* T;        // [place, head][kTfrag]: T' as A operands
     float* G;        // [place, head][kGate]
-    float* s_end;    // [place, head][D][D]: end states of the state pass
+    float* s_end;    // [segment place, head][D][D]: end states of the state pass
     float* m_end;    // [place, head][D][D]: M transposed
     float* s_start;  // [place, head][D][D]: start states of the output pass
     bool two_level;  // long chains of start states run as a two-level scan:
@@ -538,6 +546,18 @@ __device__ __forceinline__ Split2 split2_8(const float (&x)[N], int at) {
     return {__builtin_bit_cast(u16x8, u32x4{h[0], h[1], h[2], h[3]}), __builtin_bit_cast(u16x8, u32x4{l[0], l[1], l[2], l[3]})};
 }
 
+// Segments of a sequence of n tokens, and the workgroup-sets of the chain
+// through ng > 1 of them: one, or one a block of maps where it runs as a
+// two-level scan (k_pk_chain)
+constexpr int kChainShift = 3, kChainLong = 32;  // maps a block; the fewest that go two-level
+__device__ __forceinline__ int64_t segments_of(const Pk& a, int64_t n) {
+    return (n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
+}
+__device__ __forceinline__ bool in_blocks(const Pk& a, int64_t ng) { return a.two_level && ng - 2 >= kChainLong; }
+__device__ __forceinline__ int64_t chain_units(const Pk& a, int64_t ng) {
+    return in_blocks(a, ng) ? (ng - 2 + (1 << kChainShift) - 1) >> kChainShift : 1;
+}
+
 // Per chunk and value head: the gate rows and T'.  One workgroup of four
 // waves each; K K^T on bf16 MFMA (exact operands), the inverse in fp32.  The
 // launch's first `recs` workgroups take the short sequences token by token:
@@ -556,7 +576,14 @@ __global__ __launch_bounds__(kThreads, 7) void k_pk_prep(Pk a, unsigned recs) {
     if (blockIdx.x == gridDim.x - 1) {  // one workgroup more: the segments' order
         order_sequences(a.at, a.order, reinterpret_cast<int*>(AT), tid, kThreads);
         __syncthreads();
-        count_segments(a.at, a.order, a.seg_shift, kChunkMin, a.first, reinterpret_cast<int*>(AT), tid, kThreads);
+        auto counts = [&](int s, uint32_t(&c)[3]) {
+            const int64_t n = span_of(a.at, s).n;
+            c[0] = n < kChunkMin ? 0 : (uint32_t)segments_of(a, n);
+            c[1] = c[0] > 1 ? c[0] : 0;
+            c[2] = c[0] > 1 ? (uint32_t)chain_units(a, c[0]) : 0;
+        };
+        int32_t* const out[3] = {a.first, a.sfirst, a.ufirst};
+        count_ranks<3>((int)p.S, a.order, counts, out, reinterpret_cast<uint32_t*>(AT), tid, kThreads);
         return;
     }
     if (blockIdx.x < recs) {
@@ -565,9 +592,9 @@ __global__ __launch_bounds__(kThreads, 7) void k_pk_prep(Pk a, unsigned recs) {
     }
     const unsigned id = on_one_xcd(blockIdx.x - recs, gridDim.x - 1 - recs, a.group);
     const int place = id / a.Hv, h = id - place * a.Hv, hk = h / a.group;
-    const int64_t s = seq_of_place(a.at, place, 6, l);
+    const int64_t s = seq_of_place(a.at, place, a.places, l);
     const Span sp = span_of(a.at, s);
-    const int64_t c = place - ((sp.begin >> 6) + s);
+    const int64_t c = place - a.places.first(sp.begin, s);
     if (sp.n < kChunkMin || c < 0 || c * C >= sp.n) return;
     const int64_t t0 = sp.begin + c * C;
     const int nt = (int)min<int64_t>(C, sp.n - c * C);
@@ -759,17 +786,18 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
     const int place_h = OUT ? block : block >> 1;
     const bool is_m = !OUT && (block & 1);
     const int i_seg = place_h / a.Hv, h = place_h - i_seg * a.Hv, hk = h / a.group;
-    if (i_seg >= a.first[p.S]) return;
-    const int64_t rank = rank_of_segment(a.first, p.S, i_seg, l), s = a.order[rank];
+    const int32_t* const first = OUT ? a.first : a.sfirst;
+    if (i_seg >= first[p.S]) return;
+    const int64_t rank = rank_holding(first, p.S, i_seg, l), s = a.order[rank];
     const Span sp = span_of(a.at, s);
-    const int64_t gi = i_seg - a.first[rank], ng = (sp.n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
-    // (counted apart from the lengths, which offsets out of order can overflow)
-    if (gi < 0 || gi >= ng) return;
+    const int64_t gi = i_seg - first[rank], ng = segments_of(a, sp.n);
     if (!OUT && (gi == ng - 1 || (is_m && gi == 0))) return;
-    const int64_t place = (sp.begin >> a.seg_shift) + s + gi;  // of the segment's states
+    const int64_t place = ng > 1 ? a.sfirst[rank] + gi : 0;  // of the segment's states
+    // (offsets out of order can hold more segments than N tokens can)
+    if (ng > 1 && place - gi + ng > a.nstate) return;
     const int64_t per = (int64_t)1 << (a.seg_shift - 6);       // chunks of a segment
     const int64_t i_begin = gi * per, i_end = min<int64_t>((sp.n + C - 1) / C, i_begin + per);
-    const int64_t cplace = (sp.begin >> 6) + s;  // the sequence's first chunk place
+    const int64_t cplace = a.places.first(sp.begin, s);  // the sequence's first chunk place
     const uint16_t* kin = static_cast<const uint16_t*>(p.k) + hk * D;
     const uint16_t* qin = static_cast<const uint16_t*>(p.q) + hk * D;
     const uint16_t* vin = static_cast<const uint16_t*>(p.v) + h * D + 32 * w;
@@ -1165,8 +1193,14 @@ __global__ __launch_bounds__(seg_threads<D>(), 2) void k_pk_seg(Pk a) {
 // loads, and a round of workgroups instead of two (190 -> 153 us at 127 maps
 // of 4 heads).  One level and two: 64 maps, D = 128, 150 and 101 us; at most
 // 25 maps, D = 64, 23 and 34 us.
-constexpr int kChainShift = 3, kChainLong = 32;  // maps a block; the fewest that go two-level
 enum { kCompose, kBlocks, kExpand };
+// The ranks that may hold chains in blocks: ranks fall by classes of length a
+// quarter of an octave wide, so none in front of a sequence of 33 segments has
+// fewer than 24.
+__host__ __device__ __forceinline__ int64_t block_ranks(const Packed& p, int shift) {
+    const int64_t most = p.N >> (shift + 4);
+    return p.S < most ? p.S : most;
+}
 template <int D, int MODE, int R>
 __global__ __launch_bounds__(4 * D, 2) void k_pk_chain(Pk a) {
     constexpr int NB = D / 16, LDX = D + 4;
@@ -1179,19 +1213,17 @@ __global__ __launch_bounds__(4 * D, 2) void k_pk_chain(Pk a) {
     const int j = blockIdx.x / 8, tile = j % WGS, id = (j / WGS) * 8 + blockIdx.x % 8;
     const int rt = tile % TILES * R;
     const bool is_p = MODE == kCompose && tile >= TILES;
-    const int64_t bshift = a.seg_shift + kChainShift;
-    const int64_t units = MODE == kBlocks ? p.S : (p.N >> bshift) + p.S;
-    const int place = id / a.Hv, h = id - place * a.Hv;
-    if (place >= units) return;
-    const int64_t s = MODE == kBlocks ? place : seq_of_place(a.at, place, (int)bshift, l);
-    const Span sp = span_of(a.at, s);
-    const int64_t ng = (sp.n + ((int64_t)1 << a.seg_shift) - 1) >> a.seg_shift;
-    if (sp.n < kChunkMin || ng < 2) return;
-    const int64_t base = (sp.begin >> a.seg_shift) + s, bbase = (sp.begin >> bshift) + s;
-    const bool two = a.two_level && ng - 2 >= kChainLong;
-    const int64_t nblk = two ? (ng - 2 + (1 << kChainShift) - 1) >> kChainShift : 1;
-    const int64_t blk = MODE == kBlocks ? 0 : place - bbase;
-    if (blk < 0 || blk >= nblk || (MODE != kExpand && !two)) return;
+    // units (the blocks' chains: sequences by rank, longest first)
+    const int64_t unit = id / a.Hv;
+    const int h = id - (int)unit * a.Hv;
+    if (unit >= (MODE == kBlocks ? block_ranks(p, a.seg_shift) : (int64_t)a.ufirst[p.S])) return;
+    const int64_t rank = MODE == kBlocks ? unit : rank_holding(a.ufirst, p.S, (int)unit, l), s = a.order[rank];
+    const int64_t ng = segments_of(a, span_of(a.at, s).n);
+    const bool two = in_blocks(a, ng);
+    if (ng < 2 || (MODE != kExpand && !two)) return;
+    const int64_t base = a.sfirst[rank], bbase = a.ufirst[rank], nblk = chain_units(a, ng);
+    if (base + ng > a.nstate || bbase + nblk > a.nunit) return;  // (as for the segments)
+    const int64_t blk = MODE == kBlocks ? 0 : unit - bbase;
     auto at = [&](float* pool, int64_t g) { return pool + ((base + g) * p.Hv + h) * D * D; };
     auto at_blk = [&](float* pool, int64_t b) { return pool + ((bbase + b) * p.Hv + h) * D * D; };
     // steps g0 .. g1 - 1: maps, or blocks of them
@@ -1315,13 +1347,38 @@ int64_t longest(const Packed& p) { return std::min(p.N, p.max_len); }
 // whether a sequence may have a chain that is worth two levels
 bool two_level(const Packed& p, int shift) { return longest(p) > (int64_t)(kChainLong + 1) << shift; }
 
+// What a batch has at most.  M sequences of more than 2^sh tokens (so M <= N /
+// 2^sh) have at most N / 2^sh + M segments together; their chains' units are no
+// more than one for each and one for eight segments, nor than N / 2^sh.
+struct PkSizes {
+    Places places;
+    int64_t nslot, nseg, nstate, nunit;
+};
+PkSizes sizes(const Packed& p, int shift) {
+    PkSizes z;
+    // (N / 64 + S places, or N / 32 where there are many sequences)
+    const int64_t by_seq = p.N / C + p.S, by_32 = p.N / kChunkMin;
+    z.places = by_seq <= by_32 ? chunk_places() : Places{5, 0};
+    z.nslot = std::min(by_seq, by_32);
+    const int64_t whole = p.N >> shift, m = std::min(p.S, whole);
+    z.nseg = whole + std::min(p.S, by_32);
+    z.nstate = whole + m;
+    z.nunit = std::min(whole, m + (z.nstate >> kChainShift));
+    return z;
+}
+// without segments every sequence is one, whatever its length (max_len is the
+// caller's word, the lengths are the device's)
+int shift_for(const Packed& p) { return longest(p) > (int64_t)1 << seg_shift_for(p) ? seg_shift_for(p) : kWhole; }
+
 struct PkLayout {
     size_t T, G, order, first, s_end, m_end, s_start, q_blk, p_blk, total;
 };
 PkLayout layout(const Packed& p) {
     PkLayout L{};
     if (!packed_in_chunks(p)) return L;
-    const size_t chunks = (size_t)(p.N / C + p.S) * (size_t)p.Hv;
+    const int sh = shift_for(p);
+    const PkSizes z = sizes(p, sh);
+    const size_t chunks = (size_t)(z.nslot * p.Hv);
     size_t off = 0;
     auto take = [&](size_t floats) {
         const size_t at = off;
@@ -1331,25 +1388,21 @@ PkLayout layout(const Packed& p) {
     L.T = take(chunks * kTfrag * 4);
     L.G = take(chunks * kGate);
     L.order = take((size_t)p.S);
-    L.first = take((size_t)p.S + 1);
-    const int sh = seg_shift_for(p);
-    if (longest(p) > ((int64_t)1 << sh)) {
-        const size_t states = (size_t)((p.N >> sh) + p.S) * (size_t)p.Hv * (size_t)(p.dk * p.dk);
-        L.s_end = take(states);
-        L.m_end = take(states);
-        L.s_start = take(states);
-        if (two_level(p, sh)) {
-            const size_t blocks = (size_t)((p.N >> (sh + kChainShift)) + p.S) * (size_t)p.Hv * (size_t)(p.dk * p.dk);
-            L.q_blk = take(blocks);
-            L.p_blk = take(blocks);
-        }
+    L.first = take(3 * ((size_t)p.S + 1));
+    const size_t states = (size_t)(z.nstate * p.Hv * p.dk * p.dk), blocks = (size_t)(z.nunit * p.Hv * p.dk * p.dk);
+    L.s_end = take(states);
+    L.m_end = take(states);
+    L.s_start = take(states);
+    if (two_level(p, sh)) {
+        L.q_blk = take(blocks);
+        L.p_blk = take(blocks);
     }
     L.total = off;
     return L;
 }
 
 template <int D>
-hipError_t launch_chunks(const Pk& a, bool segments, hipStream_t st) {
+hipError_t launch_chunks(const Pk& a, hipStream_t st) {
     const Packed& p = a.p;
     prof_begin(p.timer, "k_pk_prep", st);
     const unsigned recs = (unsigned)(p.S * p.Hv * (D / RecShared<GDN_BF16, kRecLPR, D / 64, kRecR, false>::RB));
@@ -1357,22 +1410,22 @@ hipError_t launch_chunks(const Pk& a, bool segments, hipStream_t st) {
     prof_end(p.timer, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(a.nseg * p.Hv)), states((unsigned)(2 * a.nseg * p.Hv)), block(seg_threads<D>());
-    if (segments) {
+    const dim3 grid((unsigned)(a.nseg * p.Hv)), states((unsigned)(2 * a.nstate * p.Hv)), block(seg_threads<D>());
+    if (a.nstate > 0) {
         prof_begin(p.timer, "k_pk_state", st);
         hipLaunchKernelGGL((k_pk_seg<D, false>), states, block, 0, st, a);
         prof_end(p.timer, st);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         // eight workgroup-sets at a time, for the eight XCDs
-        const int64_t blocks = ((p.N >> (a.seg_shift + kChainShift)) + p.S) * p.Hv;
+        const int64_t units = a.nunit * p.Hv;
         auto sets = [](int64_t n, int per) { return dim3((unsigned)((n + 7) / 8 * 8 * per)); };
         prof_begin(p.timer, "k_pk_chain", st);
         if (a.two_level) {
-            hipLaunchKernelGGL((k_pk_chain<D, kCompose, 2>), sets(blocks, D / 16), dim3(4 * D), 0, st, a);
-            hipLaunchKernelGGL((k_pk_chain<D, kBlocks, 1>), sets(p.S * p.Hv, D / 16), dim3(4 * D), 0, st, a);
-            hipLaunchKernelGGL((k_pk_chain<D, kExpand, 2>), sets(blocks, D / 32), dim3(4 * D), 0, st, a);
+            hipLaunchKernelGGL((k_pk_chain<D, kCompose, 2>), sets(units, D / 16), dim3(4 * D), 0, st, a);
+            hipLaunchKernelGGL((k_pk_chain<D, kBlocks, 1>), sets(block_ranks(p, a.seg_shift) * p.Hv, D / 16), dim3(4 * D), 0, st, a);
+            hipLaunchKernelGGL((k_pk_chain<D, kExpand, 2>), sets(units, D / 32), dim3(4 * D), 0, st, a);
         } else {
-            hipLaunchKernelGGL((k_pk_chain<D, kExpand, 1>), sets(blocks, D / 16), dim3(4 * D), 0, st, a);
+            hipLaunchKernelGGL((k_pk_chain<D, kExpand, 1>), sets(units, D / 16), dim3(4 * D), 0, st, a);
         }
         prof_end(p.timer, st);
         if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1413,23 +1466,26 @@ hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st) {
         return e;
     }
     char* base = static_cast<char*>(ws);
-    // without segments every sequence is one, whatever its length (max_len
-    // is the caller's word, the lengths are the device's)
-    const bool segments = longest(p) > ((int64_t)1 << seg_shift_for(p));
-    a.seg_shift = segments ? seg_shift_for(p) : kWhole;
-    a.nslot = p.N / C + p.S;
-    a.nseg = (p.N >> a.seg_shift) + p.S;
+    a.seg_shift = shift_for(p);
+    const PkSizes z = sizes(p, a.seg_shift);
+    a.places = z.places;
+    a.nslot = z.nslot;
+    a.nseg = z.nseg;
+    a.nstate = z.nstate;
+    a.nunit = z.nunit;
     a.T = reinterpret_cast<u16x8*>(base + L.T);
     a.order = reinterpret_cast<int32_t*>(base + L.order);
     a.first = reinterpret_cast<int32_t*>(base + L.first);
+    a.sfirst = a.first + p.S + 1;
+    a.ufirst = a.sfirst + p.S + 1;
     a.G = reinterpret_cast<float*>(base + L.G);
     a.s_end = reinterpret_cast<float*>(base + L.s_end);
     a.m_end = reinterpret_cast<float*>(base + L.m_end);
     a.s_start = reinterpret_cast<float*>(base + L.s_start);
-    a.two_level = segments && two_level(p, a.seg_shift);
+    a.two_level = two_level(p, a.seg_shift);
     a.q_blk = reinterpret_cast<float*>(base + L.q_blk);
     a.p_blk = reinterpret_cast<float*>(base + L.p_blk);
-    return p.dk == 64 ? launch_chunks<64>(a, segments, st) : launch_chunks<128>(a, segments, st);
+    return p.dk == 64 ? launch_chunks<64>(a, st) : launch_chunks<128>(a, st);
 }
 
 }  // namespace gdn

@@ -1,10 +1,12 @@
 // Where packed sequences and their chunks lie, shared by the packed forward
 // (gdn_packed.hip) and backward (gdn_bwd_chunk.hip).  Internal to libgdn.
 //
-// Lengths are known on the device only.  Chunks (or segments) of 2^shift
-// tokens of sequence s get consecutive places from cu[s] / 2^shift + s on:
-// ceil(n / 2^shift) of them never reach the next sequence's first place, and
-// N / 2^shift + S places are enough, so no kernel has to lay out a table.
+// Lengths are known on the device only.  Chunks of 64 tokens of sequence s get
+// consecutive places from cu[s] / 64 + s on: ceil(n / 64) of them never reach
+// the next sequence's first place, and N / 64 + S places are enough, so no
+// kernel has to lay out a table.  Where only sequences of 32 tokens or more
+// have chunks, cu[s] / 32 serves as well, with N / 32 places however many
+// shorter ones there are: ceil(n / 64) <= floor(n / 32) from n = 32 on.
 // Offsets are clamped to 0 .. N and to rising order, so no content of cu leads
 // out of bounds.
 #pragma once
@@ -31,16 +33,23 @@ __device__ __forceinline__ Span span_of(const Offsets& p, int64_t s) {
     const int64_t a = cu_at(p, s), b = cu_at(p, s + 1);
     return {a, b > a ? b - a : 0};
 }
-// The sequence whose places hold `place` (2^shift tokens a place), found by
-// a whole wave: 64 candidates a round.
-__device__ __forceinline__ int64_t seq_of_place(const Offsets& p, int64_t place, int shift, int lane) {
+// The rule of the chunks' places
+struct Places {
+    int shift;  // 6: cu / 64 + s; 5: cu / 32
+    int each;   // 1; 0
+    __device__ int64_t first(int64_t begin, int64_t s) const { return (begin >> shift) + s * each; }
+};
+__host__ __device__ __forceinline__ Places chunk_places() { return {6, 1}; }
+// The sequence whose places hold `place`, found by a whole wave: 64 candidates
+// a round.
+__device__ __forceinline__ int64_t seq_of_place(const Offsets& p, int64_t place, const Places& rule, int lane) {
     int64_t lo = 0, cnt = p.S;
     while (cnt > 1) {
         const int64_t step = (cnt + 63) >> 6;
         bool le = false;
         if (lane * step < cnt) {
             const int64_t s = lo + lane * step;
-            le = (cu_at(p, s) >> shift) + s <= place;
+            le = rule.first(cu_at(p, s), s) <= place;
         }
         // (the count is unsigned: none of them has to give 0 too, as in front
         // of the first sequence)
@@ -80,38 +89,53 @@ __device__ __forceinline__ void order_sequences(const Offsets& p, int32_t* order
     for (int64_t s = tid; s < p.S; s += threads)
         order[atomicAdd(&hist[kLenClasses + len_class(span_of(p, s).n)], 1)] = (int32_t)s;
 }
-// Segments of 2^shift tokens of sequences of at least min_len tokens, counted
-// over the sequences in that order: first[r] those before rank r, first[S] all
-// of them.  By the workgroup that ordered them; sums: `threads` ints of LDS.
-__device__ __forceinline__ void count_segments(const Offsets& p, const int32_t* order, int shift, int64_t min_len,
-                                               int32_t* first, int* sums, int tid, int threads) {
-    const int64_t run = (p.S + threads - 1) / threads, r0 = tid * run, r1 = min(r0 + run, p.S);
-    auto segments = [&](int64_t r) {
-        const int64_t n = span_of(p, order[r]).n;
-        return n < min_len ? 0 : (int)((n + ((int64_t)1 << shift) - 1) >> shift);
-    };
-    int mine = 0;
-    for (int64_t r = r0; r < r1; ++r) mine += segments(r);
-    sums[tid] = mine;
-    __syncthreads();
-    if (tid == 0) {
-        int at = 0;
-        for (int i = 0; i < threads; ++i) {
-            const int x = sums[i];
-            sums[i] = at;
-            at += x;
+// K counts of every sequence, counts(s, c), summed over the sequences in that
+// order: out[k][r] those before rank r, out[k][S] all of them, INT32_MAX where
+// there are more (lengths of offsets out of order can sum to any number).  By
+// the workgroup that ordered them; sums: K a wave in LDS.
+__device__ __forceinline__ uint32_t add_up_to_max(uint32_t a, uint32_t b) { return min(a + b, (uint32_t)INT32_MAX); }
+template <int K, class F>
+__device__ __forceinline__ void count_ranks(int S, const int32_t* order, F counts, int32_t* const (&out)[K],
+                                            uint32_t* sums, int tid, int threads) {
+    const int run = (S + threads - 1) / threads, r0 = min(tid * run, S), r1 = min(r0 + run, S);
+    const int w = tid >> 6, lane = tid & 63;
+    uint32_t at[K] = {}, c[K];
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+        counts(order[r], c);
+#pragma unroll
+        for (int k = 0; k < K; ++k) at[k] = add_up_to_max(at[k], c[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t y = __shfl_up(at[k], o, 64);
+            if (lane >= o) at[k] = add_up_to_max(at[k], y);
         }
-        first[p.S] = at;
+        if (lane == 63) sums[w * K + k] = at[k];
+        at[k] = __shfl_up(at[k], 1, 64);
+        if (lane == 0) at[k] = 0;
     }
     __syncthreads();
-    int at = sums[tid];
-    for (int64_t r = r0; r < r1; ++r) {
-        first[r] = at;
-        at += segments(r);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        for (int i = 0; i < w; ++i) at[k] = add_up_to_max(at[k], sums[i * K + k]);
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+        counts(order[r], c);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            out[k][r] = (int32_t)at[k];
+            at[k] = add_up_to_max(at[k], c[k]);
+        }
+    }
+    if (tid == threads - 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) out[k][S] = (int32_t)at[k];
     }
 }
-// The rank whose segments hold the i-th (i < first[S]), by a whole wave.
-__device__ __forceinline__ int64_t rank_of_segment(const int32_t* first, int64_t S, int i, int lane) {
+// The rank whose things hold the i-th (i < first[S]), by a whole wave.
+__device__ __forceinline__ int64_t rank_holding(const int32_t* first, int64_t S, int i, int lane) {
     int64_t lo = 0, cnt = S;
     while (cnt > 1) {
         const int64_t step = (cnt + 63) >> 6;

@@ -476,3 +476,57 @@ def test_single_tokens(dk, dv, gate, dtype):
         c.fresh = ()
         out, pool = run(c, max_len=1, inplace=True)
         check(c, out, pool, inplace=True)
+
+
+def guarded(n, dtype, fill, rim=4096):
+    """n elements within a filled buffer, and a check that nothing around them changed."""
+    import torch
+    whole = torch.full((n + 2 * rim,), fill, dtype=dtype, device="cuda")
+    return whole[rim:rim + n], lambda: bool((whole[:rim] == fill).all() and (whole[-rim:] == fill).all())
+
+
+@pytest.mark.parametrize("lengths,d,hv", [
+    ((1,) * 90 + (33,), 64, 2),                                            # single tokens and one chunk
+    ((1,) * 60 + (700,) + (2, 0, 31) * 30 + (32, 1300), 128, 4),           # two prompts of several segments
+    ((40, 33, 64, 31) * 12 + (1,) * 150 + (900, 257, 129), 64, 4),
+    ((3,) * 300 + (6000,) + (1,) * 100 + (40, 300), 64, 1),                # a chain in two levels, one in one
+    ((3,) * 100 + (10000,) + (1,) * 300 + (400, 9000), 128, 1),
+])
+def test_many_short_sequences_beside_prompts(lengths, d, hv):
+    """Sequences without chunks or segments have no places in the workspace."""
+    import torch
+    c = Packed(lengths, 1, hv, d, d, seed=43, slots=1, alpha_mean=5.0).make()
+    n = gdn.gdn_packed_workspace_bytes(sum(lengths), len(lengths), 1, hv, d, d, sum(lengths), gdn.GDN_BF16, 0)
+    ws, untouched = guarded(n, torch.uint8, 0xA5)
+    check(c, *run(c, workspace=ws))
+    assert untouched()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S", [3, 40])
+def test_bad_offsets_and_slots_write_nothing_else(S, d):
+    """Offsets and slots of any value: nothing outside the outputs, the pool and
+    the workspace, and no slot that the call does not name."""
+    import torch
+    N, hv = 3000, 2
+    r = np.random.Generator(np.random.PCG64(44))
+    c = Packed((N,), 1, hv, d, d, seed=44).make()
+    t = {n: c.cuda(n) for n in ("q", "k", "v", "alpha", "beta")}
+    state = hv * d * d
+    for cu in ([0, N] * S, [N, 0] * S, [0] * (2 * S) + [2**31 - 1], [-2**31] + [2**31 - 1] * (2 * S),
+               list(r.integers(-10, N + 10, 2 * S))):
+        cu = cu[:S + 1]
+        slots = r.choice([-1, -2**31, 2**31 - 1, S + 2, 5], S)
+        slots[0] = 1
+        pool, pool_whole = guarded((S + 2) * state, torch.float32, 7.0)
+        out, out_whole = guarded(N * hv * d, torch.bfloat16, 7.0)
+        n = gdn.gdn_packed_workspace_bytes(N, S, 1, hv, d, d, N, gdn.GDN_BF16, 0)
+        ws, ws_whole = guarded(n, torch.uint8, 0xA5)
+        print("offsets", cu[:6], "slots", slots[:6], flush=True)
+        cu, slots = (torch.tensor(np.array(x), dtype=torch.int32).cuda() for x in (cu, slots))
+        gdn.packed_fwd(t["q"], t["k"], t["v"], t["alpha"], t["beta"], cu, c.cuda("pool"), slots, pool.view(S + 2, hv, d, d),
+                       slots, out=out.view(N, hv, d), workspace=ws)
+        torch.cuda.synchronize()
+        assert pool_whole() and out_whole() and ws_whole()
+        rest = [s for s in range(S + 2) if s not in (1, 5)]
+        assert (pool.view(S + 2, -1)[rest] == 7.0).all()

@@ -159,3 +159,22 @@ def test_packed_backward_workspace():
     one, shared = ws(1000, 2, 4, 4, 64, 64, 1, 0), ws(1000, 2, 2, 4, 64, 64, 1, 0)
     assert shared == one + 2 * (1000 * 4 * 64 * 4)
     assert ws(1 << 20, 1, 64, 64, 128, 128, 1, 0) <= (8 << 30) + (1 << 20)  # heads in groups
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,Hv", [(1024, 32), (5120, 16), (16384, 16), (65531, 4), (4096, 1)])
+def test_packed_workspace_does_not_grow_with_short_sequences(N, Hv, d):
+    """Sequences that no chunk kernel or segment serves need offsets and counts
+    alone: at most three times the workspace of one sequence of N tokens (chunks of
+    32 to 64 tokens, segments more than half full) and 20 bytes a sequence."""
+    ws = gdn.gdn_packed_workspace_bytes
+    one = ws(N, 1, Hv, Hv, d, d, N, 1, 0)
+    for S in (2, 40, N // 8, N, 2**19 // Hv):
+        assert 0 < ws(N, S, Hv, Hv, d, d, N, 1, 0) <= 3 * one + 20 * S + 4096, S
+
+
+def test_packed_workspace_of_a_server_step():
+    """Single tokens beside a prompt, and alone with no bound on their lengths given."""
+    ws = gdn.gdn_packed_workspace_bytes
+    assert ws(1024, 1024, 32, 32, 128, 128, 1024, 1, 0) < 64 << 20
+    assert ws(5120, 1025, 16, 16, 128, 128, 4096, 1, 0) < 256 << 20
