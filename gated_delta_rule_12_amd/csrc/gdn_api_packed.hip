@@ -14,7 +14,6 @@ bool dim_ok(int64_t d) { return d >= 16 && d <= 128 && d % 16 == 0; }
 // sequence and head token by token; 8 x 512 a sequence and head and, beside
 // those, 8 x 512 a head and 2048 tokens or 256 a head and 64 tokens in chunks.
 constexpr int64_t kMaxStates = (int64_t)1 << 21, kMaxChunkStates = (int64_t)1 << 19, kMaxChunkRows = (int64_t)1 << 28;
-constexpr int64_t kMaxCols = 16384;
 constexpr int64_t kMaxStride = (int64_t)1 << 23;
 
 int packed_check(const Packed& p) {
@@ -130,7 +129,7 @@ int packed_bwd_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, 
 int norm_check(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype) {
     if ((x_dtype != GDN_F32 && x_dtype != GDN_BF16) || (y_dtype != GDN_F32 && y_dtype != GDN_BF16)) return GDN_E_ARG;
     if (rows < 0 || n <= 0 || rows > ((int64_t)1 << 40)) return GDN_E_SHAPE;
-    if (n > kMaxCols) return GDN_E_UNSUPPORTED;
+    if (n > kLayerNormMaxCols) return GDN_E_UNSUPPORTED;
     return GDN_OK;
 }
 bool elem_aligned(const void* ptr, int32_t dtype) { return aligned(ptr, dtype == GDN_BF16 ? 2 : 4); }

@@ -174,6 +174,7 @@ size_t packed_backward_workspace(const Packed& p);
 hipError_t packed_backward(const PackedBwd& b, void* ws, hipStream_t st);
 
 // Layer norm (gdn_norm.hip).
+constexpr int64_t kLayerNormMaxCols = 16384;
 struct LayerNorm {
     int64_t rows, n;
     int x_dtype, y_dtype;  // of x and dx; of y and dy

@@ -369,7 +369,7 @@ int ln_rows_per_block(int tpr) { return tpr > 256 ? 1 : 256 / tpr; }
 struct LnShape {
     int tpr, nv;
 };
-LnShape ln_shape(int64_t n, int v) {
+constexpr LnShape ln_shape(int64_t n, int v) {
     const int64_t nvec = (n + v - 1) / v;
     if (nvec <= 8) return {8, 1};
     if (nvec <= 16) return {8, 2};
@@ -384,6 +384,15 @@ LnShape ln_shape(int64_t n, int v) {
     if (nvec <= 8192) return {1024, 8};
     return {1024, 16};
 }
+// Whether any width takes TPR threads and NV vectors of v elements (the
+// shapes change at powers of two of vectors, and the widest row is one)
+constexpr bool ln_taken(int v, int tpr, int nv) {
+    for (int64_t nvec = 8; nvec * v <= kLayerNormMaxCols; nvec *= 2) {
+        const LnShape s = ln_shape(nvec * v, v);
+        if (s.tpr == tpr && s.nv == nv) return true;
+    }
+    return false;
+}
 int64_t ln_groups(int64_t rows, int tpr) {
     const int64_t rpb = ln_rows_per_block(tpr);
     return std::min<int64_t>((rows + rpb - 1) / rpb, tpr > 256 ? kMaxGroups / 2 : kMaxGroups);
@@ -391,8 +400,8 @@ int64_t ln_groups(int64_t rows, int tpr) {
 
 template <int XT, int YT, int V, int TPR, int NV>
 hipError_t launch(const LnArgs& a, bool bwd, hipStream_t st) {
-    if constexpr (NV * V > 32) {
-        return hipErrorInvalidValue;  // (no shape within kMaxCols asks for it)
+    if constexpr (!ln_taken(V, TPR, NV)) {
+        return hipErrorInvalidValue;  // (never asked for)
     } else {
         const int64_t blocks = (a.rows + ln_rows_per_block(TPR) - 1) / ln_rows_per_block(TPR);
         if (bwd)
