@@ -8,10 +8,13 @@
 //   g  = dy w,  dx = r (g - mean g - xhat mean(g xhat))
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy.
 //
-// Both directions are one pass over memory: a row sits in the registers of
-// TPR threads (NV vectors of V elements each) between its load and its store,
-// so x (and dy) are read once and y (dx) is written once, and the variance is
-// taken from the centred values, not from a difference of sums.  Rows of up
+// Both directions are one pass over x, dy, y and dx: a row sits in the
+// registers of TPR threads (NV vectors of V elements each) between its load and
+// its store, and the variance is taken from the centred values, not from a
+// difference of sums.  (Workgroups of 1024 threads have 128 registers a thread.
+// Backward rows of more than 8192 elements need more and spill: 30 to 65 of
+// them in vectors, 94 to 100 element by element, which forward spills 8 to 10.)
+// Rows of up
 // to 1024 elements (4 a vector) stay within a wave and reduce across lanes on
 // the vector ALU; longer rows take a workgroup and one exchange through LDS
 // per sum.  All statistics and sums are fp32.
@@ -22,10 +25,17 @@
 // adds the partial rows.  Every sum has a fixed order (no atomics), so
 // repeated calls give identical results.
 //
-// Bound by memory: 262144 x 128 (fp32 in, bf16 out) forward 39 us for 203 MB
-// (5.2 TB/s; 31.5 us where the input is still in the last-level cache),
-// backward 63 us for 338 MB (5 of them k_ln_params); 16381 x 2048 bf16
-// backward 45 us for 201 MB.
+// Whole vectors are bound by memory: 262144 x 128 (fp32 in, bf16 out) forward
+// 39 us for 203 MB (5.2 TB/s; 31.5 us where the input is still in the last-level
+// cache), backward 63 us for 338 MB (5 of them k_ln_params); 16381 x 2048 bf16
+// backward 45 us for 201 MB.  Element by element it is the instructions (two
+// bytes a load, and four to eight times the threads a row), and beyond 8192
+// columns the spills; forward and backward TB/s (the kernels alone, inputs in
+// turn from three buffers):
+//   262144 x 128 fp32 -> bf16 5.4 and 4.9; x 127 2.7 and 2.6
+//   16381 x 2048 bf16 4.8 and 4.7; x 2047 2.8 and 3.0
+//   4095 x 8192 bf16 4.7 and 3.7; x 8191 2.6 and 3.3
+//   4095 x 12288 bf16 4.4 and 1.9; x 12287 1.9 and 0.8
 #include "gdn_internal.h"
 #include "../../include/gdn.h"
 

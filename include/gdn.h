@@ -405,16 +405,19 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
                                            int64_t dv, int32_t dtype, int32_t gate);
 
 /*
- * gdn_layer_norm_fwd — layer norm of rows of n elements, as the DeltaNet
- * block normalises the heads' outputs (rows of dv) and its input (rows of
- * model width): y = (x - mean) rstd weight + bias, rstd = 1 / sqrt(var + eps),
- * var the mean of (x - mean)^2.  One pass over x; statistics in fp32.
+ * gdn_layer_norm_fwd — layer norm of rows of n elements, for blocks that
+ * normalise the heads' outputs (rows of dv) or their input (rows of model
+ * width) by it; the notes' DeltaNet block has an RMS norm and an output gate
+ * there, which this is not: y = (x - mean) rstd weight + bias, rstd = 1 /
+ * sqrt(var + eps), var the mean of (x - mean)^2.  One pass over x; statistics
+ * in fp32.
  *   x           [rows, n], x_dtype;  y [rows, n], y_dtype (rounded once)
  *   weight      [n] fp32 or NULL (ones);  bias [n] fp32 or NULL (zeros)
  *   mean, rstd  [rows] fp32, what the backward takes, or NULL: not wanted
  * y may equal x (same dtype).  Pointers aligned to their elements; rows of a
  * multiple of 8 (bf16 to bf16) or 4 elements with 16-byte aligned pointers
- * move in whole vectors, others element by element.  n <= 16384, else
+ * move in whole vectors, others element by element (about half as fast up to
+ * 8192 columns, down to a quarter beyond).  n <= 16384, else
  * GDN_E_UNSUPPORTED.
  */
 int gdn_layer_norm_fwd(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps,
