@@ -568,6 +568,10 @@ def _packed_check(q, k, v, alpha, beta, cu_seqlens, pools, slots):
     for t in slots:
         if t is not None and t.shape != (S,):
             raise ValueError("slots must be [S]")
+    for t, i in zip(pools, slots):
+        # (an empty tensor has no address, which would stand for no pool)
+        if t is not None and i is None and t.shape[0] == 0 < S * Hv:
+            raise GdnError(GDN_E_SHAPE, "a state pool without slots' indices")
     dev = q.get_device()
     _on(alpha, dev, f32, "alpha")
     _on(beta, dev, f32, "beta")

@@ -416,8 +416,8 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  *   mean, rstd  [rows] fp32, what the backward takes, or NULL: not wanted
  * y may equal x (same dtype).  Pointers aligned to their elements; rows of a
  * multiple of 8 (bf16 to bf16) or 4 elements with 16-byte aligned pointers
- * move in whole vectors, others element by element (about half as fast up to
- * 8192 columns, down to a quarter beyond).  n <= 16384, else
+ * move in whole vectors, others element by element (about half as fast).
+ * n <= 16384, else
  * GDN_E_UNSUPPORTED.
  */
 int gdn_layer_norm_fwd(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps,

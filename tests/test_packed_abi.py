@@ -178,3 +178,16 @@ def test_packed_workspace_of_a_server_step():
     ws = gdn.gdn_packed_workspace_bytes
     assert ws(1024, 1024, 32, 32, 128, 128, 1024, 1, 0) < 64 << 20
     assert ws(5120, 1025, 16, 16, 128, 128, 4096, 1, 0) < 256 << 20
+
+
+def test_an_empty_pool_without_slots_is_refused():
+    """A pool of no slots holds no sequence; it is not the same as no pool."""
+    import torch
+    z = torch.zeros
+    q, v, a = z(10, 2, 64, dtype=torch.bfloat16), z(10, 4, 64, dtype=torch.bfloat16), z(10, 4)
+    cu, none = torch.tensor([0, 4, 10], dtype=torch.int32), z(0, 4, 64, 64)
+    for call in (lambda: gdn.packed_fwd(q, q, v, a, a, cu, none), lambda: gdn.packed_fwd(q, q, v, a, a, cu, None, None, none),
+                 lambda: gdn.packed_backward(q, q, v, a, a, cu, none, None, v)):
+        with pytest.raises(gdn.GdnError) as e:
+            call()
+        assert e.value.status == SHAPE
