@@ -562,16 +562,17 @@ def _packed_check(q, k, v, alpha, beta, cu_seqlens, pools, slots):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [S+1]")
     S = cu_seqlens.shape[0] - 1
-    for t in pools:
-        if t is not None and (t.dim() != 4 or t.shape[1:] != (Hv, dv, dk)):
-            raise ValueError("state pools must be [slots,Hv,dv,dk]")
+    for t, i in zip(pools, slots):
+        if t is not None:
+            pool = t.shape
+            if len(pool) != 4 or pool[1:] != (Hv, dv, dk):
+                raise ValueError("state pools must be [slots,Hv,dv,dk]")
+            # (an empty tensor has no address, which would stand for no pool)
+            if pool[0] == 0 and i is None and S * Hv:
+                raise GdnError(GDN_E_SHAPE, "an empty state pool without slots")
     for t in slots:
         if t is not None and t.shape != (S,):
             raise ValueError("slots must be [S]")
-    for t, i in zip(pools, slots):
-        # (an empty tensor has no address, which would stand for no pool)
-        if t is not None and i is None and t.shape[0] == 0 < S * Hv:
-            raise GdnError(GDN_E_SHAPE, "a state pool without slots' indices")
     dev = q.get_device()
     _on(alpha, dev, f32, "alpha")
     _on(beta, dev, f32, "beta")
