@@ -57,7 +57,7 @@ struct Pk {
     Packed p;
     Offsets at;
     int Hv, group;   // value heads; value heads per key head
-    int rec_below;   // sequences of fewer tokens go token by token
+    int64_t rec_below;  // sequences of fewer tokens go token by token
     int seg_shift;   // a segment holds 2^seg_shift tokens
     Places places;   // of the chunks
     int64_t nslot;   // so many of them
@@ -1454,7 +1454,7 @@ hipError_t packed_forward(const Packed& p, void* ws, hipStream_t st) {
     a.group = (int)(p.Hv / p.Hk);
     const PkLayout L = layout(p);
     const bool chunks = L.total > 0;
-    a.rec_below = chunks ? kChunkMin : INT32_MAX;
+    a.rec_below = chunks ? kChunkMin : INT64_MAX;  // (a sequence may have INT32_MAX tokens)
     if (!chunks) {
         prof_begin(p.timer, "k_pk_rec", st);
         hipError_t e;
