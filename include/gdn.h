@@ -384,9 +384,10 @@ int gdn_packed_path(int64_t dk, int64_t dv, int32_t dtype, int32_t gate);
  *                   (sequences that share a slot each have their own); NULL:
  *                   not wanted
  *   workspace       gdn_packed_backward_workspace_bytes(...): per value head
- *                   and chunk as gdn_backward, capped at about 8 GiB (more
- *                   heads run in groups), 4 S, and with shared key heads
- *                   twice 4 N Hv dk
+ *                   and chunk as gdn_backward, for N / 64 + S chunks, capped at
+ *                   about 8 GiB (more heads run in groups, one key head's value
+ *                   heads at least), 4 S, and with shared key heads twice
+ *                   4 N Hv dk
  * Alignment: as gdn_packed_fwd; the gradients on 16 bytes, grad_alpha and
  * grad_beta on 4.
  */
@@ -417,8 +418,7 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  * y may equal x (same dtype).  Pointers aligned to their elements; rows of a
  * multiple of 8 (bf16 to bf16) or 4 elements with 16-byte aligned pointers
  * move in whole vectors, others element by element (about half as fast).
- * n <= 16384, else
- * GDN_E_UNSUPPORTED.
+ * n <= 16384, else GDN_E_UNSUPPORTED.
  */
 int gdn_layer_norm_fwd(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps,
                        const void* x, const float* weight, const float* bias, void* y,
