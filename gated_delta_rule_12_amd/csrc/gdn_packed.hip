@@ -28,9 +28,12 @@
 //     the sequence-parallel notes' increment and correction, as a two-level
 //     scan where it is long) and the output pass from the true start states.
 // Measured (bf16, D = 128): 40 sequences of very different lengths, 16384
-// tokens, 16 value heads, 309 us (prep 62, state pass 76, chain 28, outputs
-// 140 to 150; the bytes alone 47 us); one of 65531, 4 heads, 391 us (46, 112,
-// 101, 139; bytes 45 us).
+// tokens, 16 value heads, 298 us a call (preparation 64, state pass 76, chain
+// 18, outputs 148; the bytes alone 47 us); one of 65531, 4 heads, 394 us (47,
+// 119, 103, 148; bytes 45 us).  (Calls are timed with inputs that are not in the
+// caches; kernels are averages under the profiler, which adds some percent.
+// Two figures of a change, below, are event times of the two builds as they
+// were then, not parts of these totals.)
 // Chunks have their places by rule (gdn_packed_common.h), segments theirs by
 // counts that the preparation's launch makes: only sequences longer than a
 // segment have states of segments, so that short ones cost no workspace.
@@ -407,7 +410,9 @@ hipError_t launch_rec_shape(const Pk& a, hipStream_t st) {
     // of 128, lanes a row x rows a thread 32 x 1, 16 x 1, 16 x 2: 16 states, 1000
     // tokens 233, 269, 391 us; 256 states, 100 tokens 125, 102, 107 us; 4096, 8
     // tokens 201, 167, 155 us.  Heads of 64, 16 x 1 and 16 x 2: 16 states 231 and
-    // 294 us, 1024 of 30 tokens 39 and 43, 4096 of 8 tokens 50 and 46.
+    // 294 us, 1024 of 30 tokens 39 and 43, 4096 of 8 tokens 50 and 46.  (The
+    // borders lie somewhere between these; bf16 and channel gates, which were not
+    // timed so, take the same.)
     const int64_t states = a.p.S * a.p.Hv;
     if (pieces <= 16) {
         if (states <= 1024)
@@ -1326,7 +1331,10 @@ __global__ __launch_bounds__(4 * D, 2) void k_pk_chain(Pk a) {
 }
 
 // Tokens of a segment, as a power of two: as many segments as there are
-// compute units over all heads, at least four chunks each.  Twice as many run
+// compute units over all heads, at least four chunks each.  Rounded up, so just
+// past a power of two there are half as many, each twice as long, and a call
+// takes a quarter to two fifths longer (one of 65536 and 65600 tokens, 4 heads:
+// 419 and 526 us; of 16384 and 16400, 16 heads: 337 and 469).  Twice as many run
 // the output pass two workgroups a compute unit (one of 65531 tokens, 4 heads:
 // outputs 113 instead of 139 us), but have twice the matrices to multiply
 // through the chain (153 instead of 101 us); mixed batch of 16384, 16 heads:
