@@ -28,11 +28,12 @@
 //     the sequence-parallel notes' increment and correction, as a two-level
 //     scan where it is long) and the output pass from the true start states.
 // Measured (bf16, D = 128): 40 sequences of very different lengths, 16384
-// tokens, 16 value heads, 298 us a call (preparation 64, state pass 76, chain
+// tokens, 16 value heads, 298 us a call (preparation 64, state pass 77, chain
 // 18, outputs 148; the bytes alone 47 us); one of 65531, 4 heads, 394 us (47,
-// 119, 103, 148; bytes 45 us).  (Calls are timed with inputs that are not in the
-// caches; kernels are averages under the profiler, which adds some percent.
-// Two figures of a change, below, are event times of the two builds as they
+// 118, 103, 147; bytes 45 us).  (Calls are timed with inputs that are not in the
+// caches; kernels are averages under the profiler, which adds some percent, and
+// differ by a microsecond or two from one trace to the next.  Two figures of a
+// change, below, are event times of the two builds as they
 // were then, not parts of these totals.)
 // Chunks have their places by rule (gdn_packed_common.h), segments theirs by
 // counts that the preparation's launch makes: only sequences longer than a
