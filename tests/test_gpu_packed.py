@@ -530,3 +530,19 @@ def test_bad_offsets_and_slots_write_nothing_else(S, d):
         assert pool_whole() and out_whole() and ws_whole()
         rest = [s for s in range(S + 2) if s not in (1, 5)]
         assert (pool.view(S + 2, -1)[rest] == 7.0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_non_finite_rows_outside_the_sequences(d):
+    """Rows in front of the first and behind the last sequence are not read."""
+    import torch
+    c = Packed((70, 1, 500, 33), 1, 2, d, d, seed=45, tail=70).make()
+    t = {n: c.cuda(n) for n in ("q", "k", "v", "alpha", "beta", "cu", "pool", "slots_in")}
+    call = lambda: gdn.packed_fwd(t["q"], t["k"], t["v"], t["alpha"], t["beta"], t["cu"][1:], t["pool"],  # noqa: E731
+                                  t["slots_in"][1:])
+    out, pool = call()
+    for n in ("q", "k", "v", "alpha", "beta"):
+        t[n][:70], t[n][604:] = np.nan, np.inf
+    again, pool2 = call()
+    torch.cuda.synchronize()
+    assert torch.equal(out[70:604], again[70:604]) and torch.equal(pool, pool2)

@@ -312,3 +312,24 @@ def test_without_sequences_every_row_is_zero(d):
                                            t["dout"][:, :0].contiguous())
     torch.cuda.synchronize()
     assert (dq == 0).all() and (dkk == 0).all() and dvv.shape == (70, 0, d)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (128, "f32")])
+def test_non_finite_values_stay_where_they_are(d, dtype):
+    """Rows outside the sequences are not read, and what is not finite in one
+    sequence leaves the others' gradients as they are, bit for bit."""
+    import torch
+    c = Packed((70, 1, 130, 33), 1, 2, d, d, dtype=dtype, seed=52, tail=70).make()
+    t = tensors(c)
+    t.update(cu=t["cu"][1:], slots_in=t["slots_in"][1:], dstate=t["dstate"][1:].contiguous())
+    first = run(c, t)
+    for n in ("q", "k", "v", "alpha", "beta", "dout"):
+        t[n][:70], t[n][234:] = np.nan, np.inf
+    for x, y in zip(first, run(c, t)):
+        assert torch.equal(x, y)
+    t["v"][71 + 65, 1, 3], t["dout"][71 + 100, 0, 2] = np.inf, np.nan  # the second of three sequences
+    for name, x, y in zip(NAMES, first, run(c, t)):
+        if name == "dstate0":
+            assert torch.equal(x[0], y[0]) and torch.equal(x[2], y[2]) and not torch.isfinite(y[1]).all()
+        else:
+            assert torch.equal(x[:71], y[:71]) and torch.equal(x[201:], y[201:]) and not torch.isfinite(y[71:201]).all(), name
