@@ -418,7 +418,9 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  * y may equal x (same dtype).  Pointers aligned to their elements; rows of a
  * multiple of 8 (bf16 to bf16) or 4 elements with 16-byte aligned pointers
  * move in whole vectors, others element by element (about half as fast).
- * n <= 16384, else GDN_E_UNSUPPORTED.
+ * The sum of a row's (x - mean)^2 has to stay within fp32: a row of values of
+ * about 2^63 / sqrt(n) and more comes out as its bias.  n <= 16384, else
+ * GDN_E_UNSUPPORTED.
  */
 int gdn_layer_norm_fwd(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps,
                        const void* x, const float* weight, const float* bias, void* y,
