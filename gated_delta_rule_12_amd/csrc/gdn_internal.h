@@ -173,6 +173,70 @@ struct PackedBwd {
 size_t packed_backward_workspace(const Packed& p);
 hipError_t packed_backward(const PackedBwd& b, void* ws, hipStream_t st);
 
+// Linear attention with a decay for each head over packed sequences
+// (gdn_linear.hip).
+struct Linear {
+    int64_t N, S, Hk, Hv, dk, dv, n_in, n_out, max_len;  // n_in, n_out: slots of the pools
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    int dtype;
+    float scale;
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* alpha;        // [Hv]
+    const int32_t* cu;
+    const float* s_in;         // pool, null: zero start states
+    const int32_t* slots_in;   // null: sequence s starts from slot s
+    float* s_out;              // pool, null: end states not wanted
+    const int32_t* slots_out;  // null: sequence s ends in slot s
+    void* out;                 // [N, Hv, dv], dtype
+    gdn_timer* timer;
+};
+bool linear_in_chunks(const Linear& p);
+size_t linear_workspace(const Linear& p);
+hipError_t linear_forward(const Linear& p, void* ws, hipStream_t st);
+struct LinearBwd {
+    Linear p;
+    const void* dout;     // [N, Hv, dv], dtype
+    const float* ds_out;  // [S, Hv, dv, dk] or null (zero)
+    void* dq;             // [N, Hk, dk], dtype
+    void* dk;             // [N, Hk, dk], dtype
+    void* dv;             // [N, Hv, dv], dtype
+    float* dalpha;        // [Hv] or null
+    float* ds0;           // [S, Hv, dv, dk] or null
+};
+size_t linear_backward_workspace(const Linear& p);
+hipError_t linear_backward(const LinearBwd& b, void* ws, hipStream_t st);
+
+// Norm of queries and keys over each head with the position's rotation
+// (gdn_qk_norm.hip).
+struct QkNorm {
+    int64_t N, Hq, Hk, d, rot, n_pos;
+    int dtype;
+    bool pairs;  // neighbours turn together, not the halves
+    float eps;
+    const void* q;
+    const void* k;
+    const void* dyq;
+    const void* dyk;
+    void* yq;    // forward: the results; backward: the gradients of q and k, or null
+    void* yk;
+    int64_t q_stride, k_stride, gq_stride, gk_stride, yq_stride, yk_stride;  // elements between tokens
+    const float* wq;  // [d] or null (ones)
+    const float* wk;
+    const float* cos;  // [n_pos, rot / 2]
+    const float* sin;
+    const int32_t* positions;  // [N], null: token t is at position t
+    float* dwq;  // [d] or null
+    float* dwk;
+    float* part;  // workspace of the backward
+    gdn_timer* timer;
+};
+int64_t qk_norm_blocks(const QkNorm& p);  // workgroups of the forward
+hipError_t qk_norm_fwd(const QkNorm& p, hipStream_t st);
+size_t qk_norm_workspace(const QkNorm& p);
+hipError_t qk_norm_bwd(const QkNorm& p, hipStream_t st);
+
 // Layer norm (gdn_norm.hip).
 constexpr int64_t kLayerNormMaxCols = 16384;
 struct LayerNorm {

@@ -17,6 +17,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
@@ -83,6 +84,13 @@ __device__ __forceinline__ void split4(const f32x4& x, u16x4& hi, u16x4& lo) {
 
 __device__ __forceinline__ u16x8 cat(const u16x4& a, const u16x4& b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Four 16-bit elements of a column: in each group of 16 lanes, lane i points
+// at row i / 4, columns 4 (i % 4) .. of a 4 x 16 block and gets column i.
+__device__ __forceinline__ u16x4 lds_column4(const unsigned short* p) {
+    return __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) s16x4*)const_cast<unsigned short*>(p)));
 }
 
 __device__ __forceinline__ float wave_incl_scan(float x, int lane) {

@@ -39,8 +39,7 @@
 // counts that the preparation's launch makes: only sequences longer than a
 // segment have states of segments, so that short ones cost no workspace.
 // Slots outside the pool read as zero states and are not written.
-#include <type_traits>
-
+#include "gdn_elements.h"
 #include "gdn_internal.h"
 #include "gdn_mfma_common.h"
 #include "gdn_packed_common.h"
@@ -82,15 +81,6 @@ struct Pk {
     float* p_blk;    // [block place, head][D][D]: and matrix, transposed
 };
 
-// Workgroups go to the eight XCDs in turn.  The work of workgroup b of n, so
-// that `set` consecutive pieces of work fall to one XCD and meet in its L2
-// (a step's states of 256 sequences 108 -> 97 us with a sequence a set; a state
-// pass with S and M of two value heads a set 82 -> 76 us).
-__device__ __forceinline__ unsigned on_one_xcd(unsigned b, unsigned n, unsigned set) {
-    const unsigned run = 8 * set, i = b / run, r = b - i * run;
-    return (i + 1) * run <= n ? i * run + (r % 8) * set + r / 8 : b;
-}
-
 __device__ __forceinline__ const float* state_from(const Packed& p, int64_t s, int64_t h) {
     const int64_t slot = p.slots_in ? (int64_t)p.slots_in[s] : s;
     if (!p.s_in || slot < 0 || slot >= p.n_in) return nullptr;
@@ -118,34 +108,6 @@ constexpr int kRecThreads = 256;
 constexpr int kStage = 8;
 constexpr int kRecLPR = 16, kRecR = 2;
 typedef float f32x4v __attribute__((ext_vector_type(4)));
-
-// four consecutive input-typed elements, as loaded and as fp32
-template <int DT>
-using R4 = std::conditional_t<DT == GDN_BF16, u32x2, f32x4>;
-template <int DT>
-__device__ __forceinline__ R4<DT> ldr(const void* base, int64_t i) {
-    if constexpr (DT == GDN_BF16) return *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + i);
-    else return *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + i);
-}
-template <int DT>
-__device__ __forceinline__ f32x4 cvt(const R4<DT>& u) {
-    if constexpr (DT == GDN_BF16)
-        return f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xFFFF0000u), __uint_as_float(u[1] << 16),
-                     __uint_as_float(u[1] & 0xFFFF0000u)};
-    else return u;
-}
-template <int DT>
-__device__ __forceinline__ f32x4 ld4e(const void* p, int64_t i) {
-    return cvt<DT>(ldr<DT>(p, i));
-}
-__device__ __forceinline__ float dot4e(const f32x4& x, const f32x4& y) {
-    return x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
-}
-template <int DT>
-__device__ __forceinline__ void st_out(void* out, int64_t i, float x) {
-    if constexpr (DT == GDN_F32) static_cast<float*>(out)[i] = x;
-    else static_cast<uint16_t*>(out)[i] = (uint16_t)pack_bf16(x, 0.f);
-}
 
 // S' and o of one token: k, q, g (the gate) in the lane's pieces, v of its rows
 template <int LPR, int NP, int R>
@@ -442,7 +404,6 @@ constexpr int kPfrag = 3 * 2 * 2 * 64;
 constexpr int LDA = C + 4;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // D += A B on a 32 x 32 x 16 bf16 tile: lane l = 32 g + c supplies A[c][8 g ..]
 // and B[8 g ..][c]; the accumulator holds D[8 (i / 4) + 4 g + i % 4][c] in
@@ -529,13 +490,6 @@ __device__ __forceinline__ float finite_max8(float m, const u32x4& v) {  // of m
     }
     return m;
 }
-// Four 16-bit elements of a column: in each group of 16 lanes, lane i points
-// at row i / 4, columns 4 (i % 4) .. of a 4 x 16 block and gets column i.
-__device__ __forceinline__ u16x4 lds_column4(const unsigned short* p) {
-    return __builtin_bit_cast(u16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                         (__attribute__((address_space(3))) s16x4*)const_cast<unsigned short*>(p)));
-}
-
 // A log gate of a zero gate: low enough that every product over it is zero
 // in fp32, finite so that the prefix of the tokens behind it stays exact (it
 // is a compensated pair; their ratios cancel it)

@@ -24,6 +24,7 @@ GDN_OK, GDN_E_ARG, GDN_E_SHAPE, GDN_E_UNSUPPORTED, GDN_E_WORKSPACE, GDN_E_HIP = 
 GDN_E_SCRATCH = -6
 GDN_NOALLOC_SCRATCH_BYTES = 128 << 20
 GDN_PATH_VALU, GDN_PATH_MFMA = 0, 1
+GDN_ROTATE_HALVES, GDN_ROTATE_PAIRS = 0, 1
 GDN_BWD_TOKEN, GDN_BWD_CHUNKED = 0, 1
 
 # every symbol include/gdn.h declares
@@ -39,7 +40,11 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_recurrent_ref", "gdn_seqpar_fwd", "gdn_decode_s
            "gdn_packed_fwd", "gdn_packed_fwd_timed", "gdn_packed_workspace_bytes", "gdn_packed_path",
            "gdn_packed_backward", "gdn_packed_backward_timed", "gdn_packed_backward_workspace_bytes",
            "gdn_layer_norm_fwd", "gdn_layer_norm_fwd_timed", "gdn_layer_norm_backward",
-           "gdn_layer_norm_backward_timed", "gdn_layer_norm_workspace_bytes")
+           "gdn_layer_norm_backward_timed", "gdn_layer_norm_workspace_bytes",
+           "gdn_linear_fwd", "gdn_linear_fwd_timed", "gdn_linear_workspace_bytes",
+           "gdn_linear_backward", "gdn_linear_backward_timed", "gdn_linear_backward_workspace_bytes",
+           "gdn_qk_norm_fwd", "gdn_qk_norm_fwd_timed", "gdn_qk_norm_backward", "gdn_qk_norm_backward_timed",
+           "gdn_qk_norm_workspace_bytes")
 
 _lib = None
 
@@ -122,9 +127,24 @@ def lib():
     L.gdn_layer_norm_backward.restype = ctypes.c_int
     L.gdn_layer_norm_workspace_bytes.argtypes = [i64, i64]
     L.gdn_layer_norm_workspace_bytes.restype = sz
+    L.gdn_linear_fwd.argtypes = [i64] * 9 + [i32, f32] + [vp, i64] * 3 + [vp] * 7 + [vp, sz, vp]
+    L.gdn_linear_fwd.restype = ctypes.c_int
+    L.gdn_linear_workspace_bytes.argtypes = [i64] * 7 + [i32]
+    L.gdn_linear_workspace_bytes.restype = sz
+    L.gdn_linear_backward.argtypes = [i64] * 7 + [i32, f32] + [vp, i64] * 3 + [vp] * 11 + [vp, sz, vp]
+    L.gdn_linear_backward.restype = ctypes.c_int
+    L.gdn_linear_backward_workspace_bytes.argtypes = [i64] * 6 + [i32]
+    L.gdn_linear_backward_workspace_bytes.restype = sz
+    L.gdn_qk_norm_fwd.argtypes = [i64] * 6 + [i32, i32, f32] + [vp, i64] * 2 + [vp] * 5 + [vp, i64] * 2 + [vp]
+    L.gdn_qk_norm_fwd.restype = ctypes.c_int
+    L.gdn_qk_norm_backward.argtypes = [i64] * 6 + [i32, i32, f32] + [vp, i64] * 4 + [vp] * 9 + [vp, sz, vp]
+    L.gdn_qk_norm_backward.restype = ctypes.c_int
+    L.gdn_qk_norm_workspace_bytes.argtypes = [i64] * 4
+    L.gdn_qk_norm_workspace_bytes.restype = sz
     # the *_timed variants: the same arguments plus the timer
     for name in ("gdn_chunk_fwd", "gdn_chunk_fwd_raw", "gdn_seqpar_fwd", "gdn_decode_step",
-                 "gdn_backward", "gdn_packed_fwd", "gdn_packed_backward", "gdn_layer_norm_fwd", "gdn_layer_norm_backward"):
+                 "gdn_backward", "gdn_packed_fwd", "gdn_packed_backward", "gdn_layer_norm_fwd", "gdn_layer_norm_backward",
+                 "gdn_linear_fwd", "gdn_linear_backward", "gdn_qk_norm_fwd", "gdn_qk_norm_backward"):
         f = getattr(L, name + "_timed")
         f.argtypes = getattr(L, name).argtypes + [vp]
         f.restype = ctypes.c_int
@@ -188,6 +208,18 @@ def gdn_seqpar_segments(B, T, H, dk, dv, chunk, dtype, gate, n_segments) -> int:
 
 def gdn_packed_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, dtype, gate) -> int:
     return int(lib().gdn_packed_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, dtype, gate))
+
+
+def gdn_linear_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, dtype) -> int:
+    return int(lib().gdn_linear_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, dtype))
+
+
+def gdn_linear_backward_workspace_bytes(N, S, Hk, Hv, dk, dv, dtype) -> int:
+    return int(lib().gdn_linear_backward_workspace_bytes(N, S, Hk, Hv, dk, dv, dtype))
+
+
+def gdn_qk_norm_workspace_bytes(N, Hq, Hk, d) -> int:
+    return int(lib().gdn_qk_norm_workspace_bytes(N, Hq, Hk, d))
 
 
 def gdn_packed_path(dk, dv, dtype, gate) -> int:
@@ -537,6 +569,13 @@ def _on(t, device, dtype, what):
             raise ValueError(f"{what} must be contiguous")
 
 
+def _heads_contiguous(tensors):
+    """[N,H,d] tensors whose tokens are contiguous rows, at any stride."""
+    for t in tensors:
+        if not t.is_contiguous() and (t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] > 1)):
+            raise ValueError("the heads and features of a token of q, k, v must be contiguous")
+
+
 def _packed_check(q, k, v, alpha, beta, cu_seqlens, pools, slots):
     import torch
     f32, i32 = torch.float32, torch.int32
@@ -548,9 +587,7 @@ def _packed_check(q, k, v, alpha, beta, cu_seqlens, pools, slots):
     dt = q.dtype
     if k.dtype != dt or v.dtype != dt:
         raise TypeError("q, k, v must share a dtype")
-    for t, d in ((q, dk), (k, dk), (v, dv)):
-        if not t.is_contiguous() and (t.stride(2) != 1 or (t.stride(1) != d and t.shape[1] > 1)):
-            raise ValueError("the heads and features of a token of q, k, v must be contiguous")
+    _heads_contiguous((q, k, v))
     if alpha.shape == (N, Hv):
         gate = GDN_GATE_SCALAR
     elif alpha.shape == (N, Hv, dk):
@@ -586,12 +623,13 @@ def _packed_check(q, k, v, alpha, beta, cu_seqlens, pools, slots):
     return N, S, Hk, Hv, dk, dv, gate, dev
 
 
-def _token_strides(q, k, v):
+def _token_stride(t):
     """Elements between tokens; a lone token's stride says nothing."""
-    def one(t):
-        row = t.shape[1] * t.shape[2]
-        return t.stride(0) if t.shape[0] > 1 else row
-    return one(q), one(k), one(v)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _token_strides(q, k, v):
+    return _token_stride(q), _token_stride(k), _token_stride(v)
 
 
 def packed_workspace_for(q, v, alpha, cu_seqlens, max_len=None):
@@ -679,6 +717,213 @@ def packed_backward(q, k, v, alpha, beta, cu_seqlens, state_in, slots_in, grad_o
             _addr(workspace), 0 if workspace is None else workspace.numel())
     _enqueue("gdn_packed_backward", args, dev, timer)
     return (*grads, ds0)
+
+
+# ---- linear attention with a decay for each head ---------------------------------
+
+def _linear_check(q, k, v, alpha, cu_seqlens, pools, slots):
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    shape = q.shape
+    if len(shape) != 3 or k.shape != shape or v.dim() != 3 or v.shape[0] != shape[0]:
+        raise ValueError("q, k must be [N,Hk,dk] and v [N,Hv,dv]")
+    N, Hk, dk = shape
+    _, Hv, dv = v.shape
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt:
+        raise TypeError("q, k, v must share a dtype")
+    _heads_contiguous((q, k, v))
+    if alpha.shape != (Hv,):
+        raise ValueError("alpha must be [Hv]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [S+1]")
+    S = cu_seqlens.shape[0] - 1
+    for t, i in zip(pools, slots):
+        if t is not None:
+            pool = t.shape
+            if len(pool) != 4 or pool[1:] != (Hv, dv, dk):
+                raise ValueError("state pools must be [slots,Hv,dv,dk]")
+            # (an empty tensor has no address, which would stand for no pool)
+            if pool[0] == 0 and i is None and S * Hv:
+                raise GdnError(GDN_E_SHAPE, "an empty state pool without slots")
+    for t in slots:
+        if t is not None and t.shape != (S,):
+            raise ValueError("slots must be [S]")
+    dev = q.get_device()
+    _on(alpha, dev, f32, "alpha")
+    _on(cu_seqlens, dev, i32, "cu_seqlens")
+    for t in pools:
+        _on(t, dev, f32, "a state pool")
+    for t in slots:
+        _on(t, dev, i32, "slots")
+    if dev < 0 or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k, v must be on one GPU")
+    return N, S, Hk, Hv, dk, dv, dev
+
+
+def linear_workspace_for(q, v, cu_seqlens, max_len=None):
+    """A workspace for linear_fwd on tensors like these."""
+    import torch
+    N, Hk, dk = q.shape
+    n = gdn_linear_workspace_bytes(N, cu_seqlens.shape[0] - 1, Hk, v.shape[1], dk, v.shape[2],
+                                   N if max_len is None else max_len, _dtype_code(q))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+
+
+def linear_fwd(q, k, v, alpha, cu_seqlens, state_in=None, slots_in=None, state_out=None, slots_out=None, *,
+               max_len=None, scale=1.0, out=None, workspace=None, timer=None):
+    """Linear attention with a decay for each head over packed ragged sequences:
+    gdn_linear_fwd, S_t = alpha S_{t-1} + v_t k_t^T and o_t = scale S_t q_t.
+    q, k [N,Hk,dk], v [N,Hv,dv] (bf16 or fp32; slices of a wider projection
+    along the heads are taken as they are), alpha [Hv] fp32; cu_seqlens, the
+    state pools, slots and max_len as for packed_fwd (state_out None: a new pool
+    [S,Hv,dv,dk], in the sequences' order).
+    Returns (out [N,Hv,dv] of q's dtype, state_out)."""
+    import torch
+    if state_out is None and slots_out is not None:
+        raise ValueError("slots_out needs state_out")
+    N, S, Hk, Hv, dk, dv, dev = _linear_check(q, k, v, alpha, cu_seqlens, (state_in, state_out), (slots_in, slots_out))
+    if state_out is None:
+        state_out = q.new_empty((S, Hv, dv, dk), dtype=torch.float32)
+    if out is None:
+        out = q.new_empty((N, Hv, dv))
+    else:
+        if out.shape != (N, Hv, dv):
+            raise ValueError("out must be [N,Hv,dv]")
+        _on(out, dev, q.dtype, "out")
+    if max_len is None:
+        max_len = N
+    code = _dtype_code(q)
+    _on(workspace, dev, torch.uint8, "workspace")
+    if workspace is None:
+        n = lib().gdn_linear_workspace_bytes(N, S, Hk, Hv, dk, dv, max_len, code)
+        if n:
+            workspace = q.new_empty((n,), dtype=torch.uint8)
+    sq, sk, sv = _token_strides(q, k, v)
+    args = (N, S, Hk, Hv, dk, dv, 0 if state_in is None else state_in.shape[0], state_out.shape[0], max_len, code, scale,
+            _addr(q), sq, _addr(k), sk, _addr(v), sv, _addr(alpha), _addr(cu_seqlens), _addr(state_in), _addr(slots_in),
+            _addr(state_out), _addr(slots_out), _addr(out), _addr(workspace), 0 if workspace is None else workspace.numel())
+    _enqueue("gdn_linear_fwd", args, dev, timer)
+    return out, state_out
+
+
+def linear_backward(q, k, v, alpha, cu_seqlens, state_in, slots_in, grad_out, grad_state_out=None, *, scale=1.0,
+                    want_grad_alpha=True, want_grad_state0=True, workspace=None, timer=None):
+    """Gradients through linear_fwd: gdn_linear_backward.  grad_out [N,Hv,dv] of
+    q's dtype = dL/d out; grad_state_out [S,Hv,dv,dk] fp32 = dL/d of the end
+    states, in the sequences' order, or None (zero).  Returns (dq, dk, dv of q's
+    dtype, dalpha [Hv] and dstate0 [S,Hv,dv,dk] fp32 or None where not wanted);
+    rows outside every sequence are zero."""
+    import torch
+    N, S, Hk, Hv, dk, dv, dev = _linear_check(q, k, v, alpha, cu_seqlens, (state_in,), (slots_in,))
+    f32 = torch.float32
+    if grad_out.shape != (N, Hv, dv):
+        raise ValueError("grad_out must be [N,Hv,dv]")
+    _on(grad_out, dev, q.dtype, "grad_out")
+    if grad_state_out is not None and grad_state_out.shape != (S, Hv, dv, dk):
+        raise ValueError("grad_state_out must be [S,Hv,dv,dk]")
+    _on(grad_state_out, dev, f32, "grad_state_out")
+    # (without sequences the entry point enqueues nothing, and every row is outside them)
+    new = q.new_empty if S * Hv else q.new_zeros
+    grads = [new(t.shape) for t in (q, k, v)]
+    da = new((Hv,), dtype=f32) if want_grad_alpha else None
+    ds0 = q.new_empty((S, Hv, dv, dk), dtype=f32) if want_grad_state0 else None
+    code = _dtype_code(q)
+    _on(workspace, dev, torch.uint8, "workspace")
+    if workspace is None:
+        n = lib().gdn_linear_backward_workspace_bytes(N, S, Hk, Hv, dk, dv, code)
+        if n:
+            workspace = q.new_empty((n,), dtype=torch.uint8)
+    sq, sk, sv = _token_strides(q, k, v)
+    args = (N, S, Hk, Hv, dk, dv, 0 if state_in is None else state_in.shape[0], code, scale, _addr(q), sq, _addr(k), sk,
+            _addr(v), sv, _addr(alpha), _addr(cu_seqlens), _addr(state_in), _addr(slots_in), _addr(grad_out),
+            _addr(grad_state_out), *map(_addr, grads), _addr(da), _addr(ds0), _addr(workspace),
+            0 if workspace is None else workspace.numel())
+    _enqueue("gdn_linear_backward", args, dev, timer)
+    return (*grads, da, ds0)
+
+
+# ---- norm of queries and keys with the position's rotation -----------------------
+
+def _qk_check(q, k, weights, cos, sin, positions):
+    import torch
+    f32 = torch.float32
+    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [N,Hq,d] and k [N,Hk,d]")
+    N, Hq, d = q.shape
+    if k.dtype != q.dtype:
+        raise TypeError("q, k must share a dtype")
+    _heads_contiguous((q, k))
+    dev = q.get_device()
+    if dev < 0 or k.get_device() != dev:
+        raise ValueError("q, k must be on one GPU")
+    for t in weights:
+        if t is not None and t.shape != (d,):
+            raise ValueError("the weights must be [d]")
+        _on(t, dev, f32, "the weights")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    n_pos = rot = 0
+    if cos is not None:
+        if cos.dim() != 2 or sin.shape != cos.shape:
+            raise ValueError("cos and sin must be [n_pos,rot/2]")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        _on(cos, dev, f32, "cos and sin")
+        _on(sin, dev, f32, "cos and sin")
+    if positions is not None and positions.shape != (N,):
+        raise ValueError("positions must be [N]")
+    _on(positions, dev, torch.int32, "positions")
+    return N, Hq, k.shape[1], d, rot, n_pos, dev
+
+
+def qk_norm_fwd(q, k, weight_q=None, weight_k=None, cos=None, sin=None, positions=None, *, eps=1e-6, interleaved=False,
+                q_out=None, k_out=None, timer=None):
+    """RMS norm of queries and keys over each head's features and the rotation of
+    feature pairs by the token's position, in one pass: gdn_qk_norm_fwd.
+    q [N,Hq,d], k [N,Hk,d] (bf16 or fp32; slices of a wider projection along the
+    heads are taken as they are), weights [d] fp32 or None (ones), cos and sin
+    [n_pos,rot/2] fp32 or None (no rotation), positions [N] int32 or None (token t
+    is at position t).  Features i and i + rot/2 turn together, interleaved: 2i
+    and 2i + 1.  q_out, k_out: where to (None: new tensors; q and k themselves:
+    in place).  Returns (q_out, k_out)."""
+    N, Hq, Hk, d, rot, n_pos, dev = _qk_check(q, k, (weight_q, weight_k), cos, sin, positions)
+    outs = []
+    for x, y in ((q, q_out), (k, k_out)):
+        if y is None:
+            y = x.new_empty(x.shape)
+        elif y.shape != x.shape or y.dtype != x.dtype or y.get_device() != dev:
+            raise ValueError("q_out and k_out must be as q and k")
+        else:
+            _heads_contiguous((y,))
+        outs.append(y)
+    sq, sk, so, sp = (_token_stride(t) for t in (q, k, *outs))
+    args = (N, Hq, Hk, d, rot, n_pos, _dtype_code(q), int(interleaved), eps, _addr(q), sq, _addr(k), sk, _addr(weight_q),
+            _addr(weight_k), _addr(cos), _addr(sin), _addr(positions), _addr(outs[0]), so, _addr(outs[1]), sp)
+    _enqueue("gdn_qk_norm_fwd", args, dev, timer)
+    return tuple(outs)
+
+
+def qk_norm_backward(grad_q_out, grad_k_out, q, k, weight_q=None, weight_k=None, cos=None, sin=None, positions=None, *,
+                     eps=1e-6, interleaved=False, want_x=True, want_weights=True, workspace=None, timer=None):
+    """Gradients of qk_norm_fwd: gdn_qk_norm_backward.  Returns (grad_q, grad_k of
+    q's dtype, grad_weight_q, grad_weight_k [d] fp32), None where not wanted."""
+    import torch
+    N, Hq, Hk, d, rot, n_pos, dev = _qk_check(q, k, (weight_q, weight_k), cos, sin, positions)
+    for g, x in ((grad_q_out, q), (grad_k_out, k)):
+        if g.shape != x.shape or g.dtype != x.dtype or g.get_device() != dev:
+            raise ValueError("the incoming gradients must be as q and k")
+    _heads_contiguous((grad_q_out, grad_k_out))
+    dq, dk = (x.new_empty(x.shape) if want_x else None for x in (q, k))
+    dwq, dwk = (q.new_empty((d,), dtype=torch.float32) if want_weights else None for _ in range(2))
+    _on(workspace, dev, torch.uint8, "workspace")
+    if workspace is None and want_weights:
+        workspace = q.new_empty((lib().gdn_qk_norm_workspace_bytes(N, Hq, Hk, d),), dtype=torch.uint8)
+    gq, gk, sq, sk = (_token_stride(t) for t in (grad_q_out, grad_k_out, q, k))
+    args = (N, Hq, Hk, d, rot, n_pos, _dtype_code(q), int(interleaved), eps, _addr(grad_q_out), gq, _addr(grad_k_out), gk,
+            _addr(q), sq, _addr(k), sk, _addr(weight_q), _addr(weight_k), _addr(cos), _addr(sin), _addr(positions),
+            _addr(dq), _addr(dk), _addr(dwq), _addr(dwk), _addr(workspace), 0 if workspace is None else workspace.numel())
+    _enqueue("gdn_qk_norm_backward", args, dev, timer)
+    return dq, dk, dwq, dwk
 
 
 # ---- layer norm -------------------------------------------------------------------

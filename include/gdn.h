@@ -77,6 +77,9 @@ enum gdn_status {
     GDN_E_HIP = -5,          /* a HIP call failed */
     GDN_E_SCRATCH = -6       /* larger than gdn_chunk_fwd_noalloc's static scratch */
 };
+/* Which features turn together (gdn_qk_norm_fwd): i and i + rot / 2, or 2 i and
+ * 2 i + 1. */
+enum gdn_rotation { GDN_ROTATE_HALVES = 0, GDN_ROTATE_PAIRS = 1 };
 enum gdn_path { GDN_PATH_VALU = 0, GDN_PATH_MFMA = 1 };
 /* Backward algorithm (gdn_backward_path). */
 enum gdn_bwd_path { GDN_BWD_TOKEN = 0, GDN_BWD_CHUNKED = 1 };
@@ -406,6 +409,137 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
                                            int64_t dv, int32_t dtype, int32_t gate);
 
 /*
+ * gdn_linear_fwd — linear attention with a decay for each head, the layer
+ * that models put beside the delta rule or compare it with, over the same packed
+ * sequences and pools of states as gdn_packed_fwd: per value head
+ *   S_t = alpha S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+ * (the notes' decayed linear attention with one gate a head).  Prompts of any
+ * length, drafted and single tokens in one call.
+ *   q, k        [N, Hk, dk], v [N, Hv, dv], strides, Hv a multiple of Hk,
+ *               cu_seqlens, state_in, slots_in, state_out, slots_out, out,
+ *               max_len: as for gdn_packed_fwd (the same rules for slots; in
+ *               place or not)
+ *   alpha       [Hv] fp32, >= 0 (not checked; 0: a token reads its own value
+ *               alone)
+ *   workspace   gdn_linear_workspace_bytes(...) bytes: none for single tokens
+ *               (max_len or N below 32), else 8 Hv dk dv for each sequence of 32
+ *               tokens or more and 4 Hv dk dv for every 256 tokens; two calls
+ *               that may overlap need two
+ * Sequences of 32 tokens or more run in segments of 256 on the matrix cores, for
+ * every dk, dv and dtype: fp32 as it is; bf16 q, k and v exactly, what is
+ * multiplied with a power of alpha as two (scores, start states: 2^-17) or three
+ * (what enters the states: exact) bf16 terms.  The others run token by token.
+ * All sums and states are fp32; out is rounded once.
+ * NaN and infinities propagate as in the formula, to nothing of other sequences;
+ * in segments an infinity may become a NaN, and one in v may reach, within its
+ * value feature, the 31 tokens in front of its own.
+ * Everything else (empty sequences, offsets out of order or range, capture,
+ * alignment, statuses and limits) is as for gdn_packed_fwd.
+ */
+int gdn_linear_fwd(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in,
+                   int64_t n_out, int64_t max_len, int32_t dtype, float scale, const void* q,
+                   int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                   const float* alpha, const int32_t* cu_seqlens, const float* state_in,
+                   const int32_t* slots_in, float* state_out, const int32_t* slots_out, void* out,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gdn_linear_fwd needs for these arguments (0: none, or the
+ * arguments do not validate).  Host only. */
+size_t gdn_linear_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                                  int64_t max_len, int32_t dtype);
+
+/*
+ * gdn_linear_backward — gradients of a loss through gdn_linear_fwd, for all of
+ * its shapes.  Inputs as there.
+ *   grad_out        [N, Hv, dv], dtype: dL/d out
+ *   grad_state_out  [S, Hv, dv, dk] fp32 in the sequences' order: dL/d of their
+ *                   end states; NULL: zero
+ *   grad_q, grad_k  [N, Hk, dk], dtype, summed over the value heads of a key
+ *                   head in fp32 and rounded once;  grad_v [N, Hv, dv], dtype;
+ *                   rows outside every sequence are set to zero
+ *   grad_alpha      [Hv] fp32, summed over all sequences; NULL: not wanted
+ *   grad_state0     [S, Hv, dv, dk] fp32: dL/d of each sequence's start state
+ *                   (sequences that share a slot each have their own; it must
+ *                   not be grad_state_out's memory); NULL: not wanted
+ *   workspace       gdn_linear_backward_workspace_bytes(...): twice 4 Hv dk dv
+ *                   for each sequence and for every 256 tokens, and grad_alpha's
+ *                   addends
+ * S Hv = 0: nothing is enqueued, the gradients are left as they were.  Sums are
+ * taken in a fixed order (repeated calls give identical results).  Alignment: as
+ * gdn_packed_backward.
+ */
+int gdn_linear_backward(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in,
+                        int32_t dtype, float scale, const void* q, int64_t q_stride, const void* k,
+                        int64_t k_stride, const void* v, int64_t v_stride, const float* alpha,
+                        const int32_t* cu_seqlens, const float* state_in, const int32_t* slots_in,
+                        const void* grad_out, const float* grad_state_out, void* grad_q, void* grad_k,
+                        void* grad_v, float* grad_alpha, float* grad_state0, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gdn_linear_backward needs (0: none, or the arguments do not
+ * validate).  Host only. */
+size_t gdn_linear_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk,
+                                           int64_t dv, int32_t dtype);
+
+/*
+ * gdn_qk_norm_fwd — RMS norm of queries and keys over the features of each
+ * head, and the rotation of feature pairs by the token's position, in one pass;
+ * it stands between the projections and linear attention (or any attention
+ * beside it).  Per head row x of d features:
+ *   z = x weight / sqrt(mean x^2 + eps);  the pairs (a, b) of the first rot
+ *   features become (a cos - b sin, b cos + a sin), the others stay as in z.
+ *   q           [N, Hq, d], k [N, Hk, d], dtype; tokens q_stride, k_stride
+ *               elements apart (slices of one projection), heads of a token
+ *               contiguous; Hq or Hk may be 0
+ *   weight_q, weight_k  [d] fp32, or NULL (ones)
+ *   rotation    GDN_ROTATE_HALVES: pairs (i, i + rot / 2); GDN_ROTATE_PAIRS:
+ *               (2 i, 2 i + 1)
+ *   cos, sin    [n_pos, rot / 2] fp32: of pair i's angle at each position (rot
+ *               0: not read)
+ *   positions   [N] int32 on the device, or NULL: token t is at position t;
+ *               clamped to 0 .. n_pos - 1
+ *   q_out, k_out  as q and k; may be q and k (in place, the same stride)
+ * Statistics and products in fp32, rounded once; the sum of a row's x^2 has to
+ * stay within fp32.  A row's NaN and infinities stay in the row.  No workspace.
+ * d a multiple of 16 up to 256, rot of 16 up to d, else GDN_E_UNSUPPORTED (rot
+ * over d: GDN_E_SHAPE).  Pointers and token strides on 16 bytes, positions on 4,
+ * else GDN_E_ARG; strides shorter than a row or over 2^23, N or n_pos of 2^31 or
+ * more, N (Hq + Hk) d over about 2^37 (4 heads count as one at least): GDN_E_SHAPE.
+ */
+int gdn_qk_norm_fwd(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot, int64_t n_pos,
+                    int32_t dtype, int32_t rotation, float eps, const void* q, int64_t q_stride,
+                    const void* k, int64_t k_stride, const float* weight_q, const float* weight_k,
+                    const float* cos, const float* sin, const int32_t* positions, void* q_out,
+                    int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * gdn_qk_norm_backward — its gradients: with g the incoming gradient turned back
+ * and xhat = x / sqrt(mean x^2 + eps),
+ *   grad_x = (g weight - xhat mean(g weight xhat)) / sqrt(mean x^2 + eps),
+ *   grad_weight = sum over tokens and heads of g xhat.
+ *   grad_q_out, grad_k_out  as q and k, with strides of their own
+ *   grad_q, grad_k  [N, Hq, d], [N, Hk, d], dtype, contiguous; may be the
+ *               incoming gradient's buffer or q's and k's where those are
+ *               contiguous;  grad_weight_q, grad_weight_k [d] fp32.  NULL: not
+ *               wanted (both of a side NULL: that side is not read)
+ *   workspace   gdn_qk_norm_workspace_bytes(N, Hq, Hk, d), for the weights'
+ *               gradients
+ * The sums over rows are taken in a fixed order (repeated calls give identical
+ * results).
+ */
+int gdn_qk_norm_backward(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot, int64_t n_pos,
+                         int32_t dtype, int32_t rotation, float eps, const void* grad_q_out,
+                         int64_t gq_stride, const void* grad_k_out, int64_t gk_stride, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, const float* weight_q,
+                         const float* weight_k, const float* cos, const float* sin,
+                         const int32_t* positions, void* grad_q, void* grad_k, float* grad_weight_q,
+                         float* grad_weight_k, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes gdn_qk_norm_backward needs (0 when the sizes do not
+ * validate).  Host only. */
+size_t gdn_qk_norm_workspace_bytes(int64_t N, int64_t Hq, int64_t Hk, int64_t d);
+
+/*
  * gdn_layer_norm_fwd — layer norm of rows of n elements, for blocks that
  * normalise the heads' outputs (rows of dv) or their input (rows of model
  * width) by it; the notes' DeltaNet block has an RMS norm and an output gate
@@ -560,6 +694,39 @@ int gdn_packed_backward_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int6
                               float* grad_v, float* grad_alpha, float* grad_beta,
                               float* grad_state0, void* workspace, size_t workspace_bytes,
                               void* stream, gdn_timer* timer);
+int gdn_linear_fwd_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                         int64_t n_in, int64_t n_out, int64_t max_len, int32_t dtype, float scale,
+                         const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, const float* alpha,
+                         const int32_t* cu_seqlens, const float* state_in,
+                         const int32_t* slots_in, float* state_out, const int32_t* slots_out,
+                         void* out, void* workspace, size_t workspace_bytes, void* stream,
+                         gdn_timer* timer);
+int gdn_linear_backward_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk,
+                              int64_t dv, int64_t n_in, int32_t dtype, float scale, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const float* alpha, const int32_t* cu_seqlens,
+                              const float* state_in, const int32_t* slots_in,
+                              const void* grad_out, const float* grad_state_out, void* grad_q,
+                              void* grad_k, void* grad_v, float* grad_alpha, float* grad_state0,
+                              void* workspace, size_t workspace_bytes, void* stream,
+                              gdn_timer* timer);
+int gdn_qk_norm_fwd_timed(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot,
+                          int64_t n_pos, int32_t dtype, int32_t rotation, float eps,
+                          const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const float* weight_q, const float* weight_k, const float* cos,
+                          const float* sin, const int32_t* positions, void* q_out,
+                          int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream,
+                          gdn_timer* timer);
+int gdn_qk_norm_backward_timed(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot,
+                               int64_t n_pos, int32_t dtype, int32_t rotation, float eps,
+                               const void* grad_q_out, int64_t gq_stride, const void* grad_k_out,
+                               int64_t gk_stride, const void* q, int64_t q_stride, const void* k,
+                               int64_t k_stride, const float* weight_q, const float* weight_k,
+                               const float* cos, const float* sin, const int32_t* positions,
+                               void* grad_q, void* grad_k, float* grad_weight_q,
+                               float* grad_weight_k, void* workspace, size_t workspace_bytes,
+                               void* stream, gdn_timer* timer);
 int gdn_layer_norm_fwd_timed(int64_t rows, int64_t n, int32_t x_dtype, int32_t y_dtype, float eps,
                              const void* x, const float* weight, const float* bias, void* y,
                              float* mean, float* rstd, void* stream, gdn_timer* timer);
