@@ -29,9 +29,11 @@ constexpr int kLinMin = 32;
 // Tokens of a segment at most.
 constexpr int kSegMax = 512;
 
-// A segment: its tokens, its sequence, whether it is that one's first or last.
+// A segment: its tokens, its sequence, whether it is that one's first or last,
+// and above these two bits that one's rank.
 struct Seg {
     int begin, n, seq, ends;
+    __device__ int rank() const { return ends >> 2; }
 };
 constexpr int kFirst = 1, kLast = 2;
 
@@ -46,7 +48,8 @@ struct Lin {
     int32_t* count;      // [2]: such sequences, segments
     int32_t* seqs;       // [nrank]: the sequences with segments
     int32_t* first;      // [nrank + 1]: segments before each of them
-    Seg* segs;           // [nseg]
+    Seg* segs;           // [nseg], without tokens behind the last
+    float* log2a;        // [Hv]: of the decays
     float* s_seg;        // [nseg, Hv] states: what a segment adds, then the state behind it
     float* s_copy;       // [nrank, Hv]: start states of a call in place, or null
     // backward
@@ -57,9 +60,15 @@ struct Lin {
     float* g_seg;        // [nseg, Hv]: what a segment adds to its start state's gradient, then all of that
     float* part;         // [Hv, parts]: addends of dalpha
     int64_t parts;
-    int64_t part_dkv, part_scan;  // where those of the key and value rows and of the scan begin
+    int64_t part_scan;   // where those of the scan begin, behind those of the rows
 };
 
+// Segment si, in scalar registers
+__device__ __forceinline__ Seg segment(const Lin& a, int64_t si) {
+    const Seg x = a.segs[si];
+    auto same = [](int y) { return __builtin_amdgcn_readfirstlane(y); };
+    return Seg{same(x.begin), same(x.n), same(x.seq), same(x.ends)};
+}
 __device__ __forceinline__ const float* start_of(const Lin& a, int64_t s, int64_t h) {
     const Linear& p = a.p;
     const int64_t slot = p.slots_in ? (int64_t)p.slots_in[s] : s;
@@ -78,7 +87,7 @@ __device__ __forceinline__ float* end_of(const Lin& a, int64_t s, int64_t h) {
 // less than 2^-24 of a weight of one wherever the power counts.
 struct Decay {
     float a, log2a;
-    __device__ explicit Decay(float alpha) : a(alpha), log2a((float)log2((double)alpha)) {}
+    __device__ Decay(const Lin& l, int h) : a(l.p.alpha[h]), log2a(l.log2a[h]) {}
     __device__ float operator()(int x) const { return x == 0 ? 1.f : exp2f((float)x * log2a); }
 };
 
@@ -91,6 +100,7 @@ constexpr int kPlanLds = 1024;  // ranks whose counts the search finds in LDS
 __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
     __shared__ uint32_t sums[2 * kThreads / 64];
     __shared__ int lfirst[kPlanLds];
+    for (int h = tid; h < a.Hv; h += kThreads) a.log2a[h] = (float)log2((double)a.p.alpha[h]);
     const int64_t S = a.at.S, run = (S + kThreads - 1) / kThreads, r0 = min(tid * run, S), r1 = min(r0 + run, S);
     const int w = tid >> 6, lane = tid & 63;
     auto segs_of = [&](int64_t n) { return (uint32_t)((n + a.seg - 1) / a.seg); };
@@ -138,6 +148,7 @@ __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
     __threadfence_block();
     __syncthreads();
     const int ranks = total[0];
+    for (int64_t i = total[1] + tid; i < a.nseg; i += kThreads) a.segs[i] = Seg{0, 0, 0, 0};
     for (int i = tid; i < total[1]; i += kThreads) {
         int lo = 0, hi = ranks;  // first[lo] <= i, first[hi] > i or none
         while (hi - lo > 1) {
@@ -154,7 +165,7 @@ __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
         x.begin = x.n > 0 ? (int)(sp.begin + from) : 0;
         x.seq = s;
         // (where the table ends, so does the sequence: no segment looks behind it)
-        x.ends = (from == 0 ? kFirst : 0) | (from + a.seg >= sp.n || i + 1 == total[1] ? kLast : 0);
+        x.ends = (from == 0 ? kFirst : 0) | (from + a.seg >= sp.n || i + 1 == total[1] ? kLast : 0) | lo << 2;
         a.segs[i] = x;
     }
 }
@@ -162,15 +173,16 @@ __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
 // ---------------------------------------------------------------------------
 // token by token
 // ---------------------------------------------------------------------------
-// LPR lanes hold one row of S, four elements each, R rows a thread.
-constexpr int kLinR = 4;
+// LPR lanes hold a row of S, four elements each, and kLinR rows one behind the
+// other: a token's v and o of a lane's rows are one piece each.
+constexpr int kLinR = 4, kFlight = 4;
 template <int LPR>
 constexpr int rec_rows() {
     return 4 * (64 / LPR) * kLinR;  // rows a workgroup
 }
 template <int DT, int LPR>
 __device__ __forceinline__ void rec_sequence(const Lin& a, unsigned block, unsigned blocks) {
-    constexpr int RPW = 64 / LPR, RB = rec_rows<LPR>();
+    constexpr int RB = rec_rows<LPR>();
     const Linear& p = a.p;
     const int dk = (int)p.dk, dv = (int)p.dv;
     const unsigned nrb = ((unsigned)dv + RB - 1) / RB;
@@ -180,37 +192,51 @@ __device__ __forceinline__ void rec_sequence(const Lin& a, unsigned block, unsig
     const float* src = start_of(a, s, h);
     float* dst = end_of(a, s, h);
     if (sp.n >= a.chunk_min || (sp.n == 0 && src == dst)) return;
-    const int w = threadIdx.x >> 6, l = threadIdx.x & 63, c = l % LPR;
-    const bool on = 4 * c < dk;
-    const float alpha = p.alpha[h];
-    int row[kLinR];
+    const int c = threadIdx.x % LPR, row = rb * RB + threadIdx.x / LPR * kLinR;
+    // (lanes behind the row's end and rows behind the last repeat the last piece
+    // and store nothing; what such lanes add to a sum is zero)
+    const bool on = 4 * c < dk, in = row < dv;
+    const int col = on ? 4 * c : dk - 4, r0 = in ? row : dv - kLinR;
     f32x4 S[kLinR];
 #pragma unroll
-    for (int j = 0; j < kLinR; ++j) {
-        row[j] = rb * RB + (j * 4 + w) * RPW + l / LPR;
-        S[j] = zero4();
-        if (src && on && row[j] < dv) S[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(src + row[j] * dk + 4 * c));
-    }
-    for (int64_t t = sp.begin; t < sp.begin + sp.n; ++t) {
-        const f32x4 k = on ? ld4e<DT>(p.k, t * p.k_stride + hk * dk + 4 * c) : zero4();
-        const f32x4 q = on ? ld4e<DT>(p.q, t * p.q_stride + hk * dk + 4 * c) : zero4();
-        float v[kLinR], o[kLinR];
+    for (int j = 0; j < kLinR; ++j)
+        S[j] = src ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(src + (r0 + j) * dk + col)) : zero4();
+    const float alpha = p.alpha[h];
+    // the next kFlight tokens' rows are in flight
+    R4<DT> k[kFlight], q[kFlight], v[kFlight];
+    auto fetch = [&](int u, int64_t t) {
+        if (t >= sp.n) return;
+        t += sp.begin;
+        k[u] = ldr<DT>(p.k, t * p.k_stride + hk * dk + col);
+        q[u] = ldr<DT>(p.q, t * p.q_stride + hk * dk + col);
+        v[u] = ldr<DT>(p.v, t * p.v_stride + h * dv + r0);
+    };
 #pragma unroll
-        for (int j = 0; j < kLinR; ++j) v[j] = row[j] < dv ? gdn_ld<DT>(p.v, t * p.v_stride + h * dv + row[j]) : 0.f;
+    for (int u = 0; u < kFlight; ++u) fetch(u, u);
+    for (int64_t t0 = 0; t0 < sp.n; t0 += kFlight)
 #pragma unroll
-        for (int j = 0; j < kLinR; ++j) {
-            S[j] = alpha * S[j] + v[j] * k;
-            o[j] = p.scale * row_sum<LPR>(dot4e(S[j], q));
+        for (int u = 0; u < kFlight; ++u) {
+            if (t0 + u >= sp.n) break;
+            const f32x4 kt = cvt<DT>(k[u]), qt = on ? cvt<DT>(q[u]) : zero4(), vt = cvt<DT>(v[u]);
+            f32x4 o;
+#pragma unroll
+            for (int j = 0; j < kLinR; ++j) {
+                S[j] = alpha * S[j] + vt[j] * kt;
+                o[j] = p.scale * row_sum<LPR>(dot4e(S[j], qt));
+            }
+            fetch(u, t0 + u + kFlight);
+            if (c == 0 && in) {
+                const int64_t at = ((sp.begin + t0 + u) * a.Hv + h) * dv + row;
+                if constexpr (DT == GDN_BF16)
+                    st_g(static_cast<uint16_t*>(p.out) + at, u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])});
+                else
+                    st_g(static_cast<float*>(p.out) + at, o);
+            }
         }
-        if (c == 0)
-#pragma unroll
-            for (int j = 0; j < kLinR; ++j)
-                if (row[j] < dv) st_out<DT>(p.out, (t * a.Hv + h) * dv + row[j], o[j]);
-    }
-    if (!dst) return;
+    if (!dst || !on || !in) return;
 #pragma unroll
     for (int j = 0; j < kLinR; ++j)
-        if (on && row[j] < dv) __builtin_nontemporal_store(S[j], reinterpret_cast<f32x4*>(dst + row[j] * dk + 4 * c));
+        __builtin_nontemporal_store(S[j], reinterpret_cast<f32x4*>(dst + (row + j) * dk + col));
 }
 template <int DT, int LPR>
 __global__ __launch_bounds__(kThreads) void k_lin_rec(Lin a) {
@@ -254,7 +280,7 @@ template <>
 struct El<GDN_BF16> {
     using T = uint16_t;
     using Op = u16x8;
-    static constexpr int KS = 32, TT = 64, PAD = 16, TERMS = 2;  // TT: tokens a tile
+    static constexpr int KS = 32, TT = 32, PAD = 16, TERMS = 2;  // TT: tokens a tile
 };
 template <>
 struct El<GDN_F32> {
@@ -298,6 +324,21 @@ __device__ __forceinline__ typename El<DT>::Op col_op_acc(const typename El<DT>:
     }
 }
 
+// Bytes from `base` (the same for the wave) on, as far as `bytes`; a load past them
+// gives zero, without a branch.
+typedef __amdgpu_buffer_rsrc_t Bytes;
+__device__ __forceinline__ Bytes bytes_from(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00027000);
+}
+__device__ __forceinline__ u32x4 ld_bytes(Bytes from, uint32_t at) {
+    return __builtin_amdgcn_raw_buffer_load_b128(from, (int)at, 0, 0);
+}
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // behind every buffer
+// `rows` rows (none below one) of d elements of e bytes, `stride` bytes apart
+__device__ __forceinline__ uint32_t rows_bytes(int rows, uint32_t stride, int d, int e) {
+    return rows > 0 ? (uint32_t)(rows - 1) * stride + (uint32_t)(d * e) : 0u;
+}
+
 // A tile of TT tokens' rows of D features (d of them real) on its way to LDS;
 // rows behind the last and features past d are zero there.
 template <int DT, int D>
@@ -305,15 +346,21 @@ struct Tile {
     using T = typename El<DT>::T;
     static constexpr int TT = El<DT>::TT, LD = D + El<DT>::PAD, V = 16 / sizeof(T), PPR = D / V, NP = TT * PPR / kThreads;
     static constexpr int kSize = TT * LD;
-    static_assert(NP * kThreads == TT * PPR, "whole rounds");
-    u32x4 r[NP];
-    __device__ __forceinline__ void fetch(const T* from, int64_t stride, int rows, int d, int tid) {
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            const int p = tid + kThreads * k, t = p / PPR, c = V * (p % PPR);
-            r[k] = u32x4{0, 0, 0, 0};
-            if (t < rows && c < d) r[k] = ld_g<u32x4>(from + t * stride + c);
+    static_assert(NP * kThreads == TT * PPR && kThreads % PPR == 0, "whole rounds of whole rows");
+    struct At {  // a thread's pieces
+        uint32_t stride, first;
+        int d;
+        __device__ __forceinline__ At(int64_t elements, int d, int tid) : stride((uint32_t)(elements * sizeof(T))), d(d) {
+            const int c = V * (tid % PPR);
+            first = c < d ? (uint32_t)(tid / PPR) * stride + (uint32_t)(c * sizeof(T)) : kNowhere;
         }
+    };
+    u32x4 r[NP];
+    __device__ __forceinline__ void fetch(const T* from, const At& at, int rows) {
+        const Bytes b = bytes_from(from, rows_bytes(min(rows, TT), at.stride, at.d, sizeof(T)));
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+            r[k] = ld_bytes(b, at.first == kNowhere ? kNowhere : at.first + (uint32_t)k * (kThreads / PPR) * at.stride);
     }
     __device__ __forceinline__ void put(T* tile, int tid) const {
 #pragma unroll
@@ -342,7 +389,7 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t
 }
 
 template <int DT, int DV, int DK>
-__global__ __launch_bounds__(kThreads) void k_lin_add(Lin a) {
+__global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a) {
     using E = El<DT>;
     using T = typename E::T;
     using Op = typename E::Op;
@@ -357,13 +404,13 @@ __global__ __launch_bounds__(kThreads) void k_lin_add(Lin a) {
     const unsigned id = on_one_xcd(blockIdx.x, gridDim.x, a.group);
     const int64_t si = id / a.Hv;
     const int h = id - si * a.Hv;
-    if (si >= a.count[1]) return;
-    const Seg sg = a.segs[si];
+    const Seg sg = segment(a, si);
+    if (sg.n == 0) return;
     // (a last segment's end, where no one wants it; a first one's start gradient)
     if (rev ? (sg.ends & kFirst) && !a.ds0 : (sg.ends & kLast) && !(p.s_out && end_of(a, sg.seq, h))) return;
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g = l >> 4, i = l & 15;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = (tid & 63) >> 4, i = tid & 15;
     const int dk = (int)p.dk, dv = (int)p.dv;
-    const Decay decay(p.alpha[h]);
+    const Decay decay(a, h);
     for (int j = tid; j < a.seg; j += kThreads)
         wt[j] = j >= sg.n ? 0.f : rev ? p.scale * decay(j + 1) : decay(sg.n - 1 - j);
     const int hk = h / a.group;
@@ -376,24 +423,25 @@ __global__ __launch_bounds__(kThreads) void k_lin_add(Lin a) {
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[r][c] = zero4();
-    TX tx;
-    TY ty;
+    TX tx[2];
+    TY ty[2];
+    const typename TX::At ax(xs, dv, tid);
+    const typename TY::At ay(ys, dk, tid);
     const int nt = (sg.n + TT - 1) / TT;
-    tx.fetch(x, xs, sg.n, dv, tid);
-    ty.fetch(y, ys, sg.n, dk, tid);
-    for (int t = 0; t < nt; ++t) {
-        const T *bx = lx[t & 1], *by = ly[t & 1];
-        tx.put(lx[t & 1], tid);
-        ty.put(ly[t & 1], tid);
-        if (t + 1 < nt) {
-            tx.fetch(x + (t + 1) * TT * xs, xs, sg.n - (t + 1) * TT, dv, tid);
-            ty.fetch(y + (t + 1) * TT * ys, ys, sg.n - (t + 1) * TT, dk, tid);
-        }
+    auto fetch = [&](int t, int b) {
+        tx[b].fetch(x + t * TT * xs, ax, sg.n - t * TT);
+        ty[b].fetch(y + t * TT * ys, ay, sg.n - t * TT);
+    };
+    auto step = [&](int t, int b) {
+        const T *bx = lx[b], *by = ly[b];
+        tx[b].put(lx[b], tid);
+        ty[b].put(ly[b], tid);
+        fetch(t + 2, b);
         __syncthreads();
 #pragma unroll
         for (int k0 = 0; k0 < TT; k0 += KS) {
             const float* wk = wt + t * TT + k0 + KS / 4 * g;
-            Op b[RT][DT == GDN_BF16 ? 3 : 1];
+            Op bt[RT][DT == GDN_BF16 ? 3 : 1];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const Op raw = col_op<DT>(bx, TX::LD, k0, 16 * (RT * w + r), g, i);
@@ -404,9 +452,9 @@ __global__ __launch_bounds__(kThreads) void k_lin_add(Lin a) {
                         split3(wk[2 * e] * gdn_bf16_to_f32(raw[2 * e]), wk[2 * e + 1] * gdn_bf16_to_f32(raw[2 * e + 1]),
                                t3[0][e], t3[1][e], t3[2][e]);
 #pragma unroll
-                    for (int e = 0; e < 3; ++e) b[r][e] = __builtin_bit_cast(u16x8, u32x4{t3[e][0], t3[e][1], t3[e][2], t3[e][3]});
+                    for (int e = 0; e < 3; ++e) bt[r][e] = __builtin_bit_cast(u16x8, u32x4{t3[e][0], t3[e][1], t3[e][2], t3[e][3]});
                 } else {
-                    b[r][0] = raw * *reinterpret_cast<const f32x4*>(wk);
+                    bt[r][0] = raw * *reinterpret_cast<const f32x4*>(wk);
                 }
             }
 #pragma unroll
@@ -415,9 +463,16 @@ __global__ __launch_bounds__(kThreads) void k_lin_add(Lin a) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
-                    for (int e = (DT == GDN_BF16 ? 2 : 0); e >= 0; --e) acc[r][c] = mm(col, b[r][e], acc[r][c]);
+                    for (int e = (DT == GDN_BF16 ? 2 : 0); e >= 0; --e) acc[r][c] = mm(col, bt[r][e], acc[r][c]);
             }
         }
+    };
+    // two tiles ahead
+    fetch(0, 0);
+    fetch(1, 1);
+    for (int t = 0; t < nt; t += 2) {
+        step(t, 0);
+        if (t + 1 < nt) step(t + 1, 1);
     }
     // the accumulator: column 4 g .. of 16 c, row i of the wave's
     float* out = (rev ? a.g_seg : a.s_seg) + (si * a.Hv + h) * (int64_t)a.state;
@@ -488,7 +543,7 @@ __global__ __launch_bounds__(kThreads) void k_lin_scan(Lin a) {
         S = ld_g<f32x4>(src + x.e);
         if (a.s_copy) st_g(a.s_copy + ((int64_t)x.r * a.Hv + x.h) * a.state + x.e, S);
     }
-    const Decay decay(a.p.alpha[x.h]);
+    const Decay decay(a, x.h);
     const float whole = decay(a.seg), rest = decay((int)(x.sp.n - (int64_t)(x.G - 1) * a.seg));
     const int64_t stride = (int64_t)a.Hv * a.state;
     float* at = a.s_seg + ((int64_t)x.f * a.Hv + x.h) * a.state + x.e;
@@ -516,7 +571,7 @@ __global__ __launch_bounds__(kThreads) void k_lin_bscan(Lin a) {
     const ScanAt x = scan_at(a, tid);
     float da = 0.f;
     if (x.on) {
-        const Decay decay(a.p.alpha[x.h]);
+        const Decay decay(a, x.h);
         const int n_last = (int)(x.sp.n - (int64_t)(x.G - 1) * a.seg);
         const float whole = decay(a.seg), rest = x.G > 0 ? decay(n_last) : 1.f;
         const int64_t stride = (int64_t)a.Hv * a.state, off = ((int64_t)x.f * a.Hv + x.h) * a.state + x.e;
@@ -625,106 +680,78 @@ struct Weights {
     }
 };
 
-// A wave's rows as right operands, straight from memory (zero behind the last)
-template <int DT, int D, int IT>
-__device__ __forceinline__ void load_rows(typename El<DT>::Op (&x)[IT][D / El<DT>::KS], const typename El<DT>::T* from,
-                                          int64_t stride, int row0, int rows, int d, int g, int i) {
+// A wave's 16 rows as right operands, straight from memory (zero behind the
+// last); from: the wave's first row, rows: as many as there are from it on
+template <int DT, int D>
+__device__ __forceinline__ void load_rows(typename El<DT>::Op (&x)[D / El<DT>::KS], const typename El<DT>::T* from,
+                                          int64_t stride, int rows, int d, int g, int i) {
     using Op = typename El<DT>::Op;
-    constexpr int KS = El<DT>::KS;
+    constexpr int KS = El<DT>::KS, e = sizeof(typename El<DT>::T);
+    const uint32_t sb = (uint32_t)(stride * e);
+    const Bytes b = bytes_from(from, rows_bytes(min(rows, 16), sb, d, e));
 #pragma unroll
-    for (int it = 0; it < IT; ++it)
-#pragma unroll
-        for (int k = 0; k < D / KS; ++k) {
-            const int row = row0 + 16 * it + i, c = KS * k + KS / 4 * g;
-            x[it][k] = Op{};
-            if (row < rows && c < d) x[it][k] = ld_g<Op>(from + row * stride + c);
-        }
-}
-
-// p[jt][it]: scores of 32 keys from k0 of the tile on and the wave's rows
-template <int DT, int D, int IT>
-__device__ __forceinline__ void scores(f32x4 (&p)[2][IT], const typename El<DT>::T* tile, int k0,
-                                       const typename El<DT>::Op (&x)[IT][D / El<DT>::KS], int g, int i) {
-    constexpr int KS = El<DT>::KS, LD = D + El<DT>::PAD;
-#pragma unroll
-    for (int jt = 0; jt < 2; ++jt) {
-#pragma unroll
-        for (int it = 0; it < IT; ++it) p[jt][it] = zero4();
-#pragma unroll
-        for (int k = 0; k < D / KS; ++k) {
-            const auto op = row_op<DT>(tile + (k0 + 16 * jt + i) * LD + KS * k, g);
-#pragma unroll
-            for (int it = 0; it < IT; ++it) p[jt][it] = mm(op, x[it][k], p[jt][it]);
-        }
+    for (int k = 0; k < D / KS; ++k) {
+        const int c = KS * k + KS / 4 * g;
+        x[k] = __builtin_bit_cast(Op, ld_bytes(b, c < d ? (uint32_t)i * sb + (uint32_t)(c * e) : kNowhere));
     }
 }
-// acc[it][mt] += (columns of 32 rows of the tile) p
-template <int DT, int D, int IT>
-__device__ __forceinline__ void gather(f32x4 (&acc)[IT][D / 16], const f32x4 (&p)[2][IT], const typename El<DT>::T* tile,
-                                       int k0, int g, int i) {
+
+// p[jt]: scores of the tile's 32 keys and the wave's rows
+template <int DT, int D>
+__device__ __forceinline__ void scores(f32x4 (&p)[2], const typename El<DT>::T* tile,
+                                       const typename El<DT>::Op (&x)[D / El<DT>::KS], int g, int i) {
+    constexpr int KS = El<DT>::KS, LD = D + El<DT>::PAD;
+    p[0] = p[1] = zero4();
+#pragma unroll
+    for (int k = 0; k < D / KS; ++k)
+#pragma unroll
+        for (int jt = 0; jt < 2; ++jt) p[jt] = mm(row_op<DT>(tile + (16 * jt + i) * LD + KS * k, g), x[k], p[jt]);
+}
+// acc[mt] += (columns 16 mt .. of the tile's 32 rows) p
+template <int DT, int D>
+__device__ __forceinline__ void gather(f32x4 (&acc)[D / 16], const f32x4 (&p)[2], const typename El<DT>::T* tile, int g, int i) {
     constexpr int LD = D + El<DT>::PAD;
     if constexpr (DT == GDN_BF16) {
-        u16x8 hi[IT], lo[IT];
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            u16x4 h0, l0, h1, l1;
-            split4(p[0][it], h0, l0);
-            split4(p[1][it], h1, l1);
-            hi[it] = cat(h0, h1);
-            lo[it] = cat(l0, l1);
-        }
+        u16x4 h0, l0, h1, l1;
+        split4(p[0], h0, l0);
+        split4(p[1], h1, l1);
+        const u16x8 hi = cat(h0, h1), lo = cat(l0, l1);
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
-            const u16x8 col = col_op_acc<DT>(tile, LD, k0, 16 * mt, g, i);
-#pragma unroll
-            for (int it = 0; it < IT; ++it) acc[it][mt] = mm(col, hi[it], mm(col, lo[it], acc[it][mt]));
+            const u16x8 col = col_op_acc<DT>(tile, LD, 0, 16 * mt, g, i);
+            acc[mt] = mm(col, hi, mm(col, lo, acc[mt]));
         }
     } else {
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
-            for (int jt = 0; jt < 2; ++jt) {
-                const f32x4 col = col_op_acc<DT>(tile, LD, k0 + 16 * jt, 16 * mt, g, i);
-#pragma unroll
-                for (int it = 0; it < IT; ++it) acc[it][mt] = mm(col, p[jt][it], acc[it][mt]);
-            }
+            for (int jt = 0; jt < 2; ++jt) acc[mt] = mm(col_op_acc<DT>(tile, LD, 16 * jt, 16 * mt, g, i), p[jt], acc[mt]);
     }
 }
 
-// M X for the state's product, 32 rows of M (TR: columns) at a time through LDS,
-// split into terms there; use(mt, it, t): rows 16 mt .. of M X.  M has dm rows and
-// dx columns, TR: dx rows and dm columns.
-template <int DT, int DX, int DM, bool TR>
-constexpr int slab_size() {
-    constexpr int PAD = El<DT>::PAD;
-    return El<DT>::TERMS * (TR ? DX * (32 + PAD) : 32 * (DX + PAD));
-}
-template <int DT, int DX, int DM, int IT, bool TR, class F>
-__device__ __forceinline__ void state_rows(const float* M, typename El<DT>::T* slab,
-                                           const typename El<DT>::Op (&x)[IT][DX / El<DT>::KS], int dx, int dm, int tid, F use) {
+// 32 rows (TR: columns) of a state [dv][dk] on their way to LDS, where they lie
+// split into terms, and their products with a wave's rows.
+template <int DT, int DV, int DK, bool TR>
+struct Slab {
+    using T = typename El<DT>::T;
     using Op = typename El<DT>::Op;
-    constexpr int KS = El<DT>::KS, NP = DX / 32, LD = TR ? 32 + El<DT>::PAD : DX + El<DT>::PAD;
-    constexpr int LO = slab_size<DT, DX, DM, TR>() / El<DT>::TERMS;
-    const int l = tid & 63, g = l >> 4, i = l & 15;
+    static constexpr int DX = TR ? DV : DK;  // what is contracted
+    static constexpr int W = TR ? 32 : DK, LD = TR ? 36 : DK + El<DT>::PAD, ROWS = TR ? DV : 32, LO = ROWS * LD;
+    static constexpr int kSize = El<DT>::TERMS * LO, NP = DX / 32;
     f32x4 r[NP];
-    auto fetch = [&](int m0) {
+    __device__ __forceinline__ void fetch(const float* M, int m0, int dv, int dk, int tid) {
+        const Bytes b = bytes_from(M, (uint32_t)(dv * dk * 4));
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            const int p = tid + kThreads * k, row = TR ? p / 8 : p / (DX / 4), c = 4 * (TR ? p % 8 : p % (DX / 4));
-            r[k] = zero4();
-            if (TR ? row < dx && m0 + c < dm : m0 + row < dm && c < dx)
-                r[k] = ld_g<f32x4>(M + (TR ? row * dm + m0 + c : (m0 + row) * dx + c));
+            const int p = tid + kThreads * k, row = p / (W / 4) + (TR ? 0 : m0), c = 4 * (p % (W / 4)) + (TR ? m0 : 0);
+            r[k] = __builtin_bit_cast(f32x4, ld_bytes(b, c < dk ? (uint32_t)(row * dk + c) * 4u : kNowhere));
         }
-    };
-    fetch(0);
-#pragma unroll
-    for (int m0 = 0; m0 < DM; m0 += 32) {
-        if (m0 >= dm) break;
-        __syncthreads();
+    }
+    __device__ __forceinline__ void put(T* slab, int tid) const {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            const int p = tid + kThreads * k, row = TR ? p / 8 : p / (DX / 4), c = 4 * (TR ? p % 8 : p % (DX / 4));
-            auto* to = slab + row * LD + c;
+            const int p = tid + kThreads * k;
+            T* to = slab + p / (W / 4) * LD + 4 * (p % (W / 4));
             if constexpr (DT == GDN_BF16) {
                 u16x4 hi, lo;
                 split4(r[k], hi, lo);
@@ -734,27 +761,22 @@ __device__ __forceinline__ void state_rows(const float* M, typename El<DT>::T* s
                 *reinterpret_cast<f32x4*>(to) = r[k];
             }
         }
-        if (m0 + 32 < dm) fetch(m0 + 32);
-        __syncthreads();
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            f32x4 t[IT];
-#pragma unroll
-            for (int it = 0; it < IT; ++it) t[it] = zero4();
-#pragma unroll
-            for (int k = 0; k < DX / KS; ++k)
-#pragma unroll
-                for (int e = El<DT>::TERMS - 1; e >= 0; --e) {
-                    const Op op = TR ? col_op<DT>(slab + e * LO, LD, KS * k, 16 * m, g, i)
-                                     : row_op<DT>(slab + e * LO + (16 * m + i) * LD + KS * k, g);
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) t[it] = mm(op, x[it][k], t[it]);
-                }
-            use(m0 / 16 + m, t);
-        }
     }
-    __syncthreads();
-}
+    // rows (TR: columns) 16 m .. of the slab times the rows x
+    static __device__ __forceinline__ f32x4 times(const T* slab, int m, const Op (&x)[DX / El<DT>::KS], int g, int i) {
+        constexpr int KS = El<DT>::KS;
+        f32x4 t = zero4();
+#pragma unroll
+        for (int k = 0; k < DX / KS; ++k)
+#pragma unroll
+            for (int e = El<DT>::TERMS - 1; e >= 0; --e) {
+                const Op op = TR ? col_op<DT>(slab + e * LO, LD, KS * k, 16 * m, g, i)
+                                 : row_op<DT>(slab + e * LO + (16 * m + i) * LD + KS * k, g);
+                t = mm(op, x[k], t);
+            }
+        return t;
+    }
+};
 
 // Four features of a row, rounded once
 template <int DT>
@@ -767,275 +789,199 @@ __device__ __forceinline__ void st4(typename El<DT>::T* to, const f32x4& x) {
 __device__ __forceinline__ const float* state_before(const Lin& a, const Seg& sg, int64_t si, int h) {
     if (!(sg.ends & kFirst)) return a.s_seg + ((si - 1) * a.Hv + h) * (int64_t)a.state;
     const float* src = start_of(a, sg.seq, h);
-    if (!src || !a.s_copy) return src;
-    // (its rank: the first segments before it are counted in a.first)
-    int lo = 0, hi = a.count[0];
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.first[mid] <= si) lo = mid;
-        else hi = mid;
-    }
-    return a.s_copy + ((int64_t)lo * a.Hv + h) * a.state;
+    return src && a.s_copy ? a.s_copy + ((int64_t)sg.rank() * a.Hv + h) * a.state : src;
+}
+// The gradient of the state behind segment si, or null (zero)
+__device__ __forceinline__ const float* gradient_behind(const Lin& a, const Seg& sg, int64_t si, int h) {
+    if (!(sg.ends & kLast)) return a.g_seg + ((si + 1) * a.Hv + h) * (int64_t)a.state;
+    return a.ds_out ? a.ds_out + ((int64_t)sg.seq * a.Hv + h) * a.state : nullptr;
 }
 
-// Rows up to i: the forward's outputs (BACK false; a workgroup a value head) and
-// dq (a workgroup a key head, its value heads one after the other in one sum).
-constexpr int kIT = 2, kBlockRows = 64 * kIT;
-template <int DT, int DX, int DM, bool BACK>
-__global__ __launch_bounds__(kThreads, 2) void k_lin_rows(Lin a) {
+// The four results and what they are made of
+enum Kind { kOut, kDq, kDk, kDv };
+template <int KIND>
+struct Made {
+    static constexpr bool REV = KIND == kDk || KIND == kDv;  // over the tokens from i on
+    static constexpr bool TR = KIND == kDq || KIND == kDk;   // the state's transpose
+    static constexpr bool SUM = TR;                          // of a key head, over its value heads
+};
+struct Rows {  // an array's rows, one behind the other by token
+    const void* at;
+    int64_t stride;
+    bool key;  // heads are key heads
+};
+template <int KIND>
+__device__ __forceinline__ void made_of(const Lin& a, Rows& x, Rows& left, Rows& right) {
+    const Linear& p = a.p;
+    const Rows q{p.q, p.q_stride, true}, k{p.k, p.k_stride, true}, v{p.v, p.v_stride, false},
+        o{a.dout, (int64_t)a.Hv * p.dv, false};
+    x = KIND == kOut ? q : KIND == kDq ? o : KIND == kDk ? v : k;
+    left = KIND == kOut ? k : KIND == kDq ? v : KIND == kDk ? o : q;
+    right = KIND == kOut ? v : KIND == kDq ? k : KIND == kDk ? q : o;
+}
+
+// x, not known to be what it was: what a loop's body derives from it is formed
+// anew in every round and holds no registers across it.
+__device__ __forceinline__ int anew(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// A workgroup has 64 rows of a head, 16 a wave; dq's and dk's are a key head's, its
+// value heads one after the other in one sum.  64 rows and tiles of 32 tokens keep
+// it to 128 registers and 39 KB of LDS (bf16, heads of 128): four of them share a
+// compute unit and hide each other's waits.
+constexpr int kBlockRows = 64;
+template <int DT, int DK, int DV>
+constexpr int rows_lds() {
+    constexpr int tiles = 2 * (Tile<DT, DK>::kSize + Tile<DT, DV>::kSize);
+    return std::max(tiles, 2 * std::max(Slab<DT, DV, DK, false>::kSize, Slab<DT, DV, DK, true>::kSize));
+}
+template <int DT, int DK, int DV, int KIND, bool SLOPES>
+__device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned blocks, typename El<DT>::T* lds, float* tab,
+                                        float* sums) {
     using E = El<DT>;
     using T = typename E::T;
     using Op = typename E::Op;
-    constexpr int TT = E::TT, IT = kIT;
+    constexpr bool REV = Made<KIND>::REV, TR = Made<KIND>::TR, SUM = Made<KIND>::SUM;
+    constexpr int DX = TR ? DV : DK, DM = TR ? DK : DV, TT = E::TT;
     using TA = Tile<DT, DX>;
     using TB = Tile<DT, DM>;
-    static_assert(slab_size<DT, DX, DM, BACK>() <= 2 * TA::kSize, "a slab of the state fits the tiles");
-    __shared__ __attribute__((aligned(16))) T la[2 * TA::kSize];
-    __shared__ __attribute__((aligned(16))) T lb[2 * TB::kSize];
-    __shared__ __attribute__((aligned(16))) float tab[kSegMax];
-    __shared__ float sums[kThreads / 64];
+    using SL = Slab<DT, DV, DK, TR>;
     const Linear& p = a.p;
-    const int heads = BACK ? (int)p.Hk : a.Hv, nh = BACK ? a.group : 1;
-    const unsigned nrb = (a.seg + kBlockRows - 1) / kBlockRows;
-    const unsigned block = on_one_xcd(blockIdx.x, gridDim.x, BACK ? nrb : nrb * a.group), id = block / nrb;
-    const int rb = block - id * nrb, hh = id % heads;
+    const int heads = SUM ? (int)p.Hk : a.Hv, nh = SUM ? a.group : 1;
+    const unsigned nrb = a.seg / kBlockRows;
+    const unsigned b = on_one_xcd(block, blocks, SUM ? nrb : nrb * a.group), id = b / nrb;
+    const int rb = b - id * nrb, hh = id % heads;
     const int64_t si = id / heads;
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g = l >> 4, i = l & 15;
-    const Seg sg = si < a.count[1] ? a.segs[si] : Seg{0, 0, 0, 0};
-    const bool slopes = BACK && a.dalpha;
-    float* part = slopes ? a.part + (int64_t)hh * nh * a.parts + si * nrb + rb : nullptr;
+    const int thread = threadIdx.x, w = __builtin_amdgcn_readfirstlane(thread >> 6);
+    const Seg sg = segment(a, si);
+    float* part = SLOPES ? a.part + (int64_t)hh * nh * a.parts + ((KIND - 1) * a.nseg + si) * nrb + rb : nullptr;
     if (rb * kBlockRows >= sg.n) {
-        for (int j = tid; slopes && j < nh; j += kThreads) part[j * a.parts] = 0.f;
+        for (int j = thread; SLOPES && j < nh; j += kThreads) part[j * a.parts] = 0.f;
         return;
     }
-    const int dx = (int)(BACK ? p.dv : p.dk), dm = (int)(BACK ? p.dk : p.dv);
-    const int64_t xs = BACK ? (int64_t)a.Hv * p.dv : p.q_stride, as = BACK ? p.v_stride : p.k_stride,
-                  bs = BACK ? p.k_stride : p.v_stride;
-    const int row0 = rb * kBlockRows + 16 * IT * w, rblk = row0 / 16;
-    const int nkeys = min(sg.n, (rb + 1) * kBlockRows), nt = (nkeys + TT - 1) / TT;
+    const int dk = (int)p.dk, dv = (int)p.dv, dx = TR ? dv : dk, dm = TR ? dk : dv;
+    Rows X, A, B;
+    made_of<KIND>(a, X, A, B);
+    const int row0 = rb * kBlockRows + 16 * w, rblk = row0 / 16;
+    // tiles of keys
+    const int first = REV ? rb * kBlockRows / TT : 0, nkeys = REV ? sg.n : min(sg.n, (rb + 1) * kBlockRows),
+              nt = (nkeys + TT - 1) / TT;
 
-    f32x4 acc[IT][DM / 16];
+    f32x4 acc[DM / 16];
 #pragma unroll
-    for (int it = 0; it < IT; ++it)
-#pragma unroll
-        for (int mt = 0; mt < DM / 16; ++mt) acc[it][mt] = zero4();
+    for (int mt = 0; mt < DM / 16; ++mt) acc[mt] = zero4();
     for (int j = 0; j < nh; ++j) {
-        const int h = hh * nh + j, hk = BACK ? hh : hh / a.group;
-        const T* xp = static_cast<const T*>(BACK ? a.dout : p.q) + sg.begin * xs + (int64_t)(BACK ? h : hk) * dx;
-        const T* ap = static_cast<const T*>(BACK ? p.v : p.k) + sg.begin * as + (int64_t)(BACK ? h : hk) * dx;
-        const T* bp = static_cast<const T*>(BACK ? p.k : p.v) + sg.begin * bs + (int64_t)(BACK ? hk : h) * dm;
-        const Decay decay(p.alpha[h]);
+        const int tid = SUM ? anew(thread) : thread, g = (tid & 63) >> 4, i = tid & 15, row = row0 + i;
+        const int h = hh * nh + j, hk = SUM ? hh : hh / a.group;
+        const T* xp = static_cast<const T*>(X.at) + (sg.begin + row0) * X.stride + (int64_t)(X.key ? hk : h) * dx;
+        const T* ap = static_cast<const T*>(A.at) + sg.begin * A.stride + (int64_t)(A.key ? hk : h) * dx;
+        const T* bp = static_cast<const T*>(B.at) + sg.begin * B.stride + (int64_t)(B.key ? hk : h) * dm;
+        const float* M = REV ? gradient_behind(a, sg, si, h) : state_before(a, sg, si, h);
+        SL sl;
+        if (M) sl.fetch(M, 0, dv, dk, tid);
+        Op x[DX / E::KS];
+        load_rows<DT, DX>(x, xp, X.stride, sg.n - row0, dx, g, i);
+        const Decay decay(a, h);
         if (j > 0) __syncthreads();
-        Weights<false>::fill(decay, tab, a.seg, tid);
-        Weights<false> weight;
+        Weights<REV>::fill(decay, tab, a.seg, tid);
+        Weights<REV> weight;
         weight.set(decay, p.scale, tab, g, i);
-        Op x[IT][DX / E::KS];
-        load_rows<DT, DX, IT>(x, xp, xs, row0, sg.n, dx, g, i);
+        float da = 0.f;
+        const typename TA::At aa(A.stride, dx, tid);
+        const typename TB::At ab(B.stride, dm, tid);
         TA ta;
         TB tb;
-        const float* M = state_before(a, sg, si, h);
-        float da = 0.f;
+        auto fetch = [&](int t) {
+            ta.fetch(ap + t * TT * A.stride, aa, nkeys - t * TT);
+            tb.fetch(bp + t * TT * B.stride, ab, nkeys - t * TT);
+        };
         if (M) {
-            float f[IT], df[IT];
+            // (a power below zero: no row)
+            const int e = REV ? sg.n - 1 - row : row + 1;
+            const float scale = REV ? 1.f : p.scale, f = e >= 0 ? scale * decay(e) : 0.f,
+                        df = e > 0 ? scale * (float)e * decay(e - 1) : 0.f;
+            // rows of the token that the product is multiplied with for dalpha: q, v
+            const int64_t with = KIND == kDq ? (sg.begin + row) * p.q_stride + hk * dm : (sg.begin + row) * p.v_stride + h * dm;
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int row = row0 + 16 * it + i;
-                df[it] = p.scale * (float)(row + 1) * decay(row);
-                f[it] = p.scale * decay(row + 1);
-            }
-            state_rows<DT, DX, DM, IT, BACK>(M, la, x, dx, dm, tid, [&](int mt, const f32x4 (&t)[IT]) {
+            for (int s = 0; s < DM / 32; ++s) {
+                if (32 * s >= dm) break;
+                T* slab = lds + (s & 1) * SL::kSize;
+                sl.put(slab, tid);
+                if (s + 1 < DM / 32) sl.fetch(M, 32 * (s + 1), dv, dk, tid);
+                else fetch(first);
+                __syncthreads();
 #pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    acc[it][mt] += f[it] * t[it];
-                    if constexpr (BACK) {
-                        const int row = row0 + 16 * it + i, c = 16 * mt + 4 * g;
-                        if (slopes && row < sg.n && c < dm)
-                            da += df[it] * dot4e(t[it], ld4e<DT>(p.q, (sg.begin + row) * p.q_stride + hk * dm + c));
+                for (int m = 0; m < 2; ++m) {
+                    const f32x4 t = SL::times(slab, m, x, g, i);
+                    acc[2 * s + m] += f * t;
+                    if constexpr (SLOPES && (KIND == kDq || KIND == kDv)) {
+                        const int c = 32 * s + 16 * m + 4 * g;
+                        if (row < sg.n && c < dm) da += df * dot4e(t, ld4e<DT>(KIND == kDq ? p.q : p.v, with + c));
                     }
                 }
-            });
+            }
+            __syncthreads();
         }
-        ta.fetch(ap, as, nkeys, dx, tid);
-        tb.fetch(bp, bs, nkeys, dm, tid);
-        for (int t = 0; t < nt; ++t) {
-            T *ba = la + (t & 1) * TA::kSize, *bb = lb + (t & 1) * TB::kSize;
+        if (!M || dm <= DM - 32) fetch(first);
+        Op x2[SLOPES && KIND == kDk ? DK / E::KS : 1];
+        if constexpr (SLOPES && KIND == kDk)
+            load_rows<DT, DK>(x2, static_cast<const T*>(p.k) + (sg.begin + row0) * p.k_stride + (int64_t)hk * dk, p.k_stride,
+                              sg.n - row0, dk, g, i);
+        for (int t = first; t < nt; ++t) {
+            T *ba = lds + (t & 1) * TA::kSize, *bb = lds + 2 * TA::kSize + (t & 1) * TB::kSize;
             ta.put(ba, tid);
             tb.put(bb, tid);
-            if (t + 1 < nt) {
-                ta.fetch(ap + (t + 1) * TT * as, as, nkeys - (t + 1) * TT, dx, tid);
-                tb.fetch(bp + (t + 1) * TT * bs, bs, nkeys - (t + 1) * TT, dm, tid);
-            }
+            fetch(t + 1);
             __syncthreads();
+            const int kblk = t * TT / 16;
+            if (REV ? kblk + 1 < rblk : kblk > rblk) continue;
+            f32x4 s[2];
+            scores<DT, DX>(s, ba, x, g, i);
+            if constexpr (SLOPES && KIND == kDk) {
+                f32x4 r[2];
+                scores<DT, DK>(r, bb, x2, g, i);
 #pragma unroll
-            for (int k0 = 0; k0 < TT; k0 += 32) {
-                const int kblk = (t * TT + k0) / 16;
-                if (kblk > rblk + IT - 1) continue;
-                f32x4 s[2][IT];
-                scores<DT, DX, IT>(s, ba, k0, x, g, i);
+                for (int jt = 0; jt < 2; ++jt) {
+                    const int D = kblk + jt - rblk;
+                    const f32x4 u = weight.slope(D, g, i);
 #pragma unroll
-                for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) s[jt][it] = weight(s[jt][it], rblk + it - kblk - jt, g, i);
-                gather<DT, DM, IT>(acc, s, bb, k0, g, i);
+                    for (int e = 0; e < 4; ++e)
+                        da += D > 0 || (D == 0 && weight.seen(g, i, e)) ? u[e] * s[jt][e] * r[jt][e] : 0.f;
+                }
             }
+#pragma unroll
+            for (int jt = 0; jt < 2; ++jt) s[jt] = weight(s[jt], REV ? kblk + jt - rblk : rblk - kblk - jt, g, i);
+            gather<DT, DM>(acc, s, bb, g, i);
         }
-        if (slopes) sum_to(da, sums, part + j * a.parts, tid);
+        if constexpr (SLOPES) sum_to(da, sums, part + j * a.parts, tid);
     }
-    T* out = static_cast<T*>(BACK ? a.dq : p.out) + (int64_t)hh * dm;
+    T* out = static_cast<T*>(KIND == kOut ? p.out : KIND == kDq ? a.dq : KIND == kDk ? a.dk : a.dv) + (int64_t)hh * dm;
     const int64_t os = (int64_t)heads * dm;
+    const int g = (thread & 63) >> 4, row = row0 + (thread & 15);
+    if (row < sg.n)
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
-        const int row = row0 + 16 * it + i;
-        if (row < sg.n)
-#pragma unroll
-            for (int mt = 0; mt < DM / 16; ++mt)
-                if (16 * mt < dm) st4<DT>(out + (sg.begin + row) * os + 16 * mt + 4 * g, acc[it][mt]);
-    }
+        for (int mt = 0; mt < DM / 16; ++mt)
+            if (16 * mt < dm) st4<DT>(out + (sg.begin + row) * os + 16 * mt + 4 * g, acc[mt]);
 }
 
-// Rows from j on: dk and dv together, whose products read the same tiles of q and
-// do.  A workgroup a key head; dk is summed over its value heads.
-template <int DT, int DK, int DV, int IT>
-__global__ __launch_bounds__(kThreads) void k_lin_dkv(Lin a) {
-    using E = El<DT>;
-    using T = typename E::T;
-    using Op = typename E::Op;
-    constexpr int TT = E::TT, kRows = 64 * IT;
-    using TQ = Tile<DT, DK>;
-    using TO = Tile<DT, DV>;
-    constexpr int SLAB = std::max(slab_size<DT, DK, DV, false>(), slab_size<DT, DV, DK, true>());
-    static_assert(SLAB <= 2 * TQ::kSize + 2 * TO::kSize, "a slab of the state fits the tiles");
-    __shared__ __attribute__((aligned(16))) T tiles[2 * TQ::kSize + 2 * TO::kSize];
+template <int DT, int DK, int DV>
+__global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 4 : 2) void k_lin_out(Lin a) {
+    __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV>()];
+    __shared__ __attribute__((aligned(16))) float tab[kSegMax];
+    rows_of<DT, DK, DV, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, nullptr);
+}
+// dq and dk of the key heads (blocks_k of each) and dv of the value heads
+template <int DT, int DK, int DV, bool SLOPES>
+__global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 3 : 2) void k_lin_grads(Lin a, unsigned blocks_k) {
+    __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV>()];
     __shared__ __attribute__((aligned(16))) float tab[kSegMax];
     __shared__ float sums[kThreads / 64];
-    T *lq = tiles, *lo = tiles + 2 * TQ::kSize;
-    const Linear& p = a.p;
-    const unsigned nrb = (a.seg + kRows - 1) / kRows;
-    const unsigned block = on_one_xcd(blockIdx.x, gridDim.x, nrb), id = block / nrb;
-    const int rb = block - id * nrb, hk = id % (int)p.Hk;
-    const int64_t si = id / (int)p.Hk;
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g = l >> 4, i = l & 15;
-    const Seg sg = si < a.count[1] ? a.segs[si] : Seg{0, 0, 0, 0};
-    const bool slopes = a.dalpha;
-    float* part = slopes ? a.part + (int64_t)hk * a.group * a.parts + a.part_dkv + si * nrb + rb : nullptr;
-    if (rb * kRows >= sg.n) {
-        for (int j = tid; slopes && j < a.group; j += kThreads) part[j * a.parts] = 0.f;
-        return;
-    }
-    const int dk = (int)p.dk, dv = (int)p.dv;
-    const int64_t os = (int64_t)a.Hv * dv;
-    const int row0 = rb * kRows + 16 * IT * w, rblk = row0 / 16;
-    const int first = rb * kRows / TT, nt = (sg.n + TT - 1) / TT;
-
-    Op xk[IT][DK / E::KS];
-    load_rows<DT, DK, IT>(xk, static_cast<const T*>(p.k) + sg.begin * p.k_stride + (int64_t)hk * dk, p.k_stride, row0, sg.n, dk,
-                          g, i);
-    const T* qp = static_cast<const T*>(p.q) + sg.begin * p.q_stride + (int64_t)hk * dk;
-    f32x4 ak[IT][DK / 16];
-#pragma unroll
-    for (int it = 0; it < IT; ++it)
-#pragma unroll
-        for (int mt = 0; mt < DK / 16; ++mt) ak[it][mt] = zero4();
-    for (int j = 0; j < a.group; ++j) {
-        const int h = hk * a.group + j;
-        const T* vp = static_cast<const T*>(p.v) + sg.begin * p.v_stride + (int64_t)h * dv;
-        const T* op = static_cast<const T*>(a.dout) + sg.begin * os + (int64_t)h * dv;
-        const Decay decay(p.alpha[h]);
-        if (j > 0) __syncthreads();
-        Weights<true>::fill(decay, tab, a.seg, tid);
-        Weights<true> weight;
-        weight.set(decay, p.scale, tab, g, i);
-        Op xv[IT][DV / E::KS];
-        load_rows<DT, DV, IT>(xv, vp, p.v_stride, row0, sg.n, dv, g, i);
-        f32x4 av[IT][DV / 16];
-#pragma unroll
-        for (int it = 0; it < IT; ++it)
-#pragma unroll
-            for (int mt = 0; mt < DV / 16; ++mt) av[it][mt] = zero4();
-        const float* G = !(sg.ends & kLast) ? a.g_seg + ((si + 1) * a.Hv + h) * (int64_t)a.state
-                         : a.ds_out         ? a.ds_out + ((int64_t)sg.seq * a.Hv + h) * a.state
-                                            : nullptr;
-        float da = 0.f;
-        if (G) {
-            float f[IT], df[IT];
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int e = sg.n - 1 - (row0 + 16 * it + i);  // (below zero: no row)
-                f[it] = e >= 0 ? decay(e) : 0.f;
-                df[it] = e > 0 ? (float)e * decay(e - 1) : 0.f;
-            }
-            state_rows<DT, DK, DV, IT, false>(G, tiles, xk, dk, dv, tid, [&](int mt, const f32x4 (&t)[IT]) {
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    av[it][mt] += f[it] * t[it];
-                    const int row = row0 + 16 * it + i, c = 16 * mt + 4 * g;
-                    if (slopes && row < sg.n && c < dv)
-                        da += df[it] * dot4e(t[it], ld4e<DT>(p.v, (sg.begin + row) * p.v_stride + (int64_t)h * dv + c));
-                }
-            });
-            state_rows<DT, DV, DK, IT, true>(G, tiles, xv, dv, dk, tid, [&](int mt, const f32x4 (&t)[IT]) {
-#pragma unroll
-                for (int it = 0; it < IT; ++it) ak[it][mt] += f[it] * t[it];
-            });
-        }
-        TQ tq;
-        TO to;
-        tq.fetch(qp + first * TT * p.q_stride, p.q_stride, sg.n - first * TT, dk, tid);
-        to.fetch(op + first * TT * os, os, sg.n - first * TT, dv, tid);
-        for (int t = first; t < nt; ++t) {
-            T *bq = lq + (t & 1) * TQ::kSize, *bo = lo + (t & 1) * TO::kSize;
-            tq.put(bq, tid);
-            to.put(bo, tid);
-            if (t + 1 < nt) {
-                tq.fetch(qp + (t + 1) * TT * p.q_stride, p.q_stride, sg.n - (t + 1) * TT, dk, tid);
-                to.fetch(op + (t + 1) * TT * os, os, sg.n - (t + 1) * TT, dv, tid);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k0 = 0; k0 < TT; k0 += 32) {
-                const int kblk = (t * TT + k0) / 16;
-                if (kblk + 1 < rblk) continue;
-                f32x4 s[2][IT], r[2][IT];
-                scores<DT, DK, IT>(s, bq, k0, xk, g, i);
-                scores<DT, DV, IT>(r, bo, k0, xv, g, i);
-#pragma unroll
-                for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) {
-                        const int D = kblk + jt - rblk - it;
-                        if (slopes) {
-                            const f32x4 u = weight.slope(D, g, i);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                da += D > 0 || (D == 0 && weight.seen(g, i, e)) ? u[e] * s[jt][it][e] * r[jt][it][e] : 0.f;
-                        }
-                        s[jt][it] = weight(s[jt][it], D, g, i);
-                        r[jt][it] = weight(r[jt][it], D, g, i);
-                    }
-                gather<DT, DV, IT>(av, s, bo, k0, g, i);
-                gather<DT, DK, IT>(ak, r, bq, k0, g, i);
-            }
-        }
-        T* out = static_cast<T*>(a.dv) + (int64_t)h * dv;
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const int row = row0 + 16 * it + i;
-            if (row < sg.n)
-#pragma unroll
-                for (int mt = 0; mt < DV / 16; ++mt)
-                    if (16 * mt < dv) st4<DT>(out + (sg.begin + row) * os + 16 * mt + 4 * g, av[it][mt]);
-        }
-        if (slopes) sum_to(da, sums, part + j * a.parts, tid);
-    }
-    T* out = static_cast<T*>(a.dk) + (int64_t)hk * dk;
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-        const int row = row0 + 16 * it + i;
-        if (row < sg.n)
-#pragma unroll
-            for (int mt = 0; mt < DK / 16; ++mt)
-                if (16 * mt < dk) st4<DT>(out + (sg.begin + row) * (p.Hk * dk) + 16 * mt + 4 * g, ak[it][mt]);
-    }
+    const unsigned b = blockIdx.x;
+    if (b < blocks_k) rows_of<DT, DK, DV, kDk, SLOPES>(a, b, blocks_k, lds, tab, sums);
+    else if (b < 2 * blocks_k) rows_of<DT, DK, DV, kDq, SLOPES>(a, b - blocks_k, blocks_k, lds, tab, sums);
+    else rows_of<DT, DK, DV, kDv, SLOPES>(a, b - 2 * blocks_k, gridDim.x - 2 * blocks_k, lds, tab, sums);
 }
 
 // ---------------------------------------------------------------------------
@@ -1065,8 +1011,8 @@ bool overlap(const Linear& p) {
 bool in_chunks(const Linear& p) { return std::min(p.N, p.max_len) >= kLinMin; }
 
 struct LinLayout {
-    size_t count, seqs, first, segs, s_seg, s_copy, g_seg, part, total;
-    int64_t parts, part_dkv, part_scan;
+    size_t count, seqs, first, segs, log2a, s_seg, s_copy, g_seg, part, total;
+    int64_t parts, part_scan;
 };
 LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
     LinLayout L{};
@@ -1080,13 +1026,12 @@ LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
     L.seqs = take(4 * (size_t)z.nrank);
     L.first = take(4 * ((size_t)z.nrank + 1));
     L.segs = take(sizeof(Seg) * (size_t)z.nseg);
+    L.log2a = take(4 * (size_t)p.Hv);
     const size_t head = sizeof(float) * (size_t)(p.Hv * p.dk * p.dv);
     L.s_seg = take(head * z.nseg);
     if (back) {
         L.g_seg = take(head * z.nseg);
-        const int64_t rows = z.nseg * ((z.seg + kBlockRows - 1) / kBlockRows);
-        L.part_dkv = rows;
-        L.part_scan = L.part_dkv + z.nseg * (z.seg / 64);
+        L.part_scan = 3 * z.nseg * (z.seg / kBlockRows);  // of dq, dk and dv
         L.parts = L.part_scan + z.nrank * scan_blocks(p);
         L.part = take(sizeof(float) * (size_t)(L.parts * p.Hv));
     } else {
@@ -1112,14 +1057,15 @@ void place(Lin& a, const LinSizes& z, const LinLayout& L, char* base) {
     a.seqs = reinterpret_cast<int32_t*>(base + L.seqs);
     a.first = reinterpret_cast<int32_t*>(base + L.first);
     a.segs = reinterpret_cast<Seg*>(base + L.segs);
+    a.log2a = reinterpret_cast<float*>(base + L.log2a);
     a.s_seg = reinterpret_cast<float*>(base + L.s_seg);
 }
 
-template <class K>
-hipError_t launch(const char* name, K kernel, dim3 grid, int threads, const Lin& a, hipStream_t st) {
+template <class K, class... More>
+hipError_t launch(const char* name, K kernel, dim3 grid, int threads, const Lin& a, hipStream_t st, More... more) {
     if (grid.x == 0) return hipSuccess;
     prof_begin(a.p.timer, name, st);
-    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, a);
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, a, more...);
     prof_end(a.p.timer, st);
     return hipGetLastError();
 }
@@ -1144,22 +1090,20 @@ hipError_t forward_chunks(const Lin& a, hipStream_t st) {
     if (e != hipSuccess) return e;
     e = launch("k_lin_scan", k_lin_scan, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))), kThreads, a, st);
     if (e != hipSuccess) return e;
-    const int64_t nrb = (a.seg + kBlockRows - 1) / kBlockRows;
-    return launch("k_lin_out", k_lin_rows<DT, DK, DV, false>, dim3((unsigned)(a.nseg * nrb * p.Hv)), kThreads, a, st);
+    return launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (a.seg / kBlockRows) * p.Hv)), kThreads, a, st);
 }
 template <int DT, int DK, int DV>
 hipError_t backward_chunks(const Lin& a, hipStream_t st) {
-    constexpr int IT = DT == GDN_BF16 ? 1 : 1;
     const Linear& p = a.p;
     hipError_t e = launch("k_lin_badd", k_lin_add<DT, DV, DK>, dim3((unsigned)(a.nseg * p.Hv), 2), kThreads, a, st);
     if (e != hipSuccess) return e;
     e = launch("k_lin_bscan", k_lin_bscan, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))), kThreads, a, st);
     if (e != hipSuccess) return e;
-    const int64_t nrb = (a.seg + kBlockRows - 1) / kBlockRows;
-    e = launch("k_lin_dq", k_lin_rows<DT, DV, DK, true>, dim3((unsigned)(a.nseg * nrb * p.Hk)), kThreads, a, st);
-    if (e != hipSuccess) return e;
-    const int64_t nkb = a.seg / (64 * IT);
-    e = launch("k_lin_dkv", k_lin_dkv<DT, DK, DV, IT>, dim3((unsigned)(a.nseg * nkb * p.Hk)), kThreads, a, st);
+    const int64_t units = a.nseg * (a.seg / kBlockRows);
+    const unsigned blocks_k = (unsigned)(units * p.Hk);
+    const dim3 grid(2 * blocks_k + (unsigned)(units * p.Hv));
+    e = a.dalpha ? launch("k_lin_grads", k_lin_grads<DT, DK, DV, true>, grid, kThreads, a, st, blocks_k)
+                 : launch("k_lin_grads", k_lin_grads<DT, DK, DV, false>, grid, kThreads, a, st, blocks_k);
     if (e != hipSuccess || !a.dalpha) return e;
     return launch("k_lin_dalpha", k_lin_dalpha, dim3((unsigned)p.Hv), 1024, a, st);
 }
@@ -1214,7 +1158,6 @@ hipError_t linear_backward(const LinearBwd& b, void* ws, hipStream_t st) {
     a.g_seg = reinterpret_cast<float*>(base + L.g_seg);
     a.part = reinterpret_cast<float*>(base + L.part);
     a.parts = L.parts;
-    a.part_dkv = L.part_dkv;
     a.part_scan = L.part_scan;
     a.dout = b.dout;
     a.ds_out = b.ds_out;

@@ -218,21 +218,24 @@ __global__ __launch_bounds__(kThreads) void k_qk_norm_bwd(QkArgs A) {
 }
 
 // dw: 16 features of q or of k a block, the partial rows in a fixed order
-__global__ __launch_bounds__(kThreads) void k_qk_norm_params(QkArgs A, float* dwq, float* dwk) {
-    __shared__ float sums[16][17];
-    const int sets = A.d / 16, f = 16 * (blockIdx.x % sets) + threadIdx.x % 16, r = threadIdx.x / 16;
+constexpr int kParamThreads = 1024;
+__global__ __launch_bounds__(kParamThreads) void k_qk_norm_params(QkArgs A, float* dwq, float* dwk) {
+    constexpr int NR = kParamThreads / 16;
+    __shared__ float sums[NR][17];
+    const int sets = A.d / 16, c = threadIdx.x % 16, f = 16 * (blockIdx.x % sets) + c, r = threadIdx.x / 16;
     const bool second = (int)blockIdx.x >= sets;
     const Side& S = A.side[second];
     float* dw = second ? dwk : dwq;
     if (!dw) return;
     float y = 0.f;
-    for (unsigned b = r; b < S.blocks; b += 16) y += S.part[(int64_t)b * A.d + f];
-    sums[r][threadIdx.x % 16] = y;
-    __syncthreads();
-    if (r > 0) return;
-    y = 0.f;
-    for (int i = 0; i < 16; ++i) y += sums[i][threadIdx.x];
-    dw[f] = y;
+#pragma unroll 8
+    for (unsigned b = r; b < S.blocks; b += NR) y += S.part[(int64_t)b * A.d + f];
+    sums[r][c] = y;
+    for (int o = NR / 2; o > 0; o /= 2) {
+        __syncthreads();
+        if (r < o) sums[r][c] += sums[r + o][c];
+    }
+    if (r == 0) dw[f] = sums[0][c];
 }
 
 // Lanes a row: d / 8 or the next power of two
@@ -331,7 +334,7 @@ hipError_t qk_norm_bwd(const QkNorm& p, hipStream_t st) {
     }
     if (!p.dwq && !p.dwk) return hipSuccess;
     prof_begin(p.timer, "k_qk_norm_params", st);
-    hipLaunchKernelGGL(k_qk_norm_params, dim3(2 * (unsigned)p.d / 16), dim3(kThreads), 0, st, A, p.dwq, p.dwk);
+    hipLaunchKernelGGL(k_qk_norm_params, dim3(2 * (unsigned)p.d / 16), dim3(kParamThreads), 0, st, A, p.dwq, p.dwk);
     prof_end(p.timer, st);
     return hipGetLastError();
 }
