@@ -26,8 +26,8 @@ namespace {
 
 // Sequences of fewer tokens go token by token (forward).
 constexpr int kLinMin = 32;
-// Tokens of a segment at most.
-constexpr int kSegMax = 512;
+// Tokens of a segment.
+constexpr int kSeg = 256;
 
 // A segment: its tokens, its sequence, whether it is that one's first or last,
 // and above these two bits that one's rank.
@@ -42,7 +42,6 @@ struct Lin {
     Offsets at;
     int Hv, group;
     int state;           // elements of a state
-    int seg;             // tokens a segment
     int64_t chunk_min;   // sequences of fewer tokens have no segments
     int64_t nrank, nseg; // the most sequences with segments, and segments
     int32_t* count;      // [2]: such sequences, segments
@@ -103,7 +102,7 @@ __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
     for (int h = tid; h < a.Hv; h += kThreads) a.log2a[h] = (float)log2((double)a.p.alpha[h]);
     const int64_t S = a.at.S, run = (S + kThreads - 1) / kThreads, r0 = min(tid * run, S), r1 = min(r0 + run, S);
     const int w = tid >> 6, lane = tid & 63;
-    auto segs_of = [&](int64_t n) { return (uint32_t)((n + a.seg - 1) / a.seg); };
+    auto segs_of = [&](int64_t n) { return (uint32_t)((n + kSeg - 1) / kSeg); };
     uint32_t at[2] = {0, 0};
     for (int64_t s = r0; s < r1; ++s) {
         const int64_t n = span_of(a.at, s).n;
@@ -159,13 +158,13 @@ __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
         }
         const int s = a.seqs[lo];
         const Span sp = span_of(a.at, s);
-        const int64_t from = (int64_t)(i - (lo < kPlanLds ? lfirst[lo] : a.first[lo])) * a.seg;
+        const int64_t from = (int64_t)(i - (lo < kPlanLds ? lfirst[lo] : a.first[lo])) * kSeg;
         Seg x;
-        x.n = (int)max<int64_t>(min<int64_t>(a.seg, sp.n - from), 0);
+        x.n = (int)max<int64_t>(min<int64_t>(kSeg, sp.n - from), 0);
         x.begin = x.n > 0 ? (int)(sp.begin + from) : 0;
         x.seq = s;
         // (where the table ends, so does the sequence: no segment looks behind it)
-        x.ends = (from == 0 ? kFirst : 0) | (from + a.seg >= sp.n || i + 1 == total[1] ? kLast : 0) | lo << 2;
+        x.ends = (from == 0 ? kFirst : 0) | (from + kSeg >= sp.n || i + 1 == total[1] ? kLast : 0) | lo << 2;
         a.segs[i] = x;
     }
 }
@@ -339,20 +338,28 @@ __device__ __forceinline__ uint32_t rows_bytes(int rows, uint32_t stride, int d,
     return rows > 0 ? (uint32_t)(rows - 1) * stride + (uint32_t)(d * e) : 0u;
 }
 
+// No instruction moves across this.  The products below ask for a batch of
+// operands from LDS and only then work on the one before it (left to itself, the
+// compiler keeps few operands in few registers and waits for each), and tiles on
+// their way are asked for in the order in which they are waited for, on every path
+// into a loop (else its waits are for all of them).
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // A tile of TT tokens' rows of D features (d of them real) on its way to LDS;
 // rows behind the last and features past d are zero there.
-template <int DT, int D>
+template <int DT, int D, int NT>
 struct Tile {
     using T = typename El<DT>::T;
-    static constexpr int TT = El<DT>::TT, LD = D + El<DT>::PAD, V = 16 / sizeof(T), PPR = D / V, NP = TT * PPR / kThreads;
+    static constexpr int TT = El<DT>::TT, LD = D + El<DT>::PAD, V = 16 / sizeof(T), PPR = D / V, ALL = TT * PPR;
+    static constexpr int NP = ALL < NT ? 1 : ALL / NT;  // (fewer pieces than threads: the rest has none)
     static constexpr int kSize = TT * LD;
-    static_assert(NP * kThreads == TT * PPR && kThreads % PPR == 0, "whole rounds of whole rows");
+    static_assert(ALL < NT || (NP * NT == ALL && NT % PPR == 0), "whole rounds of whole rows");
     struct At {  // a thread's pieces
         uint32_t stride, first;
         int d;
         __device__ __forceinline__ At(int64_t elements, int d, int tid) : stride((uint32_t)(elements * sizeof(T))), d(d) {
             const int c = V * (tid % PPR);
-            first = c < d ? (uint32_t)(tid / PPR) * stride + (uint32_t)(c * sizeof(T)) : kNowhere;
+            first = c < d && tid < ALL ? (uint32_t)(tid / PPR) * stride + (uint32_t)(c * sizeof(T)) : kNowhere;
         }
     };
     u32x4 r[NP];
@@ -360,12 +367,13 @@ struct Tile {
         const Bytes b = bytes_from(from, rows_bytes(min(rows, TT), at.stride, at.d, sizeof(T)));
 #pragma unroll
         for (int k = 0; k < NP; ++k)
-            r[k] = ld_bytes(b, at.first == kNowhere ? kNowhere : at.first + (uint32_t)k * (kThreads / PPR) * at.stride);
+            r[k] = ld_bytes(b, at.first == kNowhere ? kNowhere : at.first + (uint32_t)k * (NT / PPR) * at.stride);
     }
     __device__ __forceinline__ void put(T* tile, int tid) const {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            const int p = tid + kThreads * k;
+            const int p = tid + NT * k;
+            if (ALL < NT && p >= ALL) return;
             *reinterpret_cast<u32x4*>(tile + p / PPR * LD + V * (p % PPR)) = r[k];
         }
     }
@@ -394,11 +402,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a) {
     using T = typename E::T;
     using Op = typename E::Op;
     constexpr int TT = E::TT, KS = E::KS, RT = DV / 64, CT = DK / 16;
-    using TX = Tile<DT, DV>;
-    using TY = Tile<DT, DK>;
+    using TX = Tile<DT, DV, kThreads>;
+    using TY = Tile<DT, DK, kThreads>;
     __shared__ __attribute__((aligned(16))) T lx[2][TX::kSize];
     __shared__ __attribute__((aligned(16))) T ly[2][TY::kSize];
-    __shared__ __attribute__((aligned(16))) float wt[kSegMax];
+    __shared__ __attribute__((aligned(16))) float wt[kSeg];
     const Linear& p = a.p;
     const bool rev = blockIdx.y == 1;
     const unsigned id = on_one_xcd(blockIdx.x, gridDim.x, a.group);
@@ -411,7 +419,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a) {
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = (tid & 63) >> 4, i = tid & 15;
     const int dk = (int)p.dk, dv = (int)p.dv;
     const Decay decay(a, h);
-    for (int j = tid; j < a.seg; j += kThreads)
+    for (int j = tid; j < kSeg; j += kThreads)
         wt[j] = j >= sg.n ? 0.f : rev ? p.scale * decay(j + 1) : decay(sg.n - 1 - j);
     const int hk = h / a.group;
     const int64_t xs = rev ? (int64_t)a.Hv * dv : p.v_stride, ys = rev ? p.q_stride : p.k_stride;
@@ -436,7 +444,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a) {
         const T *bx = lx[b], *by = ly[b];
         tx[b].put(lx[b], tid);
         ty[b].put(ly[b], tid);
+        in_order();
         fetch(t + 2, b);
+        in_order();
         __syncthreads();
 #pragma unroll
         for (int k0 = 0; k0 < TT; k0 += KS) {
@@ -468,12 +478,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a) {
         }
     };
     // two tiles ahead
+    in_order();
     fetch(0, 0);
+    in_order();
     fetch(1, 1);
-    for (int t = 0; t < nt; t += 2) {
+    in_order();
+    // (a step behind the loop, not a way out of its middle: that would be taken for
+    // a way back to its start, with other loads in flight)
+    int t = 0;
+    for (; t + 1 < nt; t += 2) {
         step(t, 0);
-        if (t + 1 < nt) step(t + 1, 1);
+        step(t + 1, 1);
     }
+    if (t < nt) step(t, 0);
     // the accumulator: column 4 g .. of 16 c, row i of the wave's
     float* out = (rev ? a.g_seg : a.s_seg) + (si * a.Hv + h) * (int64_t)a.state;
 #pragma unroll
@@ -544,7 +561,7 @@ __global__ __launch_bounds__(kThreads) void k_lin_scan(Lin a) {
         if (a.s_copy) st_g(a.s_copy + ((int64_t)x.r * a.Hv + x.h) * a.state + x.e, S);
     }
     const Decay decay(a, x.h);
-    const float whole = decay(a.seg), rest = decay((int)(x.sp.n - (int64_t)(x.G - 1) * a.seg));
+    const float whole = decay(kSeg), rest = decay((int)(x.sp.n - (int64_t)(x.G - 1) * kSeg));
     const int64_t stride = (int64_t)a.Hv * a.state;
     float* at = a.s_seg + ((int64_t)x.f * a.Hv + x.h) * a.state + x.e;
     scan_places<false>(at, stride, dst ? x.G : x.G - 1, [&](int g, const f32x4& add) {
@@ -555,11 +572,16 @@ __global__ __launch_bounds__(kThreads) void k_lin_scan(Lin a) {
 }
 
 // The workgroup's sum of x, in a fixed order, written by one thread.
+template <int NT>
 __device__ __forceinline__ void sum_to(float x, float* sums, float* to, int tid) {
     x = xor32_sum(row_sum<32>(x));
     if ((tid & 63) == 0) sums[tid >> 6] = x;
     __syncthreads();
-    if (tid == 0) *to = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    if (tid == 0) {
+        x = 0.f;
+        for (int i = 0; i < NT / 64; ++i) x += sums[i];
+        *to = x;
+    }
     __syncthreads();
 }
 
@@ -572,8 +594,8 @@ __global__ __launch_bounds__(kThreads) void k_lin_bscan(Lin a) {
     float da = 0.f;
     if (x.on) {
         const Decay decay(a, x.h);
-        const int n_last = (int)(x.sp.n - (int64_t)(x.G - 1) * a.seg);
-        const float whole = decay(a.seg), rest = x.G > 0 ? decay(n_last) : 1.f;
+        const int n_last = (int)(x.sp.n - (int64_t)(x.G - 1) * kSeg);
+        const float whole = decay(kSeg), rest = x.G > 0 ? decay(n_last) : 1.f;
         const int64_t stride = (int64_t)a.Hv * a.state, off = ((int64_t)x.f * a.Hv + x.h) * a.state + x.e;
         const float* src = start_of(a, x.s, x.h);
         const f32x4 S0 = src ? ld_g<f32x4>(src + x.e) : zero4();
@@ -588,7 +610,7 @@ __global__ __launch_bounds__(kThreads) void k_lin_bscan(Lin a) {
         float* ga = a.g_seg + off;
         // (without a gradient of the start state the first segment adds nothing)
         const int lowest = a.ds0 ? 0 : 1;
-        const float dw = (float)a.seg * decay(a.seg - 1), dr = (float)n_last * decay(n_last - 1);
+        const float dw = (float)kSeg * decay(kSeg - 1), dr = (float)n_last * decay(n_last - 1);
         scan_places<true>(ga + lowest * stride, stride, x.G - lowest, [&](int g, const f32x4& add) {
             g += lowest;
             if (a.dalpha) {
@@ -604,7 +626,7 @@ __global__ __launch_bounds__(kThreads) void k_lin_bscan(Lin a) {
     if (a.dalpha) {
         const unsigned per = ((unsigned)a.state + 4 * kThreads - 1) / (4 * kThreads), id = blockIdx.x / per;
         const int64_t r = id / a.Hv, h = id - r * a.Hv;
-        sum_to(da, sums, a.part + h * a.parts + a.part_scan + r * per + (blockIdx.x - id * per), tid);
+        sum_to<kThreads>(da, sums, a.part + h * a.parts + a.part_scan + r * per + (blockIdx.x - id * per), tid);
     }
 }
 
@@ -656,16 +678,20 @@ struct Weights {
             du[e] = d > 0 ? scale * (float)d * decay(d - 1) : 0.f;
         }
     }
-    static __device__ __forceinline__ void fill(const Decay& decay, float* table, int n, int tid) {
-        for (int x = tid; x < n; x += kThreads) table[x] = decay(REV ? x : x + 15 - 2 * (x & 15));
+    static __device__ __forceinline__ void fill(const Decay& decay, float* table, int n, int tid, int threads) {
+        for (int x = tid; x < n; x += threads) table[x] = decay(REV ? x : x + 15 - 2 * (x & 15));
     }
     __device__ __forceinline__ bool seen(int g, int i, int e) const { return REV ? 4 * g + e >= i : i >= 4 * g + e; }
-    // scores of keys of block kb and rows of block rb, weighted
-    __device__ __forceinline__ f32x4 operator()(const f32x4& p, int D, int g, int i) const {
-        if (D > 0) return p * (rl * *reinterpret_cast<const f32x4*>(tab + 16 * (D - 1) + 4 * g));
-        f32x4 y;
+    // factors of the scores of a block of keys D blocks from the rows'
+    __device__ __forceinline__ f32x4 factors(int D, int g) const {
+        return D > 0 ? rl * *reinterpret_cast<const f32x4*>(tab + 16 * (D - 1) + 4 * g) : dw;
+    }
+    // the scores p times them; zero on the other side, whatever p is
+    __device__ __forceinline__ f32x4 weighted(const f32x4& p, const f32x4& f, int D, int g, int i) const {
+        f32x4 y = p * f;
+        if (D <= 0)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = D == 0 && seen(g, i, e) ? p[e] * dw[e] : 0.f;
+            for (int e = 0; e < 4; ++e) y[e] = D == 0 && seen(g, i, e) ? y[e] : 0.f;
         return y;
     }
     // their derivatives with respect to a
@@ -680,77 +706,123 @@ struct Weights {
     }
 };
 
-// A wave's 16 rows as right operands, straight from memory (zero behind the
+// A wave's 16 IT rows as right operands, straight from memory (zero behind the
 // last); from: the wave's first row, rows: as many as there are from it on
-template <int DT, int D>
-__device__ __forceinline__ void load_rows(typename El<DT>::Op (&x)[D / El<DT>::KS], const typename El<DT>::T* from,
+template <int DT, int D, int IT>
+__device__ __forceinline__ void load_rows(typename El<DT>::Op (&x)[IT][D / El<DT>::KS], const typename El<DT>::T* from,
                                           int64_t stride, int rows, int d, int g, int i) {
     using Op = typename El<DT>::Op;
     constexpr int KS = El<DT>::KS, e = sizeof(typename El<DT>::T);
     const uint32_t sb = (uint32_t)(stride * e);
-    const Bytes b = bytes_from(from, rows_bytes(min(rows, 16), sb, d, e));
+    const Bytes b = bytes_from(from, rows_bytes(min(rows, 16 * IT), sb, d, e));
 #pragma unroll
-    for (int k = 0; k < D / KS; ++k) {
-        const int c = KS * k + KS / 4 * g;
-        x[k] = __builtin_bit_cast(Op, ld_bytes(b, c < d ? (uint32_t)i * sb + (uint32_t)(c * e) : kNowhere));
-    }
+    for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int k = 0; k < D / KS; ++k) {
+            const int c = KS * k + KS / 4 * g;
+            x[it][k] = __builtin_bit_cast(Op, ld_bytes(b, c < d ? (uint32_t)(16 * it + i) * sb + (uint32_t)(c * e) : kNowhere));
+        }
+}
+
+// Four features from c on of a wave's row i, from a buffer of its rows
+template <int DT>
+__device__ __forceinline__ f32x4 row_piece(Bytes rows, uint32_t stride, int i, int c) {
+    if constexpr (DT == GDN_BF16)
+        return cvt<DT>(__builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rows, (int)((uint32_t)i * stride + 2u * c), 0, 0)));
+    else
+        return __builtin_bit_cast(f32x4, ld_bytes(rows, (uint32_t)i * stride + 4u * c));
 }
 
 // p[jt]: scores of the tile's 32 keys and the wave's rows
 template <int DT, int D>
-__device__ __forceinline__ void scores(f32x4 (&p)[2], const typename El<DT>::T* tile,
-                                       const typename El<DT>::Op (&x)[D / El<DT>::KS], int g, int i) {
-    constexpr int KS = El<DT>::KS, LD = D + El<DT>::PAD;
-    p[0] = p[1] = zero4();
+struct ScoreOps {
+    using Op = typename El<DT>::Op;
+    static constexpr int KS = El<DT>::KS, LD = D + El<DT>::PAD, N = D / KS;
+    Op op[2][N];
+    __device__ __forceinline__ void load(const typename El<DT>::T* tile, int g, int i) {
 #pragma unroll
-    for (int k = 0; k < D / KS; ++k)
+        for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int jt = 0; jt < 2; ++jt) p[jt] = mm(row_op<DT>(tile + (16 * jt + i) * LD + KS * k, g), x[k], p[jt]);
-}
-// acc[mt] += (columns 16 mt .. of the tile's 32 rows) p
+            for (int jt = 0; jt < 2; ++jt) op[jt][k] = row_op<DT>(tile + (16 * jt + i) * LD + KS * k, g);
+    }
+    __device__ __forceinline__ void times(f32x4 (&p)[2], const Op (&x)[N]) const {
+        p[0] = p[1] = zero4();
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int jt = 0; jt < 2; ++jt) p[jt] = mm(op[jt][k], x[k], p[jt]);
+    }
+};
+// acc[mt] += (columns 16 mt .. of the tile's 32 rows) p, B columns' blocks a batch
 template <int DT, int D>
-__device__ __forceinline__ void gather(f32x4 (&acc)[D / 16], const f32x4 (&p)[2], const typename El<DT>::T* tile, int g, int i) {
-    constexpr int LD = D + El<DT>::PAD;
-    if constexpr (DT == GDN_BF16) {
-        u16x4 h0, l0, h1, l1;
-        split4(p[0], h0, l0);
-        split4(p[1], h1, l1);
-        const u16x8 hi = cat(h0, h1), lo = cat(l0, l1);
+struct ColumnOps {
+    using Op = typename El<DT>::Op;
+    static constexpr int LD = D + El<DT>::PAD, PER = DT == GDN_BF16 ? 1 : 2, B = 4 / PER, N = D / 16 / B;
+    Op op[B][PER];
+    __device__ __forceinline__ void load(const typename El<DT>::T* tile, int n, int g, int i) {
 #pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt) {
-            const u16x8 col = col_op_acc<DT>(tile, LD, 0, 16 * mt, g, i);
-            acc[mt] = mm(col, hi, mm(col, lo, acc[mt]));
+        for (int m = 0; m < B; ++m)
+#pragma unroll
+            for (int j = 0; j < PER; ++j) op[m][j] = col_op_acc<DT>(tile, LD, 16 * j, 16 * (n * B + m), g, i);
+    }
+};
+template <int DT, int D, int IT>
+__device__ __forceinline__ void gather(f32x4 (&acc)[IT][D / 16], const f32x4 (&p)[IT][2], ColumnOps<DT, D>& first,
+                                       const typename El<DT>::T* tile, int g, int i) {
+    using C = ColumnOps<DT, D>;
+    typename El<DT>::Op t[IT][2];  // the terms (bf16), the two blocks (fp32)
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        if constexpr (DT == GDN_BF16) {
+            u16x4 h0, l0, h1, l1;
+            split4(p[it][0], h0, l0);
+            split4(p[it][1], h1, l1);
+            t[it][0] = cat(l0, l1);
+            t[it][1] = cat(h0, h1);
+        } else {
+            t[it][0] = p[it][0];
+            t[it][1] = p[it][1];
         }
-    } else {
+    }
+    C next;
 #pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt)
+    for (int n = 0; n < C::N; ++n) {
+        C &now = n & 1 ? next : first, &then = n & 1 ? first : next;
+        if (n + 1 < C::N) then.load(tile, n + 1, g, i);
+        in_order();
 #pragma unroll
-            for (int jt = 0; jt < 2; ++jt) acc[mt] = mm(col_op_acc<DT>(tile, LD, 16 * jt, 16 * mt, g, i), p[jt], acc[mt]);
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int m = 0; m < C::B; ++m)
+#pragma unroll
+                for (int it = 0; it < IT; ++it)
+                    acc[it][n * C::B + m] = mm(now.op[m][e % C::PER], t[it][e], acc[it][n * C::B + m]);
+        in_order();
     }
 }
 
 // 32 rows (TR: columns) of a state [dv][dk] on their way to LDS, where they lie
 // split into terms, and their products with a wave's rows.
-template <int DT, int DV, int DK, bool TR>
+template <int DT, int DV, int DK, bool TR, int NT>
 struct Slab {
     using T = typename El<DT>::T;
     using Op = typename El<DT>::Op;
     static constexpr int DX = TR ? DV : DK;  // what is contracted
     static constexpr int W = TR ? 32 : DK, LD = TR ? 36 : DK + El<DT>::PAD, ROWS = TR ? DV : 32, LO = ROWS * LD;
-    static constexpr int kSize = El<DT>::TERMS * LO, NP = DX / 32;
+    static constexpr int kSize = El<DT>::TERMS * LO, NP = 8 * DX / NT;
     f32x4 r[NP];
     __device__ __forceinline__ void fetch(const float* M, int m0, int dv, int dk, int tid) {
         const Bytes b = bytes_from(M, (uint32_t)(dv * dk * 4));
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            const int p = tid + kThreads * k, row = p / (W / 4) + (TR ? 0 : m0), c = 4 * (p % (W / 4)) + (TR ? m0 : 0);
+            const int p = tid + NT * k, row = p / (W / 4) + (TR ? 0 : m0), c = 4 * (p % (W / 4)) + (TR ? m0 : 0);
             r[k] = __builtin_bit_cast(f32x4, ld_bytes(b, c < dk ? (uint32_t)(row * dk + c) * 4u : kNowhere));
         }
     }
     __device__ __forceinline__ void put(T* slab, int tid) const {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            const int p = tid + kThreads * k;
+            const int p = tid + NT * k;
             T* to = slab + p / (W / 4) * LD + 4 * (p % (W / 4));
             if constexpr (DT == GDN_BF16) {
                 u16x4 hi, lo;
@@ -762,19 +834,31 @@ struct Slab {
             }
         }
     }
-    // rows (TR: columns) 16 m .. of the slab times the rows x
-    static __device__ __forceinline__ f32x4 times(const T* slab, int m, const Op (&x)[DX / El<DT>::KS], int g, int i) {
-        constexpr int KS = El<DT>::KS;
-        f32x4 t = zero4();
+};
+// Rows (TR: columns) 16 m .. of a state that lies in LDS in terms LO elements
+// apart, LD elements a row, as operands; K of them contract all features.
+template <int DT, int D, bool TR, int LD, int LO>
+struct StateOps {
+    using Op = typename El<DT>::Op;
+    static constexpr int KS = El<DT>::KS, K = D / KS, TERMS = El<DT>::TERMS;
+    Op op[K][TERMS];
+    __device__ __forceinline__ void load(const typename El<DT>::T* at, int m, int g, int i) {
 #pragma unroll
-        for (int k = 0; k < DX / KS; ++k)
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = El<DT>::TERMS - 1; e >= 0; --e) {
-                const Op op = TR ? col_op<DT>(slab + e * LO, LD, KS * k, 16 * m, g, i)
-                                 : row_op<DT>(slab + e * LO + (16 * m + i) * LD + KS * k, g);
-                t = mm(op, x[k], t);
-            }
-        return t;
+            for (int e = 0; e < TERMS; ++e)
+                op[k][e] = TR ? col_op<DT>(at + e * LO, LD, KS * k, 16 * m, g, i)
+                              : row_op<DT>(at + e * LO + (16 * m + i) * LD + KS * k, g);
+    }
+    __device__ __forceinline__ f32x4 times(const Op (&x)[K]) const {
+        f32x4 t[TERMS];
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e) t[e] = zero4();
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e) t[e] = mm(op[k][e], x[k], t[e]);
+        return TERMS == 2 ? t[0] + t[TERMS - 1] : t[0];
     }
 };
 
@@ -827,15 +911,13 @@ __device__ __forceinline__ int anew(int x) {
     return x;
 }
 
-// A workgroup has 64 rows of a head, 16 a wave; dq's and dk's are a key head's, its
-// value heads one after the other in one sum.  64 rows and tiles of 32 tokens keep
-// it to 128 registers and 39 KB of LDS (bf16, heads of 128): four of them share a
-// compute unit and hide each other's waits.
-constexpr int kBlockRows = 64;
+// A workgroup has 128 rows of a head, 32 a wave; dq's and dk's are a key head's,
+// its value heads one after the other in one sum.
+constexpr int kIT = 2, kBlockRows = 64 * kIT;
 template <int DT, int DK, int DV>
 constexpr int rows_lds() {
-    constexpr int tiles = 2 * (Tile<DT, DK>::kSize + Tile<DT, DV>::kSize);
-    return std::max(tiles, 2 * std::max(Slab<DT, DV, DK, false>::kSize, Slab<DT, DV, DK, true>::kSize));
+    constexpr int tiles = 2 * (Tile<DT, DK, kThreads>::kSize + Tile<DT, DV, kThreads>::kSize);
+    return std::max(tiles, 2 * std::max(Slab<DT, DV, DK, false, kThreads>::kSize, Slab<DT, DV, DK, true, kThreads>::kSize));
 }
 template <int DT, int DK, int DV, int KIND, bool SLOPES>
 __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned blocks, typename El<DT>::T* lds, float* tab,
@@ -844,13 +926,14 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
     using T = typename E::T;
     using Op = typename E::Op;
     constexpr bool REV = Made<KIND>::REV, TR = Made<KIND>::TR, SUM = Made<KIND>::SUM;
-    constexpr int DX = TR ? DV : DK, DM = TR ? DK : DV, TT = E::TT;
-    using TA = Tile<DT, DX>;
-    using TB = Tile<DT, DM>;
-    using SL = Slab<DT, DV, DK, TR>;
+    constexpr int DX = TR ? DV : DK, DM = TR ? DK : DV, TT = E::TT, NT = kThreads, IT = kIT;
+    using TA = Tile<DT, DX, NT>;
+    using TB = Tile<DT, DM, NT>;
+    using SL = Slab<DT, DV, DK, TR, NT>;
+    using SO = StateOps<DT, DX, TR, SL::LD, SL::LO>;
     const Linear& p = a.p;
     const int heads = SUM ? (int)p.Hk : a.Hv, nh = SUM ? a.group : 1;
-    const unsigned nrb = a.seg / kBlockRows;
+    constexpr unsigned nrb = kSeg / kBlockRows;
     const unsigned b = on_one_xcd(block, blocks, SUM ? nrb : nrb * a.group), id = b / nrb;
     const int rb = b - id * nrb, hh = id % heads;
     const int64_t si = id / heads;
@@ -858,22 +941,24 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
     const Seg sg = segment(a, si);
     float* part = SLOPES ? a.part + (int64_t)hh * nh * a.parts + ((KIND - 1) * a.nseg + si) * nrb + rb : nullptr;
     if (rb * kBlockRows >= sg.n) {
-        for (int j = thread; SLOPES && j < nh; j += kThreads) part[j * a.parts] = 0.f;
+        for (int j = thread; SLOPES && j < nh; j += NT) part[j * a.parts] = 0.f;
         return;
     }
     const int dk = (int)p.dk, dv = (int)p.dv, dx = TR ? dv : dk, dm = TR ? dk : dv;
     Rows X, A, B;
     made_of<KIND>(a, X, A, B);
-    const int row0 = rb * kBlockRows + 16 * w, rblk = row0 / 16;
+    const int row0 = rb * kBlockRows + 16 * IT * w, rblk = row0 / 16;
     // tiles of keys
     const int first = REV ? rb * kBlockRows / TT : 0, nkeys = REV ? sg.n : min(sg.n, (rb + 1) * kBlockRows),
               nt = (nkeys + TT - 1) / TT;
 
-    f32x4 acc[DM / 16];
+    f32x4 acc[IT][DM / 16];
 #pragma unroll
-    for (int mt = 0; mt < DM / 16; ++mt) acc[mt] = zero4();
+    for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int mt = 0; mt < DM / 16; ++mt) acc[it][mt] = zero4();
     for (int j = 0; j < nh; ++j) {
-        const int tid = SUM ? anew(thread) : thread, g = (tid & 63) >> 4, i = tid & 15, row = row0 + i;
+        const int tid = SUM ? anew(thread) : thread, g = (tid & 63) >> 4, i = tid & 15;
         const int h = hh * nh + j, hk = SUM ? hh : hh / a.group;
         const T* xp = static_cast<const T*>(X.at) + (sg.begin + row0) * X.stride + (int64_t)(X.key ? hk : h) * dx;
         const T* ap = static_cast<const T*>(A.at) + sg.begin * A.stride + (int64_t)(A.key ? hk : h) * dx;
@@ -881,102 +966,148 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
         const float* M = REV ? gradient_behind(a, sg, si, h) : state_before(a, sg, si, h);
         SL sl;
         if (M) sl.fetch(M, 0, dv, dk, tid);
-        Op x[DX / E::KS];
-        load_rows<DT, DX>(x, xp, X.stride, sg.n - row0, dx, g, i);
+        Op x[IT][DX / E::KS];
+        load_rows<DT, DX, IT>(x, xp, X.stride, sg.n - row0, dx, g, i);
         const Decay decay(a, h);
         if (j > 0) __syncthreads();
-        Weights<REV>::fill(decay, tab, a.seg, tid);
+        Weights<REV>::fill(decay, tab, kSeg, tid, NT);
         Weights<REV> weight;
         weight.set(decay, p.scale, tab, g, i);
         float da = 0.f;
         const typename TA::At aa(A.stride, dx, tid);
         const typename TB::At ab(B.stride, dm, tid);
-        TA ta;
-        TB tb;
-        auto fetch = [&](int t) {
-            ta.fetch(ap + t * TT * A.stride, aa, nkeys - t * TT);
-            tb.fetch(bp + t * TT * B.stride, ab, nkeys - t * TT);
+        TA ta[2];
+        TB tb[2];
+        auto fetch = [&](int t, int b) {
+            in_order();
+            ta[b].fetch(ap + t * TT * A.stride, aa, nkeys - t * TT);
+            tb[b].fetch(bp + t * TT * B.stride, ab, nkeys - t * TT);
+            in_order();
         };
         if (M) {
-            // (a power below zero: no row)
-            const int e = REV ? sg.n - 1 - row : row + 1;
-            const float scale = REV ? 1.f : p.scale, f = e >= 0 ? scale * decay(e) : 0.f,
-                        df = e > 0 ? scale * (float)e * decay(e - 1) : 0.f;
-            // rows of the token that the product is multiplied with for dalpha: q, v
-            const int64_t with = KIND == kDq ? (sg.begin + row) * p.q_stride + hk * dm : (sg.begin + row) * p.v_stride + h * dm;
+            float f[IT], df[IT];
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const int row = row0 + 16 * it + i, e = REV ? sg.n - 1 - row : row + 1;  // (below zero: no row)
+                const float scale = REV ? 1.f : p.scale;
+                f[it] = e >= 0 ? scale * decay(e) : 0.f;
+                df[it] = e > 0 ? scale * (float)e * decay(e - 1) : 0.f;
+            }
+            // rows that the product is multiplied with for dalpha: q, v
+            const Rows W = KIND == kDq ? Rows{p.q, p.q_stride, true} : Rows{p.v, p.v_stride, false};
+            const uint32_t ws = (uint32_t)(W.stride * sizeof(T));
+            const Bytes wb = bytes_from(static_cast<const T*>(W.at) + (sg.begin + row0) * W.stride + (int64_t)(W.key ? hk : h) * dm,
+                                        rows_bytes(min(sg.n - row0, 16 * IT), ws, dm, sizeof(T)));
 #pragma unroll
             for (int s = 0; s < DM / 32; ++s) {
                 if (32 * s >= dm) break;
                 T* slab = lds + (s & 1) * SL::kSize;
                 sl.put(slab, tid);
                 if (s + 1 < DM / 32) sl.fetch(M, 32 * (s + 1), dv, dk, tid);
-                else fetch(first);
                 __syncthreads();
+                SO so;
+                so.load(slab, 0, g, i);
+                in_order();
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const f32x4 t = SL::times(slab, m, x, g, i);
-                    acc[2 * s + m] += f * t;
-                    if constexpr (SLOPES && (KIND == kDq || KIND == kDv)) {
-                        const int c = 32 * s + 16 * m + 4 * g;
-                        if (row < sg.n && c < dm) da += df * dot4e(t, ld4e<DT>(KIND == kDq ? p.q : p.v, with + c));
+                    f32x4 t[IT];
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) t[it] = so.times(x[it]);
+                    if (m == 0) so.load(slab, 1, g, i);
+                    in_order();
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) {
+                        acc[it][2 * s + m] += f[it] * t[it];
+                        if constexpr (SLOPES && (KIND == kDq || KIND == kDv))
+                            if (32 * s + 16 * m < dm)
+                                da += df[it] * dot4e(t[it], row_piece<DT>(wb, ws, 16 * it + i, 32 * s + 16 * m + 4 * g));
+                    }
+                }
+                in_order();
+            }
+            __syncthreads();
+        }
+        fetch(first, 0);
+        fetch(first + 1, 1);
+        Op x2[SLOPES && KIND == kDk ? IT : 1][DK / E::KS];
+        if constexpr (SLOPES && KIND == kDk)
+            load_rows<DT, DK, IT>(x2, static_cast<const T*>(p.k) + (sg.begin + row0) * p.k_stride + (int64_t)hk * dk, p.k_stride,
+                                  sg.n - row0, dk, g, i);
+        auto step = [&](int t, int b) {
+            T *ba = lds + b * TA::kSize, *bb = lds + 2 * TA::kSize + b * TB::kSize;
+            ta[b].put(ba, tid);
+            tb[b].put(bb, tid);
+            fetch(t + 2, b);
+            __syncthreads();
+            const int kblk = t * TT / 16;
+            if (REV ? kblk + 1 < rblk : kblk > rblk + IT - 1) return;
+            auto between = [&](int it, int jt) { return REV ? kblk + jt - rblk - it : rblk + it - kblk - jt; };
+            ScoreOps<DT, DX> ops;
+            ops.load(ba, g, i);
+            in_order();
+            f32x4 s[IT][2];
+#pragma unroll
+            for (int it = 0; it < IT; ++it) ops.times(s[it], x[it]);
+            if constexpr (SLOPES && KIND == kDk) {
+                ScoreOps<DT, DK> qops;
+                qops.load(bb, g, i);
+                in_order();
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    f32x4 r[2];
+                    qops.times(r, x2[it]);
+#pragma unroll
+                    for (int jt = 0; jt < 2; ++jt) {
+                        const int D = between(it, jt);
+                        const f32x4 u = weight.slope(D, g, i);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            da += D > 0 || (D == 0 && weight.seen(g, i, e)) ? u[e] * s[it][jt][e] * r[jt][e] : 0.f;
                     }
                 }
             }
-            __syncthreads();
+            ColumnOps<DT, DM> cols;
+            cols.load(bb, 0, g, i);
+            in_order();
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll
+                for (int jt = 0; jt < 2; ++jt)
+                    s[it][jt] = weight.weighted(s[it][jt], weight.factors(between(it, jt), g), between(it, jt), g, i);
+            gather<DT, DM, IT>(acc, s, cols, bb, g, i);
+        };
+        int t = first;
+        for (; t + 1 < nt; t += 2) {
+            step(t, 0);
+            step(t + 1, 1);
         }
-        if (!M || dm <= DM - 32) fetch(first);
-        Op x2[SLOPES && KIND == kDk ? DK / E::KS : 1];
-        if constexpr (SLOPES && KIND == kDk)
-            load_rows<DT, DK>(x2, static_cast<const T*>(p.k) + (sg.begin + row0) * p.k_stride + (int64_t)hk * dk, p.k_stride,
-                              sg.n - row0, dk, g, i);
-        for (int t = first; t < nt; ++t) {
-            T *ba = lds + (t & 1) * TA::kSize, *bb = lds + 2 * TA::kSize + (t & 1) * TB::kSize;
-            ta.put(ba, tid);
-            tb.put(bb, tid);
-            fetch(t + 1);
-            __syncthreads();
-            const int kblk = t * TT / 16;
-            if (REV ? kblk + 1 < rblk : kblk > rblk) continue;
-            f32x4 s[2];
-            scores<DT, DX>(s, ba, x, g, i);
-            if constexpr (SLOPES && KIND == kDk) {
-                f32x4 r[2];
-                scores<DT, DK>(r, bb, x2, g, i);
-#pragma unroll
-                for (int jt = 0; jt < 2; ++jt) {
-                    const int D = kblk + jt - rblk;
-                    const f32x4 u = weight.slope(D, g, i);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        da += D > 0 || (D == 0 && weight.seen(g, i, e)) ? u[e] * s[jt][e] * r[jt][e] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int jt = 0; jt < 2; ++jt) s[jt] = weight(s[jt], REV ? kblk + jt - rblk : rblk - kblk - jt, g, i);
-            gather<DT, DM>(acc, s, bb, g, i);
-        }
-        if constexpr (SLOPES) sum_to(da, sums, part + j * a.parts, tid);
+        if (t < nt) step(t, 0);
+        if constexpr (SLOPES) sum_to<NT>(da, sums, part + j * a.parts, tid);
     }
     T* out = static_cast<T*>(KIND == kOut ? p.out : KIND == kDq ? a.dq : KIND == kDk ? a.dk : a.dv) + (int64_t)hh * dm;
     const int64_t os = (int64_t)heads * dm;
-    const int g = (thread & 63) >> 4, row = row0 + (thread & 15);
-    if (row < sg.n)
+    const int g = (thread & 63) >> 4;
 #pragma unroll
-        for (int mt = 0; mt < DM / 16; ++mt)
-            if (16 * mt < dm) st4<DT>(out + (sg.begin + row) * os + 16 * mt + 4 * g, acc[mt]);
+    for (int it = 0; it < IT; ++it) {
+        const int row = row0 + 16 * it + (thread & 15);
+        if (row < sg.n)
+#pragma unroll
+            for (int mt = 0; mt < DM / 16; ++mt)
+                if (16 * mt < dm) st4<DT>(out + (sg.begin + row) * os + 16 * mt + 4 * g, acc[it][mt]);
+    }
 }
 
 template <int DT, int DK, int DV>
-__global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 4 : 2) void k_lin_out(Lin a) {
+__global__ __launch_bounds__(kThreads, 2) void k_lin_out(Lin a) {
     __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV>()];
-    __shared__ __attribute__((aligned(16))) float tab[kSegMax];
+    __shared__ __attribute__((aligned(16))) float tab[kSeg];
     rows_of<DT, DK, DV, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, nullptr);
 }
-// dq and dk of the key heads (blocks_k of each) and dv of the value heads
+// dk and dq of the key heads (blocks_k of each) and dv of the value heads
 template <int DT, int DK, int DV, bool SLOPES>
-__global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 3 : 2) void k_lin_grads(Lin a, unsigned blocks_k) {
+__global__ __launch_bounds__(kThreads, 2) void k_lin_grads(Lin a, unsigned blocks_k) {
     __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV>()];
-    __shared__ __attribute__((aligned(16))) float tab[kSegMax];
+    __shared__ __attribute__((aligned(16))) float tab[kSeg];
     __shared__ float sums[kThreads / 64];
     const unsigned b = blockIdx.x;
     if (b < blocks_k) rows_of<DT, DK, DV, kDk, SLOPES>(a, b, blocks_k, lds, tab, sums);
@@ -987,19 +1118,15 @@ __global__ __launch_bounds__(kThreads, DT == GDN_BF16 ? 3 : 2) void k_lin_grads(
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-int seg_for(const Linear&) { return 256; }
-
 // What a batch has at most: ranks of sequences of `least` tokens or more (0:
 // empty ones too), and their segments.
 struct LinSizes {
-    int seg;
     int64_t nrank, nseg;
 };
 LinSizes sizes(const Linear& p, int64_t least) {
     LinSizes z;
-    z.seg = seg_for(p);
     z.nrank = least > 0 ? std::min(p.S, p.N / least) : p.S;
-    z.nseg = p.N / z.seg + std::min(p.S, p.N / std::max<int64_t>(least, 1));
+    z.nseg = p.N / kSeg + std::min(p.S, p.N / std::max<int64_t>(least, 1));
     return z;
 }
 int64_t scan_blocks(const Linear& p) { return (p.dk * p.dv + 4 * kThreads - 1) / (4 * kThreads); }
@@ -1031,7 +1158,7 @@ LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
     L.s_seg = take(head * z.nseg);
     if (back) {
         L.g_seg = take(head * z.nseg);
-        L.part_scan = 3 * z.nseg * (z.seg / kBlockRows);  // of dq, dk and dv
+        L.part_scan = 3 * z.nseg * (kSeg / kBlockRows);  // behind those of dq, dk and dv
         L.parts = L.part_scan + z.nrank * scan_blocks(p);
         L.part = take(sizeof(float) * (size_t)(L.parts * p.Hv));
     } else {
@@ -1050,7 +1177,6 @@ Lin arguments(const Linear& p) {
     return a;
 }
 void place(Lin& a, const LinSizes& z, const LinLayout& L, char* base) {
-    a.seg = z.seg;
     a.nrank = z.nrank;
     a.nseg = z.nseg;
     a.count = reinterpret_cast<int32_t*>(base + L.count);
@@ -1090,7 +1216,7 @@ hipError_t forward_chunks(const Lin& a, hipStream_t st) {
     if (e != hipSuccess) return e;
     e = launch("k_lin_scan", k_lin_scan, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))), kThreads, a, st);
     if (e != hipSuccess) return e;
-    return launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (a.seg / kBlockRows) * p.Hv)), kThreads, a, st);
+    return launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (kSeg / kBlockRows) * p.Hv)), kThreads, a, st);
 }
 template <int DT, int DK, int DV>
 hipError_t backward_chunks(const Lin& a, hipStream_t st) {
@@ -1099,7 +1225,7 @@ hipError_t backward_chunks(const Lin& a, hipStream_t st) {
     if (e != hipSuccess) return e;
     e = launch("k_lin_bscan", k_lin_bscan, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))), kThreads, a, st);
     if (e != hipSuccess) return e;
-    const int64_t units = a.nseg * (a.seg / kBlockRows);
+    const int64_t units = a.nseg * (kSeg / kBlockRows);
     const unsigned blocks_k = (unsigned)(units * p.Hk);
     const dim3 grid(2 * blocks_k + (unsigned)(units * p.Hv));
     e = a.dalpha ? launch("k_lin_grads", k_lin_grads<DT, DK, DV, true>, grid, kThreads, a, st, blocks_k)
