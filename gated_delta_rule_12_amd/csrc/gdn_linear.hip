@@ -59,7 +59,7 @@ struct Lin {
     float* g_seg;        // [nseg, Hv]: what a segment adds to its start state's gradient, then all of that
     float* part;         // [Hv, parts]: addends of dalpha
     int64_t parts;
-    int64_t part_scan;   // where those of the scan begin, behind those of the rows
+    int64_t part_dv, part_pairs, part_scan;  // behind dq's: where dv's, the pairs' and the scan's begin
 };
 
 // Segment si, in scalar registers
@@ -241,12 +241,7 @@ template <int DT, int LPR>
 __global__ __launch_bounds__(kThreads) void k_lin_rec(Lin a) {
     rec_sequence<DT, LPR>(a, blockIdx.x, gridDim.x);
 }
-// the segments' places, and the short sequences beside that
-template <int DT, int LPR>
-__global__ __launch_bounds__(kThreads) void k_lin_first(Lin a) {
-    if (blockIdx.x == 0) plan_segments(a, threadIdx.x);
-    else rec_sequence<DT, LPR>(a, blockIdx.x - 1, gridDim.x - 1);
-}
+__global__ __launch_bounds__(kThreads) void k_lin_plan(Lin a) { plan_segments(a, threadIdx.x); }
 // the segments' places, and the gradients' rows outside every sequence
 __global__ __launch_bounds__(kThreads) void k_lin_bfirst(Lin a) {
     if (blockIdx.x == 0) {
@@ -343,7 +338,12 @@ __device__ __forceinline__ uint32_t rows_bytes(int rows, uint32_t stride, int d,
 // compiler keeps few operands in few registers and waits for each), and tiles on
 // their way are asked for in the order in which they are waited for, on every path
 // into a loop (else its waits are for all of them).
-__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+template <int DT = GDN_BF16>
+__device__ __forceinline__ void in_order() {
+    // (fp32 operands take twice the registers and their products eight times as
+    // long: there the compiler may order them)
+    if (DT == GDN_BF16) __builtin_amdgcn_sched_barrier(0);
+}
 
 // A tile of TT tokens' rows of D features (d of them real) on its way to LDS;
 // rows behind the last and features past d are zero there.
@@ -396,8 +396,11 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t
     l = two(r0 - top(r0), r1 - top(r1));
 }
 
+// (The first `recs` workgroups work the short sequences off beside that: a chain of
+// tokens' latencies, which costs 17 us in a launch of its own in a mixed batch of
+// 16384 tokens.)
 template <int DT, int DV, int DK>
-__global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a) {
+__global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a, unsigned recs) {
     using E = El<DT>;
     using T = typename E::T;
     using Op = typename E::Op;
@@ -408,8 +411,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a) {
     __shared__ __attribute__((aligned(16))) T ly[2][TY::kSize];
     __shared__ __attribute__((aligned(16))) float wt[kSeg];
     const Linear& p = a.p;
+    if (blockIdx.x < recs) {
+        rec_sequence<DT, DK == 128 ? 32 : 16>(a, blockIdx.x, recs);
+        return;
+    }
     const bool rev = blockIdx.y == 1;
-    const unsigned id = on_one_xcd(blockIdx.x, gridDim.x, a.group);
+    const unsigned id = on_one_xcd(blockIdx.x - recs, gridDim.x - recs, a.group);
     const int64_t si = id / a.Hv;
     const int h = id - si * a.Hv;
     const Seg sg = segment(a, si);
@@ -506,26 +513,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a) {
 // the states between the segments
 // ---------------------------------------------------------------------------
 // S <- a^n S + (what the segment adds), element by element, each segment's place
-// holding the state behind it afterwards.  kAhead segments' pieces are in flight.
-constexpr int kAhead = 8;
-template <bool BACK, class F>
+// holding the state behind it afterwards.  AHEAD segments' pieces are in flight
+// (scan_ahead).
+template <int AHEAD, bool BACK, class F>
 __device__ __forceinline__ void scan_places(const float* from, int64_t stride, int count, F step) {
-    f32x4 x[kAhead], y[kAhead];
-    auto fetch = [&](f32x4 (&r)[kAhead], int g0) {
+    f32x4 x[AHEAD], y[AHEAD];
+    auto fetch = [&](f32x4 (&r)[AHEAD], int g0) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < AHEAD; ++u) {
             const int g = BACK ? count - 1 - (g0 + u) : g0 + u;
             if (g0 + u < count) r[u] = ld_g<f32x4>(from + g * stride);
         }
     };
     fetch(x, 0);
-    for (int g0 = 0; g0 < count; g0 += kAhead) {
-        if (g0 + kAhead < count) fetch(y, g0 + kAhead);
+    for (int g0 = 0; g0 < count; g0 += AHEAD) {
+        if (g0 + AHEAD < count) fetch(y, g0 + AHEAD);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+        for (int u = 0; u < AHEAD; ++u)
             if (g0 + u < count) step(BACK ? count - 1 - (g0 + u) : g0 + u, x[u]);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) x[u] = y[u];
+        for (int u = 0; u < AHEAD; ++u) x[u] = y[u];
     }
 }
 
@@ -550,6 +557,7 @@ __device__ __forceinline__ ScanAt scan_at(const Lin& a, int tid) {
     return x;
 }
 
+template <int AHEAD>
 __global__ __launch_bounds__(kThreads) void k_lin_scan(Lin a) {
     const ScanAt x = scan_at(a, threadIdx.x);
     if (!x.on) return;
@@ -564,7 +572,7 @@ __global__ __launch_bounds__(kThreads) void k_lin_scan(Lin a) {
     const float whole = decay(kSeg), rest = decay((int)(x.sp.n - (int64_t)(x.G - 1) * kSeg));
     const int64_t stride = (int64_t)a.Hv * a.state;
     float* at = a.s_seg + ((int64_t)x.f * a.Hv + x.h) * a.state + x.e;
-    scan_places<false>(at, stride, dst ? x.G : x.G - 1, [&](int g, const f32x4& add) {
+    scan_places<AHEAD, false>(at, stride, dst ? x.G : x.G - 1, [&](int g, const f32x4& add) {
         S = (g == x.G - 1 ? rest : whole) * S + add;
         if (g == x.G - 1) st_g(dst + x.e, S);
         else st_g(at + g * stride, S);
@@ -587,6 +595,7 @@ __device__ __forceinline__ void sum_to(float x, float* sums, float* to, int tid)
 
 // Backward: the states behind the segments, then the gradients behind them, and
 // n a^{n-1} <G, S> of each for dalpha.
+template <int AHEAD>
 __global__ __launch_bounds__(kThreads) void k_lin_bscan(Lin a) {
     __shared__ float sums[kThreads / 64];
     const int tid = threadIdx.x;
@@ -601,7 +610,7 @@ __global__ __launch_bounds__(kThreads) void k_lin_bscan(Lin a) {
         const f32x4 S0 = src ? ld_g<f32x4>(src + x.e) : zero4();
         f32x4 S = S0;
         float* at = a.s_seg + off;
-        scan_places<false>(at, stride, x.G - 1, [&](int g, const f32x4& add) {
+        scan_places<AHEAD, false>(at, stride, x.G - 1, [&](int g, const f32x4& add) {
             S = whole * S + add;
             st_g(at + g * stride, S);
         });
@@ -611,7 +620,7 @@ __global__ __launch_bounds__(kThreads) void k_lin_bscan(Lin a) {
         // (without a gradient of the start state the first segment adds nothing)
         const int lowest = a.ds0 ? 0 : 1;
         const float dw = (float)kSeg * decay(kSeg - 1), dr = (float)n_last * decay(n_last - 1);
-        scan_places<true>(ga + lowest * stride, stride, x.G - lowest, [&](int g, const f32x4& add) {
+        scan_places<AHEAD, true>(ga + lowest * stride, stride, x.G - lowest, [&](int g, const f32x4& add) {
             g += lowest;
             if (a.dalpha) {
                 const f32x4 from = g > 0 ? ld_g<f32x4>(at + (g - 1) * stride) : S0;
@@ -726,9 +735,9 @@ __device__ __forceinline__ void load_rows(typename El<DT>::Op (&x)[IT][D / El<DT
 
 // Four features from c on of a wave's row i, from a buffer of its rows
 template <int DT>
-__device__ __forceinline__ f32x4 row_piece(Bytes rows, uint32_t stride, int i, int c) {
+__device__ __forceinline__ R4<DT> row_piece(Bytes rows, uint32_t stride, int i, int c) {
     if constexpr (DT == GDN_BF16)
-        return cvt<DT>(__builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rows, (int)((uint32_t)i * stride + 2u * c), 0, 0)));
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rows, (int)((uint32_t)i * stride + 2u * c), 0, 0));
     else
         return __builtin_bit_cast(f32x4, ld_bytes(rows, (uint32_t)i * stride + 4u * c));
 }
@@ -789,7 +798,7 @@ __device__ __forceinline__ void gather(f32x4 (&acc)[IT][D / 16], const f32x4 (&p
     for (int n = 0; n < C::N; ++n) {
         C &now = n & 1 ? next : first, &then = n & 1 ? first : next;
         if (n + 1 < C::N) then.load(tile, n + 1, g, i);
-        in_order();
+        in_order<DT>();
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -797,7 +806,7 @@ __device__ __forceinline__ void gather(f32x4 (&acc)[IT][D / 16], const f32x4 (&p
 #pragma unroll
                 for (int it = 0; it < IT; ++it)
                     acc[it][n * C::B + m] = mm(now.op[m][e % C::PER], t[it][e], acc[it][n * C::B + m]);
-        in_order();
+        in_order<DT>();
     }
 }
 
@@ -913,20 +922,24 @@ __device__ __forceinline__ int anew(int x) {
 
 // A workgroup has 128 rows of a head, 32 a wave; dq's and dk's are a key head's,
 // its value heads one after the other in one sum.
-constexpr int kIT = 2, kBlockRows = 64 * kIT;
+// (waves of a workgroup and rows of a wave)
+template <int DT>
+struct Shape {
+    static constexpr int NT = 256, IT = DT == GDN_BF16 ? 2 : 1, ROWS = NT / 4 * IT, WAVES = 2;
+};
 template <int DT, int DK, int DV>
 constexpr int rows_lds() {
     constexpr int tiles = 2 * (Tile<DT, DK, kThreads>::kSize + Tile<DT, DV, kThreads>::kSize);
     return std::max(tiles, 2 * std::max(Slab<DT, DV, DK, false, kThreads>::kSize, Slab<DT, DV, DK, true, kThreads>::kSize));
 }
-template <int DT, int DK, int DV, int KIND, bool SLOPES>
+template <int DT, int DK, int DV, int NT, int IT, int KIND, bool SLOPES>
 __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned blocks, typename El<DT>::T* lds, float* tab,
                                         float* sums) {
     using E = El<DT>;
     using T = typename E::T;
     using Op = typename E::Op;
     constexpr bool REV = Made<KIND>::REV, TR = Made<KIND>::TR, SUM = Made<KIND>::SUM;
-    constexpr int DX = TR ? DV : DK, DM = TR ? DK : DV, TT = E::TT, NT = kThreads, IT = kIT;
+    constexpr int DX = TR ? DV : DK, DM = TR ? DK : DV, TT = E::TT, kBlockRows = NT / 4 * IT;
     using TA = Tile<DT, DX, NT>;
     using TB = Tile<DT, DM, NT>;
     using SL = Slab<DT, DV, DK, TR, NT>;
@@ -939,7 +952,7 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
     const int64_t si = id / heads;
     const int thread = threadIdx.x, w = __builtin_amdgcn_readfirstlane(thread >> 6);
     const Seg sg = segment(a, si);
-    float* part = SLOPES ? a.part + (int64_t)hh * nh * a.parts + ((KIND - 1) * a.nseg + si) * nrb + rb : nullptr;
+    float* part = SLOPES ? a.part + (int64_t)hh * nh * a.parts + (KIND == kDv ? a.part_dv : 0) + si * nrb + rb : nullptr;
     if (rb * kBlockRows >= sg.n) {
         for (int j = thread; SLOPES && j < nh; j += NT) part[j * a.parts] = 0.f;
         return;
@@ -1004,35 +1017,37 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
                 T* slab = lds + (s & 1) * SL::kSize;
                 sl.put(slab, tid);
                 if (s + 1 < DM / 32) sl.fetch(M, 32 * (s + 1), dv, dk, tid);
+                R4<DT> wr[SLOPES ? 2 : 1][SLOPES ? IT : 1];
+                if constexpr (SLOPES)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int it = 0; it < IT; ++it) wr[m][it] = row_piece<DT>(wb, ws, 16 * it + i, 32 * s + 16 * m + 4 * g);
+                in_order();
                 __syncthreads();
                 SO so;
                 so.load(slab, 0, g, i);
-                in_order();
+                in_order<DT>();
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     f32x4 t[IT];
 #pragma unroll
                     for (int it = 0; it < IT; ++it) t[it] = so.times(x[it]);
                     if (m == 0) so.load(slab, 1, g, i);
-                    in_order();
+                    in_order<DT>();
 #pragma unroll
                     for (int it = 0; it < IT; ++it) {
                         acc[it][2 * s + m] += f[it] * t[it];
                         if constexpr (SLOPES && (KIND == kDq || KIND == kDv))
-                            if (32 * s + 16 * m < dm)
-                                da += df[it] * dot4e(t[it], row_piece<DT>(wb, ws, 16 * it + i, 32 * s + 16 * m + 4 * g));
+                            if (32 * s + 16 * m < dm) da += df[it] * dot4e(t[it], cvt<DT>(wr[m][it]));
                     }
                 }
-                in_order();
+                in_order<DT>();
             }
             __syncthreads();
         }
         fetch(first, 0);
         fetch(first + 1, 1);
-        Op x2[SLOPES && KIND == kDk ? IT : 1][DK / E::KS];
-        if constexpr (SLOPES && KIND == kDk)
-            load_rows<DT, DK, IT>(x2, static_cast<const T*>(p.k) + (sg.begin + row0) * p.k_stride + (int64_t)hk * dk, p.k_stride,
-                                  sg.n - row0, dk, g, i);
         auto step = [&](int t, int b) {
             T *ba = lds + b * TA::kSize, *bb = lds + 2 * TA::kSize + b * TB::kSize;
             ta[b].put(ba, tid);
@@ -1044,31 +1059,13 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
             auto between = [&](int it, int jt) { return REV ? kblk + jt - rblk - it : rblk + it - kblk - jt; };
             ScoreOps<DT, DX> ops;
             ops.load(ba, g, i);
-            in_order();
+            in_order<DT>();
             f32x4 s[IT][2];
 #pragma unroll
             for (int it = 0; it < IT; ++it) ops.times(s[it], x[it]);
-            if constexpr (SLOPES && KIND == kDk) {
-                ScoreOps<DT, DK> qops;
-                qops.load(bb, g, i);
-                in_order();
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    f32x4 r[2];
-                    qops.times(r, x2[it]);
-#pragma unroll
-                    for (int jt = 0; jt < 2; ++jt) {
-                        const int D = between(it, jt);
-                        const f32x4 u = weight.slope(D, g, i);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            da += D > 0 || (D == 0 && weight.seen(g, i, e)) ? u[e] * s[it][jt][e] * r[jt][e] : 0.f;
-                    }
-                }
-            }
             ColumnOps<DT, DM> cols;
             cols.load(bb, 0, g, i);
-            in_order();
+            in_order<DT>();
 #pragma unroll
             for (int it = 0; it < IT; ++it)
 #pragma unroll
@@ -1098,21 +1095,117 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
 }
 
 template <int DT, int DK, int DV>
-__global__ __launch_bounds__(kThreads, 2) void k_lin_out(Lin a) {
+__global__ __launch_bounds__(Shape<DT>::NT, Shape<DT>::WAVES) void k_lin_out(Lin a) {
     __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV>()];
     __shared__ __attribute__((aligned(16))) float tab[kSeg];
-    rows_of<DT, DK, DV, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, nullptr);
+    rows_of<DT, DK, DV, Shape<DT>::NT, Shape<DT>::IT, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, nullptr);
 }
-// dk and dq of the key heads (blocks_k of each) and dv of the value heads
+// dalpha's pairs of tokens: sum over i > j of (i - j) a^(i-j-1) (q_i.k_j)
+// (do_i.v_j), rows j of a value head, both kinds of scores at once.
+template <int DT, int DK, int DV, int NT, int IT>
+__device__ __forceinline__ void slopes_of(const Lin& a, unsigned block, unsigned blocks, typename El<DT>::T* lds, float* tab,
+                                          float* sums) {
+    using E = El<DT>;
+    using T = typename E::T;
+    using Op = typename E::Op;
+    constexpr int TT = E::TT, kBlockRows = NT / 4 * IT;
+    using TQ = Tile<DT, DK, NT>;
+    using TO = Tile<DT, DV, NT>;
+    const Linear& p = a.p;
+    constexpr unsigned nrb = kSeg / kBlockRows;
+    const unsigned b = on_one_xcd(block, blocks, nrb * a.group), id = b / nrb;
+    const int rb = b - id * nrb, h = id % a.Hv, hk = h / a.group;
+    const int64_t si = id / a.Hv;
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = (tid & 63) >> 4, i = tid & 15;
+    const Seg sg = segment(a, si);
+    float* part = a.part + (int64_t)h * a.parts + a.part_pairs + si * nrb + rb;
+    if (rb * kBlockRows >= sg.n) {
+        if (tid == 0) *part = 0.f;
+        return;
+    }
+    const int dk = (int)p.dk, dv = (int)p.dv;
+    const int64_t os = (int64_t)a.Hv * dv;
+    const int row0 = rb * kBlockRows + 16 * IT * w, rblk = row0 / 16;
+    const int first = rb * kBlockRows / TT, nt = (sg.n + TT - 1) / TT;
+    const T* qp = static_cast<const T*>(p.q) + sg.begin * p.q_stride + (int64_t)hk * dk;
+    const T* op = static_cast<const T*>(a.dout) + sg.begin * os + (int64_t)h * dv;
+    Op xk[IT][DK / E::KS], xv[IT][DV / E::KS];
+    load_rows<DT, DK, IT>(xk, static_cast<const T*>(p.k) + (sg.begin + row0) * p.k_stride + (int64_t)hk * dk, p.k_stride,
+                          sg.n - row0, dk, g, i);
+    load_rows<DT, DV, IT>(xv, static_cast<const T*>(p.v) + (sg.begin + row0) * p.v_stride + (int64_t)h * dv, p.v_stride,
+                          sg.n - row0, dv, g, i);
+    const typename TQ::At aq(p.q_stride, dk, tid);
+    const typename TO::At ao(os, dv, tid);
+    TQ tq[2];
+    TO to[2];
+    auto fetch = [&](int t, int b) {
+        in_order();
+        tq[b].fetch(qp + t * TT * p.q_stride, aq, sg.n - t * TT);
+        to[b].fetch(op + t * TT * os, ao, sg.n - t * TT);
+        in_order();
+    };
+    fetch(first, 0);
+    fetch(first + 1, 1);
+    const Decay decay(a, h);
+    Weights<true>::fill(decay, tab, kSeg, tid, NT);
+    Weights<true> weight;
+    weight.set(decay, p.scale, tab, g, i);
+    float da = 0.f;
+    auto step = [&](int t, int b) {
+        T *bq = lds + b * TQ::kSize, *bo = lds + 2 * TQ::kSize + b * TO::kSize;
+        tq[b].put(bq, tid);
+        to[b].put(bo, tid);
+        fetch(t + 2, b);
+        __syncthreads();
+        const int kblk = t * TT / 16;
+        if (kblk + 1 < rblk) return;
+        ScoreOps<DT, DK> qops;
+        ScoreOps<DT, DV> oops;
+        qops.load(bq, g, i);
+        oops.load(bo, g, i);
+        in_order<DT>();
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            f32x4 s[2], r[2];
+            qops.times(s, xk[it]);
+            oops.times(r, xv[it]);
+#pragma unroll
+            for (int jt = 0; jt < 2; ++jt) {
+                const int D = kblk + jt - rblk - it;
+                const f32x4 u = weight.slope(D, g, i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    da += D > 0 || (D == 0 && weight.seen(g, i, e)) ? u[e] * s[jt][e] * r[jt][e] : 0.f;
+            }
+        }
+    };
+    int t = first;
+    for (; t + 1 < nt; t += 2) {
+        step(t, 0);
+        step(t + 1, 1);
+    }
+    if (t < nt) step(t, 0);
+    sum_to<NT>(da, sums, part, tid);
+}
+
+// dk and dq of the key heads (blocks_k of each), dv of the value heads and, with
+// SLOPES, dalpha's addends (blocks_v of each)
 template <int DT, int DK, int DV, bool SLOPES>
-__global__ __launch_bounds__(kThreads, 2) void k_lin_grads(Lin a, unsigned blocks_k) {
+__global__ __launch_bounds__(Shape<DT>::NT, Shape<DT>::WAVES) void k_lin_grads(Lin a, unsigned blocks_k, unsigned blocks_v) {
+    constexpr int NT = Shape<DT>::NT, IT = Shape<DT>::IT;
     __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV>()];
     __shared__ __attribute__((aligned(16))) float tab[kSeg];
-    __shared__ float sums[kThreads / 64];
-    const unsigned b = blockIdx.x;
-    if (b < blocks_k) rows_of<DT, DK, DV, kDk, SLOPES>(a, b, blocks_k, lds, tab, sums);
-    else if (b < 2 * blocks_k) rows_of<DT, DK, DV, kDq, SLOPES>(a, b - blocks_k, blocks_k, lds, tab, sums);
-    else rows_of<DT, DK, DV, kDv, SLOPES>(a, b - 2 * blocks_k, gridDim.x - 2 * blocks_k, lds, tab, sums);
+    __shared__ float sums[NT / 64];
+    unsigned b = blockIdx.x;
+    if (b < blocks_k) {
+        rows_of<DT, DK, DV, NT, IT, kDk, false>(a, b, blocks_k, lds, tab, sums);
+    } else if ((b -= blocks_k) < blocks_k) {
+        rows_of<DT, DK, DV, NT, IT, kDq, SLOPES>(a, b, blocks_k, lds, tab, sums);
+    } else if ((b -= blocks_k) < blocks_v) {
+        rows_of<DT, DK, DV, NT, IT, kDv, SLOPES>(a, b, blocks_v, lds, tab, sums);
+    } else if constexpr (SLOPES) {
+        slopes_of<DT, DK, DV, NT, IT>(a, b - blocks_v, blocks_v, lds, tab, sums);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1130,6 +1223,10 @@ LinSizes sizes(const Linear& p, int64_t least) {
     return z;
 }
 int64_t scan_blocks(const Linear& p) { return (p.dk * p.dv + 4 * kThreads - 1) / (4 * kThreads); }
+// Whether a sequence may have many segments: few workgroups then carry long chains
+// (one of 65531 tokens, 4 heads: 34 us with 8 pieces in flight, 31.6 with 16; 40
+// sequences of 16384 tokens, 16 heads: 36 and 50).
+bool long_chains(const Linear& p) { return std::min(p.N, p.max_len) > 32 * kSeg; }
 bool overlap(const Linear& p) {
     const char *a = reinterpret_cast<const char*>(p.s_in), *b = reinterpret_cast<const char*>(p.s_out);
     const int64_t one = p.Hv * p.dv * p.dk * 4;
@@ -1139,7 +1236,7 @@ bool in_chunks(const Linear& p) { return std::min(p.N, p.max_len) >= kLinMin; }
 
 struct LinLayout {
     size_t count, seqs, first, segs, log2a, s_seg, s_copy, g_seg, part, total;
-    int64_t parts, part_scan;
+    int64_t parts, part_dv, part_pairs, part_scan;
 };
 LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
     LinLayout L{};
@@ -1158,7 +1255,9 @@ LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
     L.s_seg = take(head * z.nseg);
     if (back) {
         L.g_seg = take(head * z.nseg);
-        L.part_scan = 3 * z.nseg * (kSeg / kBlockRows);  // behind those of dq, dk and dv
+        L.part_dv = z.nseg * (kSeg / (p.dtype == GDN_BF16 ? Shape<GDN_BF16>::ROWS : Shape<GDN_F32>::ROWS));
+        L.part_pairs = 2 * L.part_dv;
+        L.part_scan = 3 * L.part_dv;
         L.parts = L.part_scan + z.nrank * scan_blocks(p);
         L.part = take(sizeof(float) * (size_t)(L.parts * p.Hv));
     } else {
@@ -1200,36 +1299,38 @@ unsigned rec_blocks(const Linear& p, int lpr) {
     return (unsigned)(p.S * p.Hv * ((p.dv + rows - 1) / rows));
 }
 template <int DT, int LPR>
-hipError_t start(const Lin& a, bool chunks, hipStream_t st) {
-    const unsigned recs = rec_blocks(a.p, LPR);
-    return chunks ? launch("k_lin_first", k_lin_first<DT, LPR>, dim3(recs + 1), kThreads, a, st)
-                  : launch("k_lin_rec", k_lin_rec<DT, LPR>, dim3(recs), kThreads, a, st);
+hipError_t tokens(const Lin& a, hipStream_t st) {
+    return launch("k_lin_rec", k_lin_rec<DT, LPR>, dim3(rec_blocks(a.p, LPR)), kThreads, a, st);
 }
 template <int DT>
-hipError_t start_by_row(const Lin& a, bool chunks, hipStream_t st) {
-    return a.p.dk > 64 ? start<DT, 32>(a, chunks, st) : a.p.dk > 32 ? start<DT, 16>(a, chunks, st) : start<DT, 8>(a, chunks, st);
+hipError_t tokens_by_size(const Lin& a, hipStream_t st) {
+    return a.p.dk > 64 ? tokens<DT, 32>(a, st) : a.p.dk > 32 ? tokens<DT, 16>(a, st) : tokens<DT, 8>(a, st);
 }
 template <int DT, int DK, int DV>
 hipError_t forward_chunks(const Lin& a, hipStream_t st) {
     const Linear& p = a.p;
-    hipError_t e = launch("k_lin_add", k_lin_add<DT, DV, DK>, dim3((unsigned)(a.nseg * p.Hv), 1), kThreads, a, st);
+    hipError_t e = launch("k_lin_plan", k_lin_plan, dim3(1), kThreads, a, st);
     if (e != hipSuccess) return e;
-    e = launch("k_lin_scan", k_lin_scan, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))), kThreads, a, st);
+    const unsigned recs = rec_blocks(p, DK == 128 ? 32 : 16);
+    e = launch("k_lin_add", k_lin_add<DT, DV, DK>, dim3(recs + (unsigned)(a.nseg * p.Hv)), kThreads, a, st, recs);
     if (e != hipSuccess) return e;
-    return launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (kSeg / kBlockRows) * p.Hv)), kThreads, a, st);
+    e = launch("k_lin_scan", long_chains(p) ? k_lin_scan<16> : k_lin_scan<8>, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))),
+               kThreads, a, st);
+    if (e != hipSuccess) return e;
+    return launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (kSeg / Shape<DT>::ROWS) * p.Hv)), Shape<DT>::NT, a, st);
 }
 template <int DT, int DK, int DV>
 hipError_t backward_chunks(const Lin& a, hipStream_t st) {
     const Linear& p = a.p;
-    hipError_t e = launch("k_lin_badd", k_lin_add<DT, DV, DK>, dim3((unsigned)(a.nseg * p.Hv), 2), kThreads, a, st);
+    hipError_t e = launch("k_lin_badd", k_lin_add<DT, DV, DK>, dim3((unsigned)(a.nseg * p.Hv), 2), kThreads, a, st, 0u);
     if (e != hipSuccess) return e;
-    e = launch("k_lin_bscan", k_lin_bscan, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))), kThreads, a, st);
+    e = launch("k_lin_bscan", long_chains(p) ? k_lin_bscan<16> : k_lin_bscan<8>,
+               dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))), kThreads, a, st);
     if (e != hipSuccess) return e;
-    const int64_t units = a.nseg * (kSeg / kBlockRows);
-    const unsigned blocks_k = (unsigned)(units * p.Hk);
-    const dim3 grid(2 * blocks_k + (unsigned)(units * p.Hv));
-    e = a.dalpha ? launch("k_lin_grads", k_lin_grads<DT, DK, DV, true>, grid, kThreads, a, st, blocks_k)
-                 : launch("k_lin_grads", k_lin_grads<DT, DK, DV, false>, grid, kThreads, a, st, blocks_k);
+    const int64_t units = a.nseg * (kSeg / Shape<DT>::ROWS);
+    const unsigned bk = (unsigned)(units * p.Hk), bv = (unsigned)(units * p.Hv);
+    e = a.dalpha ? launch("k_lin_grads", k_lin_grads<DT, DK, DV, true>, dim3(2 * bk + 2 * bv), Shape<DT>::NT, a, st, bk, bv)
+                 : launch("k_lin_grads", k_lin_grads<DT, DK, DV, false>, dim3(2 * bk + bv), Shape<DT>::NT, a, st, bk, bv);
     if (e != hipSuccess || !a.dalpha) return e;
     return launch("k_lin_dalpha", k_lin_dalpha, dim3((unsigned)p.Hv), 1024, a, st);
 }
@@ -1266,8 +1367,7 @@ hipError_t linear_forward(const Linear& p, void* ws, hipStream_t st) {
         if (overlap(p)) a.s_copy = reinterpret_cast<float*>(static_cast<char*>(ws) + L.s_copy);
     }
     const bool bf16 = p.dtype == GDN_BF16;
-    const hipError_t e = bf16 ? start_by_row<GDN_BF16>(a, chunks, st) : start_by_row<GDN_F32>(a, chunks, st);
-    if (e != hipSuccess || !chunks) return e;
+    if (!chunks) return bf16 ? tokens_by_size<GDN_BF16>(a, st) : tokens_by_size<GDN_F32>(a, st);
     return bf16 ? forward_by_size<GDN_BF16>(a, st) : forward_by_size<GDN_F32>(a, st);
 }
 
@@ -1284,6 +1384,8 @@ hipError_t linear_backward(const LinearBwd& b, void* ws, hipStream_t st) {
     a.g_seg = reinterpret_cast<float*>(base + L.g_seg);
     a.part = reinterpret_cast<float*>(base + L.part);
     a.parts = L.parts;
+    a.part_dv = L.part_dv;
+    a.part_pairs = L.part_pairs;
     a.part_scan = L.part_scan;
     a.dout = b.dout;
     a.ds_out = b.ds_out;

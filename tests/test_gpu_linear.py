@@ -396,7 +396,7 @@ def test_timer_names_the_kernels():
     gdn.linear_fwd(*args, timer=tm)
     gdn.linear_backward(*args, None, c.cuda("dout"), timer=tm)
     torch.cuda.synchronize()
-    assert set(tm.read()) == {"k_lin_first", "k_lin_add", "k_lin_scan", "k_lin_out", "k_lin_bfirst", "k_lin_badd",
+    assert set(tm.read()) == {"k_lin_plan", "k_lin_add", "k_lin_scan", "k_lin_out", "k_lin_bfirst", "k_lin_badd",
                               "k_lin_bscan", "k_lin_grads", "k_lin_dalpha"}
 
 
