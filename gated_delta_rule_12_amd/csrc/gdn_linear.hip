@@ -50,7 +50,7 @@ struct Lin {
     Seg* segs;           // [nseg], without tokens behind the last
     float* log2a;        // [Hv]: of the decays
     float* s_seg;        // [nseg, Hv] states: what a segment adds, then the state behind it
-    float* s_copy;       // [nrank, Hv]: start states of a call in place, or null
+    bool late;           // end states are written behind the outputs (in place)
     // backward
     const void* dout;
     const float* ds_out;
@@ -81,6 +81,11 @@ __device__ __forceinline__ float* end_of(const Lin& a, int64_t s, int64_t h) {
     return p.s_out + (slot * a.Hv + h) * a.state;
 }
 
+// The state in front of segment si, or null (zero)
+__device__ __forceinline__ const float* state_before(const Lin& a, const Seg& sg, int64_t si, int h) {
+    return sg.ends & kFirst ? start_of(a, sg.seq, h) : a.s_seg + ((si - 1) * a.Hv + h) * (int64_t)a.state;
+}
+
 // Powers of a decay: e^(x log a), with a^0 = 1 for a zero decay too.  The
 // exponent's rounding leaves an error of |x log2 a| 2^-24 relative to the power,
 // less than 2^-24 of a weight of one wherever the power counts.
@@ -95,12 +100,13 @@ struct Decay {
 // ---------------------------------------------------------------------------
 // By one workgroup.  Counts saturate and are cut to the tables' sizes, so that no
 // content of the offsets leads out of them.
-constexpr int kPlanLds = 1024;  // ranks whose counts the search finds in LDS
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanLds = 2048;  // ranks whose counts the search finds in LDS
 __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
-    __shared__ uint32_t sums[2 * kThreads / 64];
+    __shared__ uint32_t sums[2 * kPlanThreads / 64];
     __shared__ int lfirst[kPlanLds];
-    for (int h = tid; h < a.Hv; h += kThreads) a.log2a[h] = (float)log2((double)a.p.alpha[h]);
-    const int64_t S = a.at.S, run = (S + kThreads - 1) / kThreads, r0 = min(tid * run, S), r1 = min(r0 + run, S);
+    for (int h = tid; h < a.Hv; h += kPlanThreads) a.log2a[h] = (float)log2((double)a.p.alpha[h]);
+    const int64_t S = a.at.S, run = (S + kPlanThreads - 1) / kPlanThreads, r0 = min(tid * run, S), r1 = min(r0 + run, S);
     const int w = tid >> 6, lane = tid & 63;
     auto segs_of = [&](int64_t n) { return (uint32_t)((n + kSeg - 1) / kSeg); };
     uint32_t at[2] = {0, 0};
@@ -137,7 +143,7 @@ __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
         at[1] = add_up_to_max(at[1], segs_of(n));
     }
     __shared__ int total[2];
-    if (tid == kThreads - 1) {
+    if (tid == kPlanThreads - 1) {
         put(at[0], at[1]);
         total[0] = (int)min<int64_t>(at[0], a.nrank);
         total[1] = (int)min<int64_t>(at[1], a.nseg);
@@ -147,8 +153,8 @@ __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
     __threadfence_block();
     __syncthreads();
     const int ranks = total[0];
-    for (int64_t i = total[1] + tid; i < a.nseg; i += kThreads) a.segs[i] = Seg{0, 0, 0, 0};
-    for (int i = tid; i < total[1]; i += kThreads) {
+    for (int64_t i = total[1] + tid; i < a.nseg; i += kPlanThreads) a.segs[i] = Seg{0, 0, 0, 0};
+    for (int i = tid; i < total[1]; i += kPlanThreads) {
         int lo = 0, hi = ranks;  // first[lo] <= i, first[hi] > i or none
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -241,9 +247,9 @@ template <int DT, int LPR>
 __global__ __launch_bounds__(kThreads) void k_lin_rec(Lin a) {
     rec_sequence<DT, LPR>(a, blockIdx.x, gridDim.x);
 }
-__global__ __launch_bounds__(kThreads) void k_lin_plan(Lin a) { plan_segments(a, threadIdx.x); }
+__global__ __launch_bounds__(kPlanThreads) void k_lin_plan(Lin a) { plan_segments(a, threadIdx.x); }
 // the segments' places, and the gradients' rows outside every sequence
-__global__ __launch_bounds__(kThreads) void k_lin_bfirst(Lin a) {
+__global__ __launch_bounds__(kPlanThreads) void k_lin_bfirst(Lin a) {
     if (blockIdx.x == 0) {
         plan_segments(a, threadIdx.x);
         return;
@@ -253,11 +259,11 @@ __global__ __launch_bounds__(kThreads) void k_lin_bfirst(Lin a) {
     const int64_t e = p.dtype == GDN_BF16 ? 2 : 4, bk = p.Hk * p.dk * e, bv = p.Hv * p.dv * e;
     for (int64_t i = blockIdx.x - 1; i < c0 + (p.N - c1); i += gridDim.x - 1) {
         const int64_t t = i < c0 ? i : c1 + (i - c0);
-        for (int64_t b = 16 * threadIdx.x; b < bk; b += 16 * kThreads) {
+        for (int64_t b = 16 * threadIdx.x; b < bk; b += 16 * kPlanThreads) {
             st_g(static_cast<char*>(a.dq) + t * bk + b, u32x4{0, 0, 0, 0});
             st_g(static_cast<char*>(a.dk) + t * bk + b, u32x4{0, 0, 0, 0});
         }
-        for (int64_t b = 16 * threadIdx.x; b < bv; b += 16 * kThreads)
+        for (int64_t b = 16 * threadIdx.x; b < bv; b += 16 * kPlanThreads)
             st_g(static_cast<char*>(a.dv) + t * bv + b, u32x4{0, 0, 0, 0});
     }
 }
@@ -396,33 +402,20 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t
     l = two(r0 - top(r0), r1 - top(r1));
 }
 
-// (The first `recs` workgroups work the short sequences off beside that: a chain of
-// tokens' latencies, which costs 17 us in a launch of its own in a mixed batch of
-// 16384 tokens.)
+// to(row, col, four columns' sums) takes them.
 template <int DT, int DV, int DK>
-__global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a, unsigned recs) {
+constexpr int add_lds() {
+    return 2 * (Tile<DT, DV, kThreads>::kSize + Tile<DT, DK, kThreads>::kSize);
+}
+template <int DT, int DV, int DK, class F>
+__device__ __forceinline__ void add_segment(const Lin& a, const Seg& sg, int h, bool rev, typename El<DT>::T* lds, float* wt, F to) {
     using E = El<DT>;
     using T = typename E::T;
     using Op = typename E::Op;
     constexpr int TT = E::TT, KS = E::KS, RT = DV / 64, CT = DK / 16;
     using TX = Tile<DT, DV, kThreads>;
     using TY = Tile<DT, DK, kThreads>;
-    __shared__ __attribute__((aligned(16))) T lx[2][TX::kSize];
-    __shared__ __attribute__((aligned(16))) T ly[2][TY::kSize];
-    __shared__ __attribute__((aligned(16))) float wt[kSeg];
     const Linear& p = a.p;
-    if (blockIdx.x < recs) {
-        rec_sequence<DT, DK == 128 ? 32 : 16>(a, blockIdx.x, recs);
-        return;
-    }
-    const bool rev = blockIdx.y == 1;
-    const unsigned id = on_one_xcd(blockIdx.x - recs, gridDim.x - recs, a.group);
-    const int64_t si = id / a.Hv;
-    const int h = id - si * a.Hv;
-    const Seg sg = segment(a, si);
-    if (sg.n == 0) return;
-    // (a last segment's end, where no one wants it; a first one's start gradient)
-    if (rev ? (sg.ends & kFirst) && !a.ds0 : (sg.ends & kLast) && !(p.s_out && end_of(a, sg.seq, h))) return;
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = (tid & 63) >> 4, i = tid & 15;
     const int dk = (int)p.dk, dv = (int)p.dv;
     const Decay decay(a, h);
@@ -448,9 +441,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a, unsigned recs) {
         ty[b].fetch(y + t * TT * ys, ay, sg.n - t * TT);
     };
     auto step = [&](int t, int b) {
-        const T *bx = lx[b], *by = ly[b];
-        tx[b].put(lx[b], tid);
-        ty[b].put(ly[b], tid);
+        T *bx = lds + b * TX::kSize, *by = lds + 2 * TX::kSize + b * TY::kSize;
+        tx[b].put(bx, tid);
+        ty[b].put(by, tid);
         in_order();
         fetch(t + 2, b);
         in_order();
@@ -499,14 +492,68 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a, unsigned recs) {
     }
     if (t < nt) step(t, 0);
     // the accumulator: column 4 g .. of 16 c, row i of the wave's
-    float* out = (rev ? a.g_seg : a.s_seg) + (si * a.Hv + h) * (int64_t)a.state;
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
             const int row = 16 * (RT * w + r) + i, col = 16 * c + 4 * g;
-            if (row < dv && col < dk) st_g(out + row * dk + col, acc[r][c]);
+            if (row < dv && col < dk) to(row, col, acc[r][c]);
         }
+}
+
+// The end state of the sequence whose last segment is si: f * (the state before) +
+// what the segment adds.
+template <int DT, int DV, int DK>
+__device__ __forceinline__ void end_state(const Lin& a, const Seg& sg, int64_t si, int h, typename El<DT>::T* lds, float* wt) {
+    float* dst = end_of(a, sg.seq, h);
+    if (!dst) return;
+    const float* before = state_before(a, sg, si, h);
+    const float f = Decay(a, h)(sg.n);
+    add_segment<DT, DV, DK>(a, sg, h, false, lds, wt, [&](int row, int col, const f32x4& x) {
+        const int at = row * (int)a.p.dk + col;
+        st_g(dst + at, before ? f * ld_g<f32x4>(before + at) + x : x);
+    });
+}
+
+// What every segment adds (blockIdx.y 1: to the gradients, the first one's only
+// where that is wanted).  A sequence of one segment is done with that.  The first
+// `recs` workgroups work the short sequences off beside that: chains of tokens'
+// latencies, which cost 17 us in a launch of their own in a mixed batch of 16384
+// tokens.
+template <int DT, int DV, int DK>
+__global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a, unsigned recs) {
+    __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[add_lds<DT, DV, DK>()];
+    __shared__ __attribute__((aligned(16))) float wt[kSeg];
+    if (blockIdx.x < recs) {
+        rec_sequence<DT, DK == 128 ? 32 : 16>(a, blockIdx.x, recs);
+        return;
+    }
+    const bool rev = blockIdx.y == 1;
+    const unsigned id = on_one_xcd(blockIdx.x - recs, gridDim.x - recs, a.group);
+    const int64_t si = id / a.Hv;
+    const int h = id - si * a.Hv;
+    const Seg sg = segment(a, si);
+    if (sg.n == 0) return;
+    if (rev ? (sg.ends & kFirst) && !a.ds0 : (sg.ends & kLast) && (a.late || !a.p.s_out)) return;
+    if (!rev && sg.ends == (kFirst | kLast | sg.rank() << 2)) {
+        end_state<DT, DV, DK>(a, sg, si, h, lds, wt);
+        return;
+    }
+    float* out = (rev ? a.g_seg : a.s_seg) + (si * a.Hv + h) * (int64_t)a.state;
+    add_segment<DT, DV, DK>(a, sg, h, rev, lds, wt, [&](int row, int col, const f32x4& x) { st_g(out + row * (int)a.p.dk + col, x); });
+}
+
+// In place, a sequence's end state goes where the outputs of its first rows are
+// read from: it waits for them (k_lin_out is in front of this).
+template <int DT, int DV, int DK>
+__global__ __launch_bounds__(kThreads, 2) void k_lin_end(Lin a) {
+    __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[add_lds<DT, DV, DK>()];
+    __shared__ __attribute__((aligned(16))) float wt[kSeg];
+    const unsigned id = on_one_xcd(blockIdx.x, gridDim.x, a.group);
+    const int r = id / a.Hv, h = id - r * a.Hv;
+    if (r >= a.count[0]) return;
+    const int64_t si = (int64_t)min(a.first[r + 1], a.count[1]) - 1;
+    if (si >= a.first[r]) end_state<DT, DV, DK>(a, segment(a, si), si, h, lds, wt);
 }
 
 // ---------------------------------------------------------------------------
@@ -560,14 +607,10 @@ __device__ __forceinline__ ScanAt scan_at(const Lin& a, int tid) {
 template <int AHEAD>
 __global__ __launch_bounds__(kThreads) void k_lin_scan(Lin a) {
     const ScanAt x = scan_at(a, threadIdx.x);
-    if (!x.on) return;
+    if (!x.on || x.G < 2) return;
     const float* src = start_of(a, x.s, x.h);
-    float* dst = end_of(a, x.s, x.h);
-    f32x4 S = zero4();
-    if (src) {
-        S = ld_g<f32x4>(src + x.e);
-        if (a.s_copy) st_g(a.s_copy + ((int64_t)x.r * a.Hv + x.h) * a.state + x.e, S);
-    }
+    float* dst = a.late ? nullptr : end_of(a, x.s, x.h);
+    f32x4 S = src ? ld_g<f32x4>(src + x.e) : zero4();
     const Decay decay(a, x.h);
     const float whole = decay(kSeg), rest = decay((int)(x.sp.n - (int64_t)(x.G - 1) * kSeg));
     const int64_t stride = (int64_t)a.Hv * a.state;
@@ -878,12 +921,6 @@ __device__ __forceinline__ void st4(typename El<DT>::T* to, const f32x4& x) {
     else st_g(to, x);
 }
 
-// The state in front of segment si, or null (zero)
-__device__ __forceinline__ const float* state_before(const Lin& a, const Seg& sg, int64_t si, int h) {
-    if (!(sg.ends & kFirst)) return a.s_seg + ((si - 1) * a.Hv + h) * (int64_t)a.state;
-    const float* src = start_of(a, sg.seq, h);
-    return src && a.s_copy ? a.s_copy + ((int64_t)sg.rank() * a.Hv + h) * a.state : src;
-}
 // The gradient of the state behind segment si, or null (zero)
 __device__ __forceinline__ const float* gradient_behind(const Lin& a, const Seg& sg, int64_t si, int h) {
     if (!(sg.ends & kLast)) return a.g_seg + ((si + 1) * a.Hv + h) * (int64_t)a.state;
@@ -1235,7 +1272,7 @@ bool overlap(const Linear& p) {
 bool in_chunks(const Linear& p) { return std::min(p.N, p.max_len) >= kLinMin; }
 
 struct LinLayout {
-    size_t count, seqs, first, segs, log2a, s_seg, s_copy, g_seg, part, total;
+    size_t count, seqs, first, segs, log2a, s_seg, g_seg, part, total;
     int64_t parts, part_dv, part_pairs, part_scan;
 };
 LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
@@ -1260,8 +1297,6 @@ LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
         L.part_scan = 3 * L.part_dv;
         L.parts = L.part_scan + z.nrank * scan_blocks(p);
         L.part = take(sizeof(float) * (size_t)(L.parts * p.Hv));
-    } else {
-        L.s_copy = take(head * z.nrank);
     }
     L.total = off;
     return L;
@@ -1309,7 +1344,7 @@ hipError_t tokens_by_size(const Lin& a, hipStream_t st) {
 template <int DT, int DK, int DV>
 hipError_t forward_chunks(const Lin& a, hipStream_t st) {
     const Linear& p = a.p;
-    hipError_t e = launch("k_lin_plan", k_lin_plan, dim3(1), kThreads, a, st);
+    hipError_t e = launch("k_lin_plan", k_lin_plan, dim3(1), kPlanThreads, a, st);
     if (e != hipSuccess) return e;
     const unsigned recs = rec_blocks(p, DK == 128 ? 32 : 16);
     e = launch("k_lin_add", k_lin_add<DT, DV, DK>, dim3(recs + (unsigned)(a.nseg * p.Hv)), kThreads, a, st, recs);
@@ -1317,7 +1352,9 @@ hipError_t forward_chunks(const Lin& a, hipStream_t st) {
     e = launch("k_lin_scan", long_chains(p) ? k_lin_scan<16> : k_lin_scan<8>, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))),
                kThreads, a, st);
     if (e != hipSuccess) return e;
-    return launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (kSeg / Shape<DT>::ROWS) * p.Hv)), Shape<DT>::NT, a, st);
+    e = launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (kSeg / Shape<DT>::ROWS) * p.Hv)), Shape<DT>::NT, a, st);
+    if (e != hipSuccess || !a.late) return e;
+    return launch("k_lin_end", k_lin_end<DT, DV, DK>, dim3((unsigned)(a.nrank * p.Hv)), kThreads, a, st);
 }
 template <int DT, int DK, int DV>
 hipError_t backward_chunks(const Lin& a, hipStream_t st) {
@@ -1364,7 +1401,7 @@ hipError_t linear_forward(const Linear& p, void* ws, hipStream_t st) {
         const LinSizes z = sizes(p, kLinMin);
         const LinLayout L = layout(p, z, false);
         place(a, z, L, static_cast<char*>(ws));
-        if (overlap(p)) a.s_copy = reinterpret_cast<float*>(static_cast<char*>(ws) + L.s_copy);
+        a.late = overlap(p);
     }
     const bool bf16 = p.dtype == GDN_BF16;
     if (!chunks) return bf16 ? tokens_by_size<GDN_BF16>(a, st) : tokens_by_size<GDN_F32>(a, st);
@@ -1394,7 +1431,7 @@ hipError_t linear_backward(const LinearBwd& b, void* ws, hipStream_t st) {
     a.dv = b.dv;
     a.dalpha = b.dalpha;
     a.ds0 = b.ds0;
-    const hipError_t e = launch("k_lin_bfirst", k_lin_bfirst, dim3(1 + (unsigned)std::min<int64_t>(std::max<int64_t>(p.N, 1), 1024)), kThreads, a, st);
+    const hipError_t e = launch("k_lin_bfirst", k_lin_bfirst, dim3(1 + (unsigned)std::min<int64_t>(std::max<int64_t>(p.N, 1), 256)), kPlanThreads, a, st);
     if (e != hipSuccess) return e;
     return p.dtype == GDN_BF16 ? backward_by_size<GDN_BF16>(a, st) : backward_by_size<GDN_F32>(a, st);
 }

@@ -419,12 +419,12 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  *               cu_seqlens, state_in, slots_in, state_out, slots_out, out,
  *               max_len: as for gdn_packed_fwd (the same rules for slots; in
  *               place or not)
- *   alpha       [Hv] fp32, >= 0 (not checked; 0: a token reads its own value
- *               alone)
+ *   alpha       [Hv] fp32, 0 to 1 (not checked: powers of more may overflow);
+ *               0: a token reads its own value alone
  *   workspace   gdn_linear_workspace_bytes(...) bytes: none for single tokens
- *               (max_len or N below 32), else 8 Hv dk dv for each sequence of 32
- *               tokens or more and 4 Hv dk dv for every 256 tokens; two calls
- *               that may overlap need two
+ *               (max_len or N below 32), else a state (4 Hv dk dv) for each
+ *               sequence of 32 tokens or more and for every 256 tokens; two
+ *               calls that may overlap need two
  * Sequences of 32 tokens or more run in segments of 256 on the matrix cores, for
  * every dk, dv and dtype: fp32 as it is; bf16 q, k and v exactly, what is
  * multiplied with a power of alpha as two (scores, start states: 2^-17) or three
@@ -465,7 +465,10 @@ size_t gdn_linear_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, 
  *                   for each sequence and for every 256 tokens, and grad_alpha's
  *                   addends
  * S Hv = 0: nothing is enqueued, the gradients are left as they were.  Sums are
- * taken in a fixed order (repeated calls give identical results).  Alignment: as
+ * taken in a fixed order (repeated calls give identical results).  NaN and
+ * infinities as in gdn_linear_fwd: one in k may reach, within its feature of
+ * grad_q, the 31 tokens in front of its own, one in q or grad_out, within its
+ * feature of grad_k or grad_v, the 31 behind it.  Alignment: as
  * gdn_packed_backward.
  */
 int gdn_linear_backward(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in,

@@ -122,16 +122,17 @@ def test_in_place(lengths, dk, dv, dtype):
 
 
 def test_overlapping_pools():
-    """Two pools that are overlapping views: every start state is read first."""
+    """In place through two views of one pool whose slots are named differently."""
     import torch
-    c = Linear((300, 70), 1, 2, 64, 64, seed=6).make()
-    both = torch.full((5, 2, 64, 64), 7.0, device="cuda")
-    both[1:3] = c.cuda("pool")
-    c.a["slots_in"] = c.a["slots_out"] = np.array([0, 1], np.int32)
-    out, end = gdn.linear_fwd(*(c.cuda(n) for n in ("q", "k", "v", "alpha", "cu")), both[1:3], None, both[0:2], None)
+    c = Linear((300, 70, 5), 1, 2, 64, 64, seed=6).make()
+    both = torch.full((6, 2, 64, 64), 7.0, device="cuda")
+    both[1:4] = c.cuda("pool")
+    c.a["slots_in"] = c.a["slots_out"] = np.array([0, 1, 2], np.int32)
+    here = torch.tensor([1, 2, 3], dtype=torch.int32, device="cuda")
+    out, end = gdn.linear_fwd(*(c.cuda(n) for n in ("q", "k", "v", "alpha", "cu")), both[1:], None, both[:5], here)
     torch.cuda.synchronize()
-    check(c, out.float().cpu().numpy(), end.cpu().numpy())
-    assert (both[3:] == 7.0).all()
+    assert (both[0] == 7.0).all() and (both[4:] == 7.0).all()
+    check(c, out.float().cpu().numpy(), both[1:4].cpu().numpy())
 
 
 @pytest.mark.parametrize("max_len", [0, 1, 31, 32, 200, 100000])
@@ -215,7 +216,7 @@ def test_exact_workspace(lengths, dk, dv, hv, dtype):
 
 def test_many_ranks():
     """More sequences in segments than the plan's search holds in LDS."""
-    lengths = (33, 1) * 1100 + (300,)
+    lengths = (33, 1) * 2100 + (300,)
     c = Linear(lengths, 1, 1, 16, 16, seed=12).make()
     check(c, *run(c))
 
