@@ -24,8 +24,13 @@
 namespace gdn {
 namespace {
 
-// Sequences of fewer tokens go token by token (forward).
-constexpr int kLinMin = 32;
+// Sequences of fewer tokens go token by token (forward): a chain of latencies that
+// many sequences share a chip for, against one pass of a segment.  Heads of 128, 16
+// heads, tokens against segments: bf16 16 sequences of 32 tokens 29.6 and 30 us,
+// 256 of 32 352 and 322, 256 of 48 516 and 344; fp32 (an eighth of the matrix
+// rate) 16 of 48 37 and 60, 256 of 48 532 and 852, 16 of 200 142 and 110, 256 of
+// 200 1894 and 1621: about even from 64 tokens (few) to 130 (many) on.
+constexpr int lin_min(int dtype) { return dtype == GDN_BF16 ? 32 : 64; }
 // Tokens of a segment.
 constexpr int kSeg = 256;
 
@@ -855,13 +860,13 @@ __device__ __forceinline__ void gather(f32x4 (&acc)[IT][D / 16], const f32x4 (&p
 
 // 32 rows (TR: columns) of a state [dv][dk] on their way to LDS, where they lie
 // split into terms, and their products with a wave's rows.
-template <int DT, int DV, int DK, bool TR, int NT>
+template <int DT, int DV, int DK, bool TR, int NT, int TERMS>
 struct Slab {
     using T = typename El<DT>::T;
     using Op = typename El<DT>::Op;
     static constexpr int DX = TR ? DV : DK;  // what is contracted
     static constexpr int W = TR ? 32 : DK, LD = TR ? 36 : DK + El<DT>::PAD, ROWS = TR ? DV : 32, LO = ROWS * LD;
-    static constexpr int kSize = El<DT>::TERMS * LO, NP = 8 * DX / NT;
+    static constexpr int kSize = TERMS * LO, NP = 8 * DX / NT;
     f32x4 r[NP];
     __device__ __forceinline__ void fetch(const float* M, int m0, int dv, int dk, int tid) {
         const Bytes b = bytes_from(M, (uint32_t)(dv * dk * 4));
@@ -876,7 +881,17 @@ struct Slab {
         for (int k = 0; k < NP; ++k) {
             const int p = tid + NT * k;
             T* to = slab + p / (W / 4) * LD + 4 * (p % (W / 4));
-            if constexpr (DT == GDN_BF16) {
+            if constexpr (TERMS == 3) {
+                u32x2 t[3];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t h, m, l;
+                    split3(r[k][2 * e], r[k][2 * e + 1], h, m, l);
+                    t[0][e] = h, t[1][e] = m, t[2][e] = l;
+                }
+#pragma unroll
+                for (int e = 0; e < 3; ++e) *reinterpret_cast<u32x2*>(to + e * LO) = t[e];
+            } else if constexpr (TERMS == 2) {
                 u16x4 hi, lo;
                 split4(r[k], hi, lo);
                 *reinterpret_cast<u16x4*>(to) = hi;
@@ -889,10 +904,10 @@ struct Slab {
 };
 // Rows (TR: columns) 16 m .. of a state that lies in LDS in terms LO elements
 // apart, LD elements a row, as operands; K of them contract all features.
-template <int DT, int D, bool TR, int LD, int LO>
+template <int DT, int D, bool TR, int LD, int LO, int TERMS>
 struct StateOps {
     using Op = typename El<DT>::Op;
-    static constexpr int KS = El<DT>::KS, K = D / KS, TERMS = El<DT>::TERMS;
+    static constexpr int KS = El<DT>::KS, K = D / KS;
     Op op[K][TERMS];
     __device__ __forceinline__ void load(const typename El<DT>::T* at, int m, int g, int i) {
 #pragma unroll
@@ -910,7 +925,9 @@ struct StateOps {
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < TERMS; ++e) t[e] = mm(op[k][e], x[k], t[e]);
-        return TERMS == 2 ? t[0] + t[TERMS - 1] : t[0];
+#pragma unroll
+        for (int e = TERMS - 1; e > 0; --e) t[e - 1] += t[e];
+        return t[0];
     }
 };
 
@@ -964,10 +981,17 @@ template <int DT>
 struct Shape {
     static constexpr int NT = 256, IT = DT == GDN_BF16 ? 2 : 1, ROWS = NT / 4 * IT, WAVES = 2;
 };
-template <int DT, int DK, int DV>
+// Terms of the states.  Rows of bf16 results are far from seeing an error of
+// 2^-17; dalpha, an fp32 sum over all tokens, is not (two terms left it 1e-6 to 9e-6
+// off, three leave 1e-7 to 4e-7), and three hold an fp32 state exactly.
+template <int DT, bool SLOPES>
+constexpr int state_terms() {
+    return DT == GDN_BF16 && SLOPES ? 3 : El<DT>::TERMS;
+}
+template <int DT, int DK, int DV, bool SLOPES>
 constexpr int rows_lds() {
-    constexpr int tiles = 2 * (Tile<DT, DK, kThreads>::kSize + Tile<DT, DV, kThreads>::kSize);
-    return std::max(tiles, 2 * std::max(Slab<DT, DV, DK, false, kThreads>::kSize, Slab<DT, DV, DK, true, kThreads>::kSize));
+    constexpr int tiles = 2 * (Tile<DT, DK, kThreads>::kSize + Tile<DT, DV, kThreads>::kSize), TERMS = state_terms<DT, SLOPES>();
+    return std::max(tiles, 2 * std::max(Slab<DT, DV, DK, false, kThreads, TERMS>::kSize, Slab<DT, DV, DK, true, kThreads, TERMS>::kSize));
 }
 template <int DT, int DK, int DV, int NT, int IT, int KIND, bool SLOPES>
 __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned blocks, typename El<DT>::T* lds, float* tab,
@@ -979,8 +1003,9 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
     constexpr int DX = TR ? DV : DK, DM = TR ? DK : DV, TT = E::TT, kBlockRows = NT / 4 * IT;
     using TA = Tile<DT, DX, NT>;
     using TB = Tile<DT, DM, NT>;
-    using SL = Slab<DT, DV, DK, TR, NT>;
-    using SO = StateOps<DT, DX, TR, SL::LD, SL::LO>;
+    constexpr int TERMS = state_terms<DT, SLOPES>();
+    using SL = Slab<DT, DV, DK, TR, NT, TERMS>;
+    using SO = StateOps<DT, DX, TR, SL::LD, SL::LO, TERMS>;
     const Linear& p = a.p;
     const int heads = SUM ? (int)p.Hk : a.Hv, nh = SUM ? a.group : 1;
     constexpr unsigned nrb = kSeg / kBlockRows;
@@ -1133,7 +1158,7 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
 
 template <int DT, int DK, int DV>
 __global__ __launch_bounds__(Shape<DT>::NT, Shape<DT>::WAVES) void k_lin_out(Lin a) {
-    __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV>()];
+    __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV, false>()];
     __shared__ __attribute__((aligned(16))) float tab[kSeg];
     rows_of<DT, DK, DV, Shape<DT>::NT, Shape<DT>::IT, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, nullptr);
 }
@@ -1230,7 +1255,7 @@ __device__ __forceinline__ void slopes_of(const Lin& a, unsigned block, unsigned
 template <int DT, int DK, int DV, bool SLOPES>
 __global__ __launch_bounds__(Shape<DT>::NT, Shape<DT>::WAVES) void k_lin_grads(Lin a, unsigned blocks_k, unsigned blocks_v) {
     constexpr int NT = Shape<DT>::NT, IT = Shape<DT>::IT;
-    __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV>()];
+    __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV, SLOPES>()];
     __shared__ __attribute__((aligned(16))) float tab[kSeg];
     __shared__ float sums[NT / 64];
     unsigned b = blockIdx.x;
@@ -1269,7 +1294,7 @@ bool overlap(const Linear& p) {
     const int64_t one = p.Hv * p.dv * p.dk * 4;
     return a && b && a < b + p.n_out * one && b < a + p.n_in * one;
 }
-bool in_chunks(const Linear& p) { return std::min(p.N, p.max_len) >= kLinMin; }
+bool in_chunks(const Linear& p) { return std::min(p.N, p.max_len) >= lin_min(p.dtype); }
 
 struct LinLayout {
     size_t count, seqs, first, segs, log2a, s_seg, g_seg, part, total;
@@ -1390,15 +1415,15 @@ hipError_t backward_by_size(const Lin& a, hipStream_t st) {
 bool linear_in_chunks(const Linear& p) { return in_chunks(p); }
 
 size_t linear_workspace(const Linear& p) {
-    return in_chunks(p) ? layout(p, sizes(p, kLinMin), false).total : 0;
+    return in_chunks(p) ? layout(p, sizes(p, lin_min(p.dtype)), false).total : 0;
 }
 
 hipError_t linear_forward(const Linear& p, void* ws, hipStream_t st) {
     Lin a = arguments(p);
     const bool chunks = in_chunks(p);
-    a.chunk_min = chunks ? kLinMin : INT64_MAX;
+    a.chunk_min = chunks ? lin_min(p.dtype) : INT64_MAX;
     if (chunks) {
-        const LinSizes z = sizes(p, kLinMin);
+        const LinSizes z = sizes(p, lin_min(p.dtype));
         const LinLayout L = layout(p, z, false);
         place(a, z, L, static_cast<char*>(ws));
         a.late = overlap(p);

@@ -421,12 +421,12 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  *               place or not)
  *   alpha       [Hv] fp32, 0 to 1 (not checked: powers of more may overflow);
  *               0: a token reads its own value alone
- *   workspace   gdn_linear_workspace_bytes(...) bytes: none for single tokens
- *               (max_len or N below 32), else a state (4 Hv dk dv) for each
- *               sequence of 32 tokens or more and for every 256 tokens; two
- *               calls that may overlap need two
- * Sequences of 32 tokens or more run in segments of 256 on the matrix cores, for
- * every dk, dv and dtype: fp32 as it is; bf16 q, k and v exactly, what is
+ *   workspace   gdn_linear_workspace_bytes(...) bytes: none for short sequences
+ *               alone (max_len or N below 32, in fp32 below 64), else a state
+ *               (4 Hv dk dv) for each longer sequence and for every 256 tokens;
+ *               two calls that may overlap need two
+ * Sequences of 32 tokens or more (fp32: 64) run in segments of 256 on the matrix
+ * cores, for every dk and dv: fp32 as it is; bf16 q, k and v exactly, what is
  * multiplied with a power of alpha as two (scores, start states: 2^-17) or three
  * (what enters the states: exact) bf16 terms.  The others run token by token.
  * All sums and states are fp32; out is rounded once.
@@ -457,7 +457,8 @@ size_t gdn_linear_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, 
  *   grad_q, grad_k  [N, Hk, dk], dtype, summed over the value heads of a key
  *                   head in fp32 and rounded once;  grad_v [N, Hv, dv], dtype;
  *                   rows outside every sequence are set to zero
- *   grad_alpha      [Hv] fp32, summed over all sequences; NULL: not wanted
+ *   grad_alpha      [Hv] fp32, summed over all sequences (states enter it as
+ *                   three bf16 terms, exactly); NULL: not wanted
  *   grad_state0     [S, Hv, dv, dk] fp32: dL/d of each sequence's start state
  *                   (sequences that share a slot each have their own; it must
  *                   not be grad_state_out's memory); NULL: not wanted
