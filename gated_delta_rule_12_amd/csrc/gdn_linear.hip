@@ -65,6 +65,8 @@ struct Lin {
     float* part;         // [Hv, parts]: addends of dalpha
     int64_t parts;
     int64_t part_dv, part_pairs, part_scan;  // behind dq's: where dv's, the pairs' and the scan's begin
+    int splits;          // parts that a key head's value heads are summed in for dq and dk
+    float* split;        // [2 (dk, dq), splits, N, Hk, dk]: these sums, where there is more than one
 };
 
 // Segment si, in scalar registers
@@ -687,10 +689,30 @@ __global__ __launch_bounds__(kThreads) void k_lin_bscan(Lin a) {
     }
 }
 
-// dalpha of a head: its addends in a fixed order
-__global__ __launch_bounds__(1024) void k_lin_dalpha(Lin a) {
+// dalpha of a head (the first `heads` workgroups) and, where they were made in
+// parts, dk and dq: their addends in a fixed order
+__device__ __forceinline__ void join_parts(const Lin& a, int64_t at) {
+    const Linear& p = a.p;
+    const int64_t row = p.Hk * p.dk, all = p.N * row;
+    const int which = 4 * at >= all;
+    const int64_t e = 4 * at - which * all, t = e / row;
+    // (rows outside every sequence are zero already)
+    if (e >= all || t < cu_at(a.at, 0) || t >= cu_at(a.at, p.S)) return;
+    const float* from = a.split + which * a.splits * all + e;
+    f32x4 x = ld_g<f32x4>(from);
+#pragma unroll 4
+    for (int z = 1; z < a.splits; ++z) x += ld_g<f32x4>(from + z * all);
+    void* to = which ? a.dq : a.dk;
+    if (p.dtype == GDN_BF16) st_g(static_cast<uint16_t*>(to) + e, u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])});
+    else st_g(static_cast<float*>(to) + e, x);
+}
+__global__ __launch_bounds__(1024) void k_lin_join(Lin a, unsigned heads) {
     __shared__ double sums[1024];
     const int tid = threadIdx.x;
+    if (blockIdx.x >= heads) {
+        join_parts(a, (int64_t)(blockIdx.x - heads) * 1024 + tid);
+        return;
+    }
     const float* part = a.part + (int64_t)blockIdx.x * a.parts;
     double s = 0.;
     for (int64_t i = tid; i < a.parts; i += 1024) s += (double)part[i];
@@ -1007,16 +1029,17 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
     using SL = Slab<DT, DV, DK, TR, NT, TERMS>;
     using SO = StateOps<DT, DX, TR, SL::LD, SL::LO, TERMS>;
     const Linear& p = a.p;
-    const int heads = SUM ? (int)p.Hk : a.Hv, nh = SUM ? a.group : 1;
+    const int heads = SUM ? (int)p.Hk : a.Hv, nh = SUM ? a.group : 1, splits = SUM ? a.splits : 1;
     constexpr unsigned nrb = kSeg / kBlockRows;
-    const unsigned b = on_one_xcd(block, blocks, SUM ? nrb : nrb * a.group), id = b / nrb;
-    const int rb = b - id * nrb, hh = id % heads;
+    const unsigned b = on_one_xcd(block, blocks, nrb * (SUM ? splits : a.group)), id0 = b / nrb, id = id0 / splits;
+    const int rb = b - id0 * nrb, hh = id % heads, z = id0 - id * splits;
+    const int from = z * nh / splits, to = (z + 1) * nh / splits;  // of the value heads
     const int64_t si = id / heads;
     const int thread = threadIdx.x, w = __builtin_amdgcn_readfirstlane(thread >> 6);
     const Seg sg = segment(a, si);
     float* part = SLOPES ? a.part + (int64_t)hh * nh * a.parts + (KIND == kDv ? a.part_dv : 0) + si * nrb + rb : nullptr;
     if (rb * kBlockRows >= sg.n) {
-        for (int j = thread; SLOPES && j < nh; j += NT) part[j * a.parts] = 0.f;
+        for (int j = from + thread; SLOPES && j < to; j += NT) part[j * a.parts] = 0.f;
         return;
     }
     const int dk = (int)p.dk, dv = (int)p.dv, dx = TR ? dv : dk, dm = TR ? dk : dv;
@@ -1032,7 +1055,7 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
     for (int it = 0; it < IT; ++it)
 #pragma unroll
         for (int mt = 0; mt < DM / 16; ++mt) acc[it][mt] = zero4();
-    for (int j = 0; j < nh; ++j) {
+    for (int j = from; j < to; ++j) {
         const int tid = SUM ? anew(thread) : thread, g = (tid & 63) >> 4, i = tid & 15;
         const int h = hh * nh + j, hk = SUM ? hh : hh / a.group;
         const T* xp = static_cast<const T*>(X.at) + (sg.begin + row0) * X.stride + (int64_t)(X.key ? hk : h) * dx;
@@ -1044,7 +1067,7 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
         Op x[IT][DX / E::KS];
         load_rows<DT, DX, IT>(x, xp, X.stride, sg.n - row0, dx, g, i);
         const Decay decay(a, h);
-        if (j > 0) __syncthreads();
+        if (j > from) __syncthreads();
         Weights<REV>::fill(decay, tab, kSeg, tid, NT);
         Weights<REV> weight;
         weight.set(decay, p.scale, tab, g, i);
@@ -1146,6 +1169,18 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
     T* out = static_cast<T*>(KIND == kOut ? p.out : KIND == kDq ? a.dq : KIND == kDk ? a.dk : a.dv) + (int64_t)hh * dm;
     const int64_t os = (int64_t)heads * dm;
     const int g = (thread & 63) >> 4;
+    if (SUM && splits > 1) {
+        float* sum = a.split + ((int64_t)(KIND == kDq ? splits : 0) + z) * p.N * os + (int64_t)hh * dm;
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int row = row0 + 16 * it + (thread & 15);
+            if (row < sg.n)
+#pragma unroll
+                for (int mt = 0; mt < DM / 16; ++mt)
+                    if (16 * mt < dm) st_g(sum + (sg.begin + row) * os + 16 * mt + 4 * g, acc[it][mt]);
+        }
+        return;
+    }
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
         const int row = row0 + 16 * it + (thread & 15);
@@ -1297,9 +1332,17 @@ bool overlap(const Linear& p) {
 bool in_chunks(const Linear& p) { return std::min(p.N, p.max_len) >= lin_min(p.dtype); }
 
 struct LinLayout {
-    size_t count, seqs, first, segs, log2a, s_seg, g_seg, part, total;
+    size_t count, seqs, first, segs, log2a, s_seg, g_seg, part, split, total;
     int64_t parts, part_dv, part_pairs, part_scan;
+    int splits;
 };
+// dq's and dk's workgroups work a key head's value heads off one by one, the
+// others have one each: it is split where all of them together give the chip's 512
+// places less than that (the parts then hold 128 dk 2^10 bytes at most).
+int head_splits(const Linear& p, int64_t rows) {
+    const int64_t group = p.Hv / p.Hk, at_once = std::min(group, (4 * rows * p.Hv + 511) / 512);
+    return at_once > 0 ? (int)((group + at_once - 1) / at_once) : 1;
+}
 LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
     LinLayout L{};
     size_t off = 0;
@@ -1318,10 +1361,12 @@ LinLayout layout(const Linear& p, const LinSizes& z, bool back) {
     if (back) {
         L.g_seg = take(head * z.nseg);
         L.part_dv = z.nseg * (kSeg / (p.dtype == GDN_BF16 ? Shape<GDN_BF16>::ROWS : Shape<GDN_F32>::ROWS));
+        L.splits = head_splits(p, L.part_dv);
         L.part_pairs = 2 * L.part_dv;
         L.part_scan = 3 * L.part_dv;
         L.parts = L.part_scan + z.nrank * scan_blocks(p);
         L.part = take(sizeof(float) * (size_t)(L.parts * p.Hv));
+        if (L.splits > 1) L.split = take(sizeof(float) * 2 * (size_t)(L.splits * p.N * p.Hk * p.dk));
     }
     L.total = off;
     return L;
@@ -1389,12 +1434,13 @@ hipError_t backward_chunks(const Lin& a, hipStream_t st) {
     e = launch("k_lin_bscan", long_chains(p) ? k_lin_bscan<16> : k_lin_bscan<8>,
                dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))), kThreads, a, st);
     if (e != hipSuccess) return e;
-    const int64_t units = a.nseg * (kSeg / Shape<DT>::ROWS);
-    const unsigned bk = (unsigned)(units * p.Hk), bv = (unsigned)(units * p.Hv);
+    const int64_t rows = a.nseg * (kSeg / Shape<DT>::ROWS);
+    const unsigned bk = (unsigned)(rows * p.Hk * a.splits), bv = (unsigned)(rows * p.Hv);
     e = a.dalpha ? launch("k_lin_grads", k_lin_grads<DT, DK, DV, true>, dim3(2 * bk + 2 * bv), Shape<DT>::NT, a, st, bk, bv)
                  : launch("k_lin_grads", k_lin_grads<DT, DK, DV, false>, dim3(2 * bk + bv), Shape<DT>::NT, a, st, bk, bv);
-    if (e != hipSuccess || !a.dalpha) return e;
-    return launch("k_lin_dalpha", k_lin_dalpha, dim3((unsigned)p.Hv), 1024, a, st);
+    if (e != hipSuccess) return e;
+    const unsigned heads = a.dalpha ? (unsigned)p.Hv : 0, joins = a.splits > 1 ? (unsigned)((p.N * p.Hk * p.dk / 2 + 1023) / 1024) : 0;
+    return launch("k_lin_join", k_lin_join, dim3(heads + joins), 1024, a, st, heads);
 }
 // (tiles of 64 or 128 features, the ones behind the real ones zero)
 template <int DT>
@@ -1445,6 +1491,8 @@ hipError_t linear_backward(const LinearBwd& b, void* ws, hipStream_t st) {
     place(a, z, L, base);
     a.g_seg = reinterpret_cast<float*>(base + L.g_seg);
     a.part = reinterpret_cast<float*>(base + L.part);
+    a.splits = L.splits;
+    a.split = reinterpret_cast<float*>(base + L.split);
     a.parts = L.parts;
     a.part_dv = L.part_dv;
     a.part_pairs = L.part_pairs;

@@ -398,7 +398,7 @@ def test_timer_names_the_kernels():
     gdn.linear_backward(*args, None, c.cuda("dout"), timer=tm)
     torch.cuda.synchronize()
     assert set(tm.read()) == {"k_lin_plan", "k_lin_add", "k_lin_scan", "k_lin_out", "k_lin_bfirst", "k_lin_badd",
-                              "k_lin_bscan", "k_lin_grads", "k_lin_dalpha"}
+                              "k_lin_bscan", "k_lin_grads", "k_lin_join"}
 
 
 # ---- gradients -------------------------------------------------------------------
@@ -417,6 +417,10 @@ GRADS = [
     Linear((300, 40), 1, 4, 64, 64, alpha=(1.0, 0.0, 1e-3, 0.5)),
     Linear((300, 40), 2, 4, 64, 64, dtype="f32", alpha=(1.0, 0.0, 1e-3, 0.5)),
     Linear((3000,), 1, 1, 64, 64, alpha=(1 - 2.0**-10,)),
+    # a key head's value heads in one sum, in two uneven ones, in one each
+    Linear((3, 1, 0, 2) * 50, 1, 6, 32, 64, tail=2),
+    Linear((3, 17) * 20, 1, 5, 64, 32, dtype="f32", tail=1),
+    Linear((1, 200, 5), 2, 16, 16, 48, tail=3),
 ]
 
 
