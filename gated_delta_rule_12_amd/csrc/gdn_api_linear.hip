@@ -10,14 +10,15 @@ namespace {
 bool aligned(const void* ptr, uintptr_t a) { return (uintptr_t)ptr % a == 0; }
 int finish(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_E_HIP; }
 bool dim_ok(int64_t d) { return d >= 16 && d <= 128 && d % 16 == 0; }
-// A launch holds fewer than 2^32 threads.  The most a call asks for: 4 x 256 a
-// sequence and head token by token; 16 x 256 a sequence with segments and head,
-// 2 x 256 a head and 256 tokens beside 2 x 256 a sequence and head, and in the
-// backward 4 x 256 for these.
+// A launch holds fewer than 2^32 threads.  The most a call asks for, for each
+// sequence and head: 4 x 256 token by token, 16 x 256 between segments (forward:
+// of those alone that have some).  For each segment and head, N Hv / 256 + S Hv of
+// them at most: 2 x 256 for the outputs and four times that for the gradients, twice
+// that in fp32.
 constexpr int64_t kMaxStates = (int64_t)1 << 21, kMaxChunkStates = (int64_t)1 << 19, kMaxChunkRows = (int64_t)1 << 28;
 constexpr int64_t kMaxStride = (int64_t)1 << 23;
 
-int linear_check(const Linear& p, bool chunks) {
+int linear_check(const Linear& p, bool chunks, bool back = false) {
     if (p.dtype != GDN_F32 && p.dtype != GDN_BF16) return GDN_E_ARG;
     if (p.N < 0 || p.S < 0 || p.Hk < 0 || p.Hv < 0 || p.dk <= 0 || p.dv <= 0 || p.n_in < 0 || p.n_out < 0 || p.max_len < 0)
         return GDN_E_SHAPE;
@@ -26,7 +27,8 @@ int linear_check(const Linear& p, bool chunks) {
     if (p.N > INT32_MAX || p.S > INT32_MAX || p.Hv > 65535) return GDN_E_SHAPE;
     if (!dim_ok(p.dk) || !dim_ok(p.dv)) return GDN_E_UNSUPPORTED;
     if (p.S * p.Hv > kMaxStates) return GDN_E_SHAPE;
-    if (chunks && (p.S * p.Hv > kMaxChunkStates || p.N * p.Hv > kMaxChunkRows)) return GDN_E_SHAPE;
+    const int half = back && p.dtype == GDN_F32;
+    if (chunks && (p.S * p.Hv > kMaxChunkStates >> half || p.N * p.Hv > kMaxChunkRows >> half)) return GDN_E_SHAPE;
     return GDN_OK;
 }
 
@@ -88,7 +90,7 @@ int linear_bwd_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, 
     LinearBwd b{};
     Linear& p = b.p;
     p = linear_sizes(N, S, Hk, Hv, dk, dv, n_in, 0, N, dtype);
-    int s = linear_check(p, true);
+    int s = linear_check(p, true, true);
     if (s != GDN_OK) return s;
     if (S * Hv == 0) return GDN_OK;
     p.scale = scale;
@@ -242,7 +244,7 @@ int gdn_linear_backward_timed(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int6
 
 size_t gdn_linear_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int32_t dtype) {
     const Linear p = linear_sizes(N, S, Hk, Hv, dk, dv, 0, 0, N, dtype);
-    return linear_check(p, true) != GDN_OK || S * Hv == 0 ? 0 : linear_backward_workspace(p);
+    return linear_check(p, true, true) != GDN_OK || S * Hv == 0 ? 0 : linear_backward_workspace(p);
 }
 
 int gdn_qk_norm_fwd(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot, int64_t n_pos, int32_t dtype, int32_t rotation,

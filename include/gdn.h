@@ -434,7 +434,8 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  * in segments an infinity may become a NaN, and one in v may reach, within its
  * value feature, the 31 tokens in front of its own.
  * Everything else (empty sequences, offsets out of order or range, capture,
- * alignment, statuses and limits) is as for gdn_packed_fwd.
+ * alignment, statuses and limits, those of chunk kernels where there are
+ * segments) is as for gdn_packed_fwd.
  */
 int gdn_linear_fwd(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in,
                    int64_t n_out, int64_t max_len, int32_t dtype, float scale, const void* q,
@@ -463,14 +464,16 @@ size_t gdn_linear_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, 
  *                   (sequences that share a slot each have their own; it must
  *                   not be grad_state_out's memory); NULL: not wanted
  *   workspace       gdn_linear_backward_workspace_bytes(...): twice 4 Hv dk dv
- *                   for each sequence and for every 256 tokens, and grad_alpha's
- *                   addends
+ *                   for each sequence and for every 256 tokens, grad_alpha's
+ *                   addends, and for few tokens (N Hk below 2^14) grad_q and
+ *                   grad_k in fp32 parts: 32 MiB of them at most
  * S Hv = 0: nothing is enqueued, the gradients are left as they were.  Sums are
  * taken in a fixed order (repeated calls give identical results).  NaN and
  * infinities as in gdn_linear_fwd: one in k may reach, within its feature of
  * grad_q, the 31 tokens in front of its own, one in q or grad_out, within its
  * feature of grad_k or grad_v, the 31 behind it.  Alignment: as
- * gdn_packed_backward.
+ * gdn_packed_backward; limits as of a call with segments, in fp32 half of them
+ * (S Hv over 2^18, N Hv over 2^27: GDN_E_SHAPE).
  */
 int gdn_linear_backward(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, int64_t n_in,
                         int32_t dtype, float scale, const void* q, int64_t q_stride, const void* k,

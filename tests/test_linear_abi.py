@@ -83,6 +83,13 @@ def test_linear_workspace():
     back = gdn.gdn_linear_backward_workspace_bytes
     assert back(4096, 1, 16, 16, 128, 128, 1) > 2 * 17 * state and back(4096, 0, 16, 16, 128, 128, 1) == 0
     assert back(4096, 1, 16, 16, 120, 128, 1) == 0
+    # few tokens: the sums of a key head's value heads in parts, 32 MiB of them at most
+    assert 0 < back(1500, 2, 1, 16, 128, 128, 1) - back(1500, 2, 16, 16, 128, 128, 1) <= 2**25
+    assert back(20000, 2, 1, 16, 128, 128, 1) == back(20000, 2, 16, 16, 128, 128, 1)
+    # gradients in fp32 have twice the workgroups
+    assert back(2**23, 1, 16, 16, 16, 16, 0) > 0 and back(2**23 + 1, 1, 16, 16, 16, 16, 0) == 0
+    assert back(2**14, 2**14, 16, 16, 16, 16, 0) > 0 and back(2**15, 2**14 + 1, 16, 16, 16, 16, 0) == 0
+    assert back(2**24, 1, 16, 16, 16, 16, 1) > 0
 
 
 def qk(N=10, Hq=4, Hk=2, d=64, rot=32, n_pos=100, dtype=1, rotation=0, eps=1e-6, q=F, sq=None, k=F, sk=None, wq=F, wk=F, cos=F,
