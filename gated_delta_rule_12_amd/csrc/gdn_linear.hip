@@ -14,7 +14,34 @@
 //   da   = sum_{i>j} (i-j) a^{i-j-1} (q_i.k_j) (do'_i.v_j) + sum_i (i+1) a^i do'_i.S q_i
 //        + sum_j (n-1-j) a^{n-2-j} v_j.G k_j + n a^{n-1} <G, S>
 // No term divides by a power of a, and each term of da has its power of a as a
-// factor, so any a >= 0 is right and none of the sums cancels by construction.
+// factor, so any a from 0 to 1 is right and none of the sums cancels by
+// construction.
+//
+// Why segments of 256: their states are written once and read twice (64 KiB a head
+// of 128, as much as 256 tokens of it in one array), and what is quadratic in a
+// segment grows with its length.  512 tokens: outputs 122 instead of 88 us, the scan
+// 20 instead of 33, additions 43 instead of 45 (one sequence of 65531 tokens, 4
+// heads of 128).
+//
+// Forward: k_lin_plan (where the segments lie), k_lin_add (what each adds to its
+// state; short sequences beside that), k_lin_scan (the states between), k_lin_out (the
+// outputs, a segment's 128 rows a workgroup), k_lin_end (in place: the last
+// segments' states).  Backward: k_lin_bfirst, k_lin_badd and k_lin_bscan do the same
+// for states and gradients of states at once, k_lin_grads has all rows, k_lin_join
+// sums addends.  Sequences of few tokens: k_lin_rec alone.
+//
+// Kernel times in us, and what bounds them (bf16, heads of 128; 6.05 TB/s is the rate
+// of a copy on this card):
+//   one sequence of 65531 tokens, 4 heads: plan 5, add 46 (201 MB moved: 4.4 TB/s),
+//     scan 35 (134 MB, one chain of 256 segments an element), out 92 (335 MB: 55 at
+//     least; its loads alone 66, without tiles of tokens 46, without the start states
+//     71, with scores of one term 80)
+//   40 sequences, 16384 tokens, 16 heads: 6, 67 (short sequences inside), 28, 90
+//   7 sequences, 16384 tokens, 16 heads, backward: 6, add 82 (260 MB moved), scan 58
+//     (235 MB), gradients 392 (870 MB from and to HBM take 145; matrix cores are busy
+//     21 % of the time, vector ALU 28 %, LDS 19 %; waves wait for memory and barriers
+//     37 % and for each other's issue 34 %), join 5
+//   a step of 256 single tokens, 16 heads: 92 (the states at 5.8 TB/s)
 #include "gdn_elements.h"
 #include "gdn_internal.h"
 #include "gdn_mfma_common.h"
@@ -568,7 +595,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_end(Lin a) {
 // ---------------------------------------------------------------------------
 // S <- a^n S + (what the segment adds), element by element, each segment's place
 // holding the state behind it afterwards.  AHEAD segments' pieces are in flight
-// (scan_ahead).
+// (long_chains).
 template <int AHEAD, bool BACK, class F>
 __device__ __forceinline__ void scan_places(const float* from, int64_t stride, int count, F step) {
     f32x4 x[AHEAD], y[AHEAD];
@@ -996,9 +1023,12 @@ __device__ __forceinline__ int anew(int x) {
     return x;
 }
 
-// A workgroup has 128 rows of a head, 32 a wave; dq's and dk's are a key head's,
-// its value heads one after the other in one sum.
-// (waves of a workgroup and rows of a wave)
+// A workgroup has 128 rows of a head (fp32: 64), 32 a wave (fp32: 16); dq's and
+// dk's are a key head's, its value heads one after the other in one sum.  With 16
+// rows a wave in bf16, each operand read from LDS serves half as many products
+// (eight waves: outputs of 65531 tokens 85 instead of 88 us, dq of 16384 172
+// instead of 130); with 256 rows a workgroup, tiles are read once but waves wait for
+// the last rows' (outputs 94 instead of 92, of a mixed batch 100 instead of 88).
 template <int DT>
 struct Shape {
     static constexpr int NT = 256, IT = DT == GDN_BF16 ? 2 : 1, ROWS = NT / 4 * IT, WAVES = 2;

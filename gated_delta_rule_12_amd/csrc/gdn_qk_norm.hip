@@ -15,7 +15,10 @@
 // rotated ones the two halves of the rest), so that the rotation stays within a
 // lane and the row's sums are its only exchange.  A group of lanes takes kU
 // heads of one token, which share its angles and the weight.  x, dy, y and dx are
-// touched once; statistics and sums are fp32.
+// touched once; statistics and sums are fp32.  Memory bounds it: 16384 tokens, 16
+// query and 8 key heads of 128, bf16: 201 MB in 35 us (5.7 TB/s; a copy's rate on
+// this card is 6.05); backward of 16 and 16 heads 403 MB in 80 us, and 5 for the
+// sums of dw.
 #include "gdn_elements.h"
 #include "gdn_internal.h"
 #include "gdn_mfma_common.h"
