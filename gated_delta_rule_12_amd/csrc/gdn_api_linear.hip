@@ -104,6 +104,10 @@ int linear_bwd_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, 
     if (!aligned(grad_out, 16) || !aligned(grad_state_out, 16) || !aligned(grad_q, 16) || !aligned(grad_k, 16) ||
         !aligned(grad_v, 16) || !aligned(grad_alpha, 4) || !aligned(grad_state0, 16) || !aligned(workspace, 16))
         return GDN_E_ARG;
+    // both are read and written in the sequences' order, by different workgroups
+    const int64_t states = S * Hv * dk * dv;
+    if (grad_state_out && grad_state0 && grad_state_out < grad_state0 + states && grad_state0 < grad_state_out + states)
+        return GDN_E_ARG;
     if (!workspace || workspace_bytes < linear_backward_workspace(p)) return GDN_E_WORKSPACE;
     b.dout = grad_out; b.ds_out = grad_state_out;
     b.dq = grad_q; b.dk = grad_k; b.dv = grad_v; b.dalpha = grad_alpha; b.ds0 = grad_state0;

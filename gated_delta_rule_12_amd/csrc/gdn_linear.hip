@@ -233,7 +233,7 @@ __device__ __forceinline__ void rec_sequence(const Lin& a, unsigned block, unsig
     if (sp.n >= a.chunk_min || (sp.n == 0 && src == dst)) return;
     const int c = threadIdx.x % LPR, row = rb * RB + threadIdx.x / LPR * kLinR;
     // (lanes behind the row's end and rows behind the last repeat the last piece
-    // and store nothing; what such lanes add to a sum is zero)
+    // and store nothing; what such lanes add to a sum is zero, whatever they hold)
     const bool on = 4 * c < dk, in = row < dv;
     const int col = on ? 4 * c : dk - 4, r0 = in ? row : dv - kLinR;
     f32x4 S[kLinR];
@@ -256,12 +256,12 @@ __device__ __forceinline__ void rec_sequence(const Lin& a, unsigned block, unsig
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             if (t0 + u >= sp.n) break;
-            const f32x4 kt = cvt<DT>(k[u]), qt = on ? cvt<DT>(q[u]) : zero4(), vt = cvt<DT>(v[u]);
+            const f32x4 kt = cvt<DT>(k[u]), qt = cvt<DT>(q[u]), vt = cvt<DT>(v[u]);
             f32x4 o;
 #pragma unroll
             for (int j = 0; j < kLinR; ++j) {
                 S[j] = alpha * S[j] + vt[j] * kt;
-                o[j] = p.scale * row_sum<LPR>(dot4e(S[j], qt));
+                o[j] = p.scale * row_sum<LPR>(on ? dot4e(S[j], qt) : 0.f);
             }
             fetch(u, t0 + u + kFlight);
             if (c == 0 && in) {

@@ -461,8 +461,8 @@ size_t gdn_linear_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, 
  *   grad_alpha      [Hv] fp32, summed over all sequences (states enter it as
  *                   three bf16 terms, exactly); NULL: not wanted
  *   grad_state0     [S, Hv, dv, dk] fp32: dL/d of each sequence's start state
- *                   (sequences that share a slot each have their own; it must
- *                   not be grad_state_out's memory); NULL: not wanted
+ *                   (sequences that share a slot each have their own; memory
+ *                   of grad_state_out's: GDN_E_ARG); NULL: not wanted
  *   workspace       gdn_linear_backward_workspace_bytes(...): twice 4 Hv dk dv
  *                   for each sequence and for every 256 tokens, grad_alpha's
  *                   addends, and for few tokens (N Hk below 2^14) grad_q and

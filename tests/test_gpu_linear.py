@@ -305,6 +305,20 @@ def test_non_finite_inputs_propagate(what, value, dtype):
     near(c, got[~bad], ends[~bad], esize[~bad], "f32")
 
 
+@pytest.mark.parametrize("dk", [16, 48, 80, 112])
+def test_infinite_states_of_single_tokens(dk):
+    """Token by token an infinity stays what the formula makes of it, in the last
+    features of head sizes that are no power of two as well."""
+    c = Linear((1, 3), 1, 2, dk, 16, dtype="f32", seed=47).make()
+    c.a["pool"][:, :, 3, dk - 1] = np.inf
+    out, pool = run(c, max_len=3)
+    (ref, ends), (size, _) = c.forward(), c.forward(size=True)
+    assert np.isinf(ref[:, :, 3]).all() and np.array_equal(out[:, :, 3], ref[:, :, 3])
+    rest = np.arange(16) != 3
+    near(c, out[:, :, rest], ref[:, :, rest], size[:, :, rest], "f32")
+    assert np.array_equal(np.isinf(pool[c.a["slots_out"]]), np.isinf(ends))
+
+
 @pytest.mark.parametrize("back", [False, True])
 def test_repeats_are_identical_and_graphs_replay(back):
     import torch

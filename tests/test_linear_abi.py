@@ -10,6 +10,8 @@ from gated_delta_rule_12_amd import gdn
 F = ctypes.c_void_p(0x10000)  # never dereferenced: every call below is refused first
 NUL = ctypes.c_void_p(0)
 ODD, HALF = ctypes.c_void_p(0x10002), ctypes.c_void_p(0x10008)
+FAR = ctypes.c_void_p(1 << 40)
+STATES = 4 * 2 * 4 * 64 * 64  # bytes of two sequences' states of four heads of 64
 OK, ARG, SHAPE, UNSUP, WS = gdn.GDN_OK, gdn.GDN_E_ARG, gdn.GDN_E_SHAPE, gdn.GDN_E_UNSUPPORTED, gdn.GDN_E_WORKSPACE
 
 
@@ -23,7 +25,7 @@ def fwd(N=100, S=2, Hk=2, Hv=4, dk=64, dv=64, n_in=2, n_out=2, max_len=1, dtype=
 
 
 def bwd(N=100, S=2, Hk=2, Hv=4, dk=64, dv=64, n_in=2, dtype=1, q=F, sq=None, k=F, sk=None, v=F, sv=None, alpha=F, cu=F,
-        s_in=F, slots_in=NUL, go=F, gs=F, dq=F, dkk=F, dvv=F, da=F, ds=F, ws=F, wsb=1 << 40):
+        s_in=F, slots_in=NUL, go=F, gs=F, dq=F, dkk=F, dvv=F, da=F, ds=FAR, ws=F, wsb=1 << 40):
     sq = Hk * dk if sq is None else sq
     sk = Hk * dk if sk is None else sk
     sv = Hv * dv if sv is None else sv
@@ -65,6 +67,8 @@ def test_linear_refusals(kw, want):
     (dict(go=HALF), ARG), (dict(gs=HALF), ARG), (dict(dq=HALF), ARG), (dict(dkk=ODD), ARG), (dict(dvv=HALF), ARG),
     (dict(da=ODD), ARG), (dict(ds=HALF), ARG), (dict(ws=HALF), ARG), (dict(ws=NUL), WS), (dict(wsb=16), WS),
     (dict(S=2**16, Hv=16, n_in=2**16), SHAPE), (dict(N=2**25, Hv=16), SHAPE),
+    (dict(ds=F), ARG), (dict(ds=ctypes.c_void_p(0x10000 + STATES - 16)), ARG),  # grad_state_out's memory
+    (dict(gs=FAR), ARG), (dict(ds=ctypes.c_void_p(0x10000 + STATES), wsb=16), WS),
 ])
 def test_linear_backward_refusals(kw, want):
     assert bwd(**kw) == want
