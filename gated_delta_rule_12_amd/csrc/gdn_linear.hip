@@ -32,7 +32,8 @@
 //
 // Kernel times in us, and what bounds them (bf16, heads of 128; 6.05 TB/s is the rate
 // of a copy on this card):
-//   one sequence of 65531 tokens, 4 heads: plan 5, add 46 (201 MB moved: 4.4 TB/s),
+//   one sequence of 65531 tokens, 4 heads: plan 5, add 46 (201 MB moved: 4.4 TB/s;
+//     without products 43, without stores 36, with few loads 37),
 //     scan 35 (134 MB, one chain of 256 segments an element), out 92 (335 MB: 55 at
 //     least; its loads alone 66, without tiles of tokens 46, without the start states
 //     71, with scores of one term 80)
@@ -307,7 +308,11 @@ __global__ __launch_bounds__(kPlanThreads) void k_lin_bfirst(Lin a) {
 // ---------------------------------------------------------------------------
 // Lane l = 16 g + i.  A step contracts KS indices; the lane holds KS / 4 of row
 // (or column) i: those from (KS / 4) g on.  bf16 elements are exact operands;
-// what fp32 arithmetic made is split into TERMS of them.
+// what fp32 arithmetic made is split into TERMS of them.  (Blocks of 32 x 32, whose
+// instructions do twice the work in the same time, were no faster: additions of a
+// training step of 16384 tokens 85 instead of 82 us, outputs of a mixed batch 94
+// instead of 90, gradients 450 instead of 430.  Products are not what these
+// kernels wait for.)
 template <int DT>
 struct El;
 template <>
