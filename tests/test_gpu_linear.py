@@ -101,6 +101,9 @@ CASES = [
     Linear((20, 3), 2, 4, 64, 64, alpha=(1.0, 0.0, 1e-3, 0.5)),
     # a long chain of segments
     Linear((5000, 1, 2600), 1, 1, 64, 64, alpha=(1 - 2.0**-12,)),
+    # chains beside short sequences, 8 and 16 segments in flight
+    Linear((1300, 2600) + (1,) * 15, 1, 1, 128, 128, alpha=(1 - 2.0**-9,)),
+    Linear((8500,) + (2,) * 16, 1, 1, 128, 128, alpha=(1 - 2.0**-11,)),
 ]
 
 
@@ -435,6 +438,9 @@ GRADS = [
     Linear((3, 1, 0, 2) * 50, 1, 6, 32, 64, tail=2),
     Linear((3, 17) * 20, 1, 5, 64, 32, dtype="f32", tail=1),
     Linear((1, 200, 5), 2, 16, 16, 48, tail=3),
+    # chains beside short sequences, 8 and 16 segments in flight
+    Linear((1300, 2600) + (1,) * 15, 1, 1, 128, 128, alpha=(1 - 2.0**-9,)),
+    Linear((8500,) + (2,) * 16, 1, 1, 128, 128, alpha=(1 - 2.0**-11,)),
 ]
 
 
