@@ -13,8 +13,8 @@ bool dim_ok(int64_t d) { return d >= 16 && d <= 128 && d % 16 == 0; }
 // A launch holds fewer than 2^32 threads.  The most a call asks for, for each
 // sequence and head: 4 x 256 token by token, 16 x 256 between segments (forward:
 // of those alone that have some).  For each segment and head, N Hv / 256 + S Hv of
-// them at most: 2 x 256 for the outputs and four times that for the gradients, twice
-// that in fp32.
+// them at most: 4 x 256 for the outputs, 8 x 256 for the gradients, twice that in
+// fp32.
 constexpr int64_t kMaxStates = (int64_t)1 << 21, kMaxChunkStates = (int64_t)1 << 19, kMaxChunkRows = (int64_t)1 << 28;
 constexpr int64_t kMaxStride = (int64_t)1 << 23;
 

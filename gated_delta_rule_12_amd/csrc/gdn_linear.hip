@@ -34,10 +34,10 @@
 // of a copy on this card):
 //   one sequence of 65531 tokens, 4 heads: plan 5, add 46 (201 MB moved: 4.4 TB/s;
 //     without products 43, without stores 36, with few loads 37),
-//     scan 35 (134 MB, one chain of 256 segments an element), out 92 (335 MB: 55 at
-//     least; its loads alone 66, without tiles of tokens 46, without the start states
-//     71, with scores of one term 80)
-//   40 sequences, 16384 tokens, 16 heads: 6, 67 (short sequences inside), 28, 90
+//     scan 35 (134 MB, one chain of 256 segments an element), out 84 (335 MB: 55 at
+//     least; with waves of 32 rows 88, of which loads alone 66, without tiles of tokens
+//     46, without the start states 71, with scores of one term 80)
+//   40 sequences, 16384 tokens, 16 heads: 6, 67 (short sequences inside), 28, 86
 //   7 sequences, 16384 tokens, 16 heads, backward: 6, add 82 (260 MB moved), scan 58
 //     (235 MB), gradients 392 (870 MB from and to HBM take 145; matrix cores are busy
 //     21 % of the time, vector ALU 28 %, LDS 19 %; waves wait for memory and barriers
@@ -1028,15 +1028,22 @@ __device__ __forceinline__ int anew(int x) {
     return x;
 }
 
-// A workgroup has 128 rows of a head (fp32: 64), 32 a wave (fp32: 16); dq's and
-// dk's are a key head's, its value heads one after the other in one sum.  With 16
-// rows a wave in bf16, each operand read from LDS serves half as many products
-// (eight waves: outputs of 65531 tokens 85 instead of 88 us, dq of 16384 172
-// instead of 130); with 256 rows a workgroup, tiles are read once but waves wait for
-// the last rows' (outputs 94 instead of 92, of a mixed batch 100 instead of 88).
+// A workgroup has 128 rows of a head (fp32: 64); dq's and dk's are a key head's,
+// its value heads one after the other in one sum.  Four waves of 32 rows (fp32: 16)
+// read each operand from LDS for twice as many products as eight of 16: gradients
+// of a training step 430 instead of 615 us (heads of 128: the eight spill), outputs
+// with values of 64 68 instead of 76 us.  Outputs with values of 128 are made by
+// eight, whose registers let sixteen waves share a compute unit (one sequence of
+// 65531: 84 instead of 88 us, a mixed batch 86 instead of 88).  With 256 rows a
+// workgroup, tiles are read once but waves wait for the last rows' (94 instead of
+// 92, 100 instead of 88).
 template <int DT>
 struct Shape {
     static constexpr int NT = 256, IT = DT == GDN_BF16 ? 2 : 1, ROWS = NT / 4 * IT, WAVES = 2;
+};
+template <int DT, int DV>
+struct OutShape {
+    static constexpr int IT = DV > 64 ? 1 : Shape<DT>::IT, NT = 4 * Shape<DT>::ROWS / IT, WAVES = NT / 128;
 };
 // Terms of the states.  Rows of bf16 results are far from seeing an error of
 // 2^-17; dalpha, an fp32 sum over all tokens, is not (two terms left it 1e-6 to 9e-6
@@ -1227,10 +1234,10 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
 }
 
 template <int DT, int DK, int DV>
-__global__ __launch_bounds__(Shape<DT>::NT, Shape<DT>::WAVES) void k_lin_out(Lin a) {
+__global__ __launch_bounds__((OutShape<DT, DV>::NT), (OutShape<DT, DV>::WAVES)) void k_lin_out(Lin a) {
     __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV, false>()];
     __shared__ __attribute__((aligned(16))) float tab[kSeg];
-    rows_of<DT, DK, DV, Shape<DT>::NT, Shape<DT>::IT, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, nullptr);
+    rows_of<DT, DK, DV, OutShape<DT, DV>::NT, OutShape<DT, DV>::IT, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, nullptr);
 }
 // dalpha's pairs of tokens: sum over i > j of (i - j) a^(i-j-1) (q_i.k_j)
 // (do_i.v_j), rows j of a value head, both kinds of scores at once.
@@ -1459,7 +1466,8 @@ hipError_t forward_chunks(const Lin& a, hipStream_t st) {
     e = launch("k_lin_scan", long_chains(p) ? k_lin_scan<16> : k_lin_scan<8>, dim3((unsigned)(a.nrank * p.Hv * scan_blocks(p))),
                kThreads, a, st);
     if (e != hipSuccess) return e;
-    e = launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (kSeg / Shape<DT>::ROWS) * p.Hv)), Shape<DT>::NT, a, st);
+    e = launch("k_lin_out", k_lin_out<DT, DK, DV>, dim3((unsigned)(a.nseg * (kSeg / Shape<DT>::ROWS) * p.Hv)),
+               OutShape<DT, DV>::NT, a, st);
     if (e != hipSuccess || !a.late) return e;
     return launch("k_lin_end", k_lin_end<DT, DV, DK>, dim3((unsigned)(a.nrank * p.Hv)), kThreads, a, st);
 }
