@@ -1,6 +1,9 @@
 // C ABI of linear attention with a decay for each head and of the query and key
 // norm: argument checks, workspace sizes, dispatch.  Every check runs on the host
 // before anything is enqueued.
+#include <algorithm>
+#include <utility>
+
 #include "gdn_internal.h"
 #include "../../include/gdn.h"
 
@@ -9,7 +12,53 @@ namespace {
 
 bool aligned(const void* ptr, uintptr_t a) { return (uintptr_t)ptr % a == 0; }
 int finish(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_E_HIP; }
+
+// Memory that a call reads or writes: n rows of `row` bytes, `stride` bytes apart
+struct Memory {
+    const void* at;
+    int64_t row, n = 1, stride = 0;
+    uintptr_t begin() const { return (uintptr_t)at; }
+    uintptr_t end() const { return begin() + (uintptr_t)((n - 1) * stride + row); }
+    bool none() const { return !at || row <= 0 || n <= 0; }
+};
+// Whether two of them have a byte in common.  Rows of one stride are compared row
+// by row (slices of one projection lie between each other); of rows of different
+// strides, their whole ranges.
+bool meet(Memory a, Memory b) {
+    if (a.none() || b.none() || a.end() <= b.begin() || b.end() <= a.begin()) return false;
+    for (Memory* m : {&a, &b})
+        if (m->n > 1 && m->stride == m->row) *m = Memory{m->at, m->n * m->row};
+    if (a.n > 1 && b.n > 1 && a.stride != b.stride) return true;
+    if (b.n == 1) std::swap(a, b);
+    if (b.n == 1) return true;
+    // b's row j and a's row i have one offset for each k = j - i; the smallest at
+    // which b's row ends behind the begin of a's
+    const int64_t off = (int64_t)(b.begin() - a.begin()), x = -off - b.row, s = b.stride;
+    const int64_t k = std::max(x / s - (x % s < 0) + 1, 1 - a.n);
+    return k < b.n && off + k * s < a.row;
+}
 bool dim_ok(int64_t d) { return d >= 16 && d <= 128 && d % 16 == 0; }
+// Whether something written meets something read, or another written
+template <int W, int R>
+bool any_meet(const Memory (&written)[W], const Memory (&read)[R]) {
+    for (int i = 0; i < W; ++i) {
+        for (const Memory& r : read)
+            if (meet(written[i], r)) return true;
+        for (int j = 0; j < i; ++j)
+            if (meet(written[i], written[j])) return true;
+    }
+    return false;
+}
+// All tokens' rows of d elements, and a pool's slots (as many as an index reaches)
+template <class P>
+Memory tokens_of(const void* at, int64_t d, int64_t stride, const P& p) {
+    const int64_t e = p.dtype == GDN_BF16 ? 2 : 4;
+    return {at, d * e, p.N, stride * e};
+}
+Memory pool_of(const void* at, int64_t slots, const Linear& p) {
+    return {at, std::min<int64_t>(slots, INT32_MAX) * p.Hv * p.dk * p.dv * 4};
+}
+
 // A launch holds fewer than 2^32 threads.  The most a call asks for, for each
 // sequence and head: 4 x 256 token by token, 16 x 256 between segments (forward:
 // of those alone that have some).  For each segment and head, N Hv / 256 + S Hv of
@@ -104,11 +153,16 @@ int linear_bwd_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, 
     if (!aligned(grad_out, 16) || !aligned(grad_state_out, 16) || !aligned(grad_q, 16) || !aligned(grad_k, 16) ||
         !aligned(grad_v, 16) || !aligned(grad_alpha, 4) || !aligned(grad_state0, 16) || !aligned(workspace, 16))
         return GDN_E_ARG;
-    // both are read and written in the sequences' order, by different workgroups
-    const int64_t states = S * Hv * dk * dv;
-    if (grad_state_out && grad_state0 && grad_state_out < grad_state0 + states && grad_state0 < grad_state_out + states)
-        return GDN_E_ARG;
-    if (!workspace || workspace_bytes < linear_backward_workspace(p)) return GDN_E_WORKSPACE;
+    const size_t need = linear_backward_workspace(p);
+    if (!workspace || workspace_bytes < need) return GDN_E_WORKSPACE;
+    // workgroups write rows and states while others read theirs
+    const int64_t e = dtype == GDN_BF16 ? 2 : 4, states = 4 * S * Hv * dk * dv;
+    const Memory read[] = {tokens_of(q, Hk * dk, q_stride, p), tokens_of(k, Hk * dk, k_stride, p),
+                           tokens_of(v, Hv * dv, v_stride, p), {grad_out, N * Hv * dv * e}, {grad_state_out, states},
+                           pool_of(state_in, n_in, p), {alpha, 4 * Hv}};
+    const Memory written[] = {{grad_q, N * Hk * dk * e}, {grad_k, N * Hk * dk * e}, {grad_v, N * Hv * dv * e},
+                              {grad_alpha, 4 * Hv}, {grad_state0, states}, {workspace, (int64_t)need}};
+    if (any_meet(written, read)) return GDN_E_ARG;
     b.dout = grad_out; b.ds_out = grad_state_out;
     b.dq = grad_q; b.dk = grad_k; b.dv = grad_v; b.dalpha = grad_alpha; b.ds0 = grad_state0;
     return finish(linear_backward(b, workspace, static_cast<hipStream_t>(stream)));

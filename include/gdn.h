@@ -461,13 +461,15 @@ size_t gdn_linear_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, 
  *   grad_alpha      [Hv] fp32, summed over all sequences (states enter it as
  *                   three bf16 terms, exactly); NULL: not wanted
  *   grad_state0     [S, Hv, dv, dk] fp32: dL/d of each sequence's start state
- *                   (sequences that share a slot each have their own; memory
- *                   of grad_state_out's: GDN_E_ARG); NULL: not wanted
+ *                   (sequences that share a slot each have their own); NULL:
+ *                   not wanted
  *   workspace       gdn_linear_backward_workspace_bytes(...): twice 4 Hv dk dv
  *                   for each sequence and for every 256 tokens, grad_alpha's
  *                   addends, and for few tokens (N Hk below 2^14) grad_q and
  *                   grad_k in fp32 parts: 32 MiB of them at most
- * S Hv = 0: nothing is enqueued, the gradients are left as they were.  Sums are
+ * No gradient, nor the workspace, may lie in memory of an input (all slots of
+ * state_in's pool count) or of another of them: GDN_E_ARG.  S Hv = 0: nothing is
+ * enqueued, the gradients are left as they were.  Sums are
  * taken in a fixed order (repeated calls give identical results).  NaN and
  * infinities as in gdn_linear_fwd: one in k may reach, within its feature of
  * grad_q, the 31 tokens in front of its own, one in q or grad_out, within its

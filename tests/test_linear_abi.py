@@ -74,6 +74,39 @@ def test_linear_backward_refusals(kw, want):
     assert bwd(**kw) == want
 
 
+# Buffers apart from each other (names as in fwd and bwd), and others within them
+APART = {n: (i + 1) << 36 for i, n in enumerate(("q", "k", "v", "alpha", "cu", "s_in", "s_out", "out", "go", "gs", "dq", "dkk",
+                                                 "dvv", "da", "ds", "ws", "gq", "gk", "wq", "wk", "cos", "sin", "pos", "qo",
+                                                 "ko", "dwq", "dwk"))}
+
+
+def at(name, offset=0):
+    return ctypes.c_void_p(APART[name] + offset)
+
+
+def apart(f, over, **kw):
+    """f with buffers of their own, but those of `over`, {name: (name, offset)}"""
+    names = f.__code__.co_varnames[:f.__code__.co_argcount]
+    args = {n: at(n) for n in names if n in APART}
+    args.update({n: at(*x) for n, x in over.items()})
+    return f(**{**args, **kw})
+
+
+ROW = 2 * 64 * 2  # bytes of a token's keys
+
+
+@pytest.mark.parametrize("over", [
+    {"ds": ("s_in", 0)}, {"ds": ("s_in", STATES - 16)}, {"s_in": ("ds", STATES - 16)},  # start states are read behind it
+    {"dq": ("q", 0)}, {"dkk": ("q", 0)}, {"dkk": ("k", 0)}, {"dvv": ("v", 0)}, {"dvv": ("go", 0)}, {"dq": ("go", 0)},
+    {"dvv": ("k", 100 * ROW - 16)}, {"go": ("dvv", 200 * ROW - 16)}, {"dq": ("v", 16)},
+    {"dkk": ("dq", 100 * ROW - 16)}, {"dvv": ("dkk", 0)}, {"ds": ("gs", STATES // 2)}, {"ds": ("dq", 0)},
+    {"da": ("alpha", 0)}, {"da": ("alpha", 12)}, {"da": ("ds", 16)}, {"ws": ("q", 0)}, {"ws": ("ds", 256)}, {"gs": ("ws", 16)},
+])
+def test_linear_backward_refuses_shared_memory(over):
+    assert apart(bwd, over) == ARG
+    assert apart(bwd, over, wsb=16) == WS  # the last of the checks
+
+
 def test_linear_workspace():
     ws = gdn.gdn_linear_workspace_bytes
     assert ws(256, 256, 16, 16, 128, 128, 1, 1) == 0 and ws(31, 1, 1, 1, 64, 64, 1000, 0) == 0  # token by token
