@@ -127,6 +127,14 @@ int linear_common(int64_t N, int64_t S, int64_t Hk, int64_t Hv, int64_t dk, int6
     const size_t need = linear_workspace(p);
     if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_E_WORKSPACE;
     if (!aligned(workspace, 16)) return GDN_E_ARG;
+    // (the pools may be one, or views of one whose slots lie upon each other)
+    const int64_t e = dtype == GDN_BF16 ? 2 : 4;
+    const Memory from = pool_of(state_in, n_in, p), to = pool_of(state_out, n_out, p);
+    const Memory read[] = {tokens_of(q, Hk * dk, q_stride, p), tokens_of(k, Hk * dk, k_stride, p),
+                           tokens_of(v, Hv * dv, v_stride, p), {alpha, 4 * Hv}};
+    const Memory written[] = {{out, N * Hv * dv * e}, to, {workspace, (int64_t)need}};
+    if (any_meet(written, read) || meet(written[0], from) || meet(written[2], from)) return GDN_E_ARG;
+    if (meet(from, to) && (int64_t)(from.begin() - to.begin()) % (4 * Hv * dk * dv) != 0) return GDN_E_ARG;
     return finish(linear_forward(p, workspace, static_cast<hipStream_t>(stream)));
 }
 

@@ -777,7 +777,8 @@ def linear_fwd(q, k, v, alpha, cu_seqlens, state_in=None, slots_in=None, state_o
     q, k [N,Hk,dk], v [N,Hv,dv] (bf16 or fp32; slices of a wider projection
     along the heads are taken as they are), alpha [Hv] fp32; cu_seqlens, the
     state pools, slots and max_len as for packed_fwd (state_out None: a new pool
-    [S,Hv,dv,dk], in the sequences' order).
+    [S,Hv,dv,dk], in the sequences' order; state_in: in place).  out and the
+    workspace may not share memory with anything else.
     Returns (out [N,Hv,dv] of q's dtype, state_out)."""
     import torch
     if state_out is None and slots_out is not None:

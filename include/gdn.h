@@ -418,7 +418,9 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  *   q, k        [N, Hk, dk], v [N, Hv, dv], strides, Hv a multiple of Hk,
  *               cu_seqlens, state_in, slots_in, state_out, slots_out, out,
  *               max_len: as for gdn_packed_fwd (the same rules for slots; in
- *               place or not)
+ *               place, in views of one pool whole slots apart, or not; any other
+ *               memory of out, the pools' or the workspace's that is also read
+ *               or written as something else: GDN_E_ARG)
  *   alpha       [Hv] fp32, 0 to 1 (not checked: powers of more may overflow);
  *               0: a token reads its own value alone
  *   workspace   gdn_linear_workspace_bytes(...) bytes: none for short sequences

@@ -107,6 +107,19 @@ def test_linear_backward_refuses_shared_memory(over):
     assert apart(bwd, over, wsb=16) == WS  # the last of the checks
 
 
+SHARED = [
+    {"out": ("v", 0)}, {"out": ("q", 0)}, {"out": ("k", 100 * ROW - 16)}, {"v": ("out", 200 * ROW - 16)},
+    {"out": ("s_in", STATES - 16)}, {"out": ("s_out", 0)}, {"s_out": ("v", 16)}, {"s_out": ("alpha", 0)},
+    {"s_out": ("s_in", 16)}, {"s_in": ("s_out", STATES - 16)},  # pools, but not slot upon slot
+]
+
+
+@pytest.mark.parametrize("max_len,over", [(n, over) for n in (1, 100) for over in SHARED] + [
+    (100, over) for over in ({"ws": ("s_in", 0)}, {"ws": ("s_out", 0)}, {"ws": ("k", 0)}, {"out": ("ws", 256)})])
+def test_linear_refuses_shared_memory(max_len, over):
+    assert apart(fwd, over, max_len=max_len, wsb=1 << 40) == ARG
+
+
 def test_linear_workspace():
     ws = gdn.gdn_linear_workspace_bytes
     assert ws(256, 256, 16, 16, 128, 128, 1, 1) == 0 and ws(31, 1, 1, 1, 64, 64, 1000, 0) == 0  # token by token
