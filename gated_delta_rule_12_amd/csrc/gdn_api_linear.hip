@@ -200,6 +200,10 @@ int qk_tables(const QkNorm& p) {
     if (!p.cos || !p.sin) return GDN_E_ARG;
     return p.n_pos > 0 ? GDN_OK : GDN_E_SHAPE;
 }
+// What of q's or k's rows the rows at y may lie upon: nothing of them, or each row
+// upon its own (in place)
+bool same_rows(const Memory& x, const Memory& y) { return x.at == y.at && x.row == y.row && (x.n == 1 || x.stride == y.stride); }
+bool qk_meet(const Memory& y, const Memory& x) { return !same_rows(x, y) && meet(x, y); }
 QkNorm qk_sizes(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot, int64_t n_pos, int32_t dtype, int32_t rotation) {
     QkNorm p{};
     p.N = N; p.Hq = Hq; p.Hk = Hk; p.d = d; p.rot = rot; p.n_pos = n_pos;
@@ -224,6 +228,11 @@ int qk_fwd_common(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot, int
     if ((s = qk_side(p, Hk, k, k_stride, k_out, k_out_stride)) != GDN_OK) return s;
     if ((s = qk_tables(p)) != GDN_OK) return s;
     if (N * (Hq + Hk) == 0) return GDN_OK;
+    const Memory read[] = {{weight_q, 4 * d}, {weight_k, 4 * d}, {cos, 2 * rot * n_pos}, {sin, 2 * rot * n_pos}, {positions, 4 * N}};
+    const Memory xq = tokens_of(q, Hq * d, q_stride, p), xk = tokens_of(k, Hk * d, k_stride, p);
+    const Memory written[] = {tokens_of(q_out, Hq * d, q_out_stride, p), tokens_of(k_out, Hk * d, k_out_stride, p)};
+    if (any_meet(written, read) || qk_meet(written[0], xq) || meet(written[0], xk) || meet(written[1], xq) || qk_meet(written[1], xk))
+        return GDN_E_ARG;
     return finish(qk_norm_fwd(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -247,10 +256,23 @@ int qk_bwd_common(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot, int
     if ((grad_k || grad_weight_k) && (s = qk_side(p, Hk, k, k_stride, grad_k_out, gk_stride)) != GDN_OK) return s;
     if ((s = qk_tables(p)) != GDN_OK) return s;
     if (!aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(grad_weight_q, 4) || !aligned(grad_weight_k, 4)) return GDN_E_ARG;
-    if ((grad_weight_q || grad_weight_k) && qk_norm_workspace(p) > 0) {
-        if (!workspace || workspace_bytes < qk_norm_workspace(p)) return GDN_E_WORKSPACE;
+    const size_t need = grad_weight_q || grad_weight_k ? qk_norm_workspace(p) : 0;
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return GDN_E_WORKSPACE;
         if (!aligned(workspace, 16)) return GDN_E_ARG;
     }
+    // (the weights' gradients are written behind everything else)
+    const Memory none{nullptr, 0};
+    const Memory xq = grad_q || grad_weight_q ? tokens_of(q, Hq * d, q_stride, p) : none,
+                 xk = grad_k || grad_weight_k ? tokens_of(k, Hk * d, k_stride, p) : none,
+                 gq = xq.at ? tokens_of(grad_q_out, Hq * d, gq_stride, p) : none,
+                 gk = xk.at ? tokens_of(grad_k_out, Hk * d, gk_stride, p) : none;
+    const Memory read[] = {{weight_q, 4 * d}, {weight_k, 4 * d}, {cos, 2 * rot * n_pos}, {sin, 2 * rot * n_pos}, {positions, 4 * N}};
+    const Memory yq = tokens_of(grad_q, Hq * d, Hq * d, p), yk = tokens_of(grad_k, Hk * d, Hk * d, p), ws{workspace, (int64_t)need};
+    const Memory first[] = {yq, yk, ws}, all[] = {{grad_weight_q, 4 * d}, {grad_weight_k, 4 * d}, yq, yk, ws};
+    if (any_meet(first, read) || any_meet(all, {none}) || any_meet({ws}, {xq, xk, gq, gk}) || any_meet({yq}, {xk, gk}) ||
+        any_meet({yk}, {xq, gq}) || qk_meet(yq, xq) || qk_meet(yq, gq) || qk_meet(yk, xk) || qk_meet(yk, gk))
+        return GDN_E_ARG;
     p.part = static_cast<float*>(workspace);
     return finish(qk_norm_bwd(p, static_cast<hipStream_t>(stream)));
 }

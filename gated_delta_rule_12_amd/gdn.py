@@ -886,7 +886,7 @@ def qk_norm_fwd(q, k, weight_q=None, weight_k=None, cos=None, sin=None, position
     [n_pos,rot/2] fp32 or None (no rotation), positions [N] int32 or None (token t
     is at position t).  Features i and i + rot/2 turn together, interleaved: 2i
     and 2i + 1.  q_out, k_out: where to (None: new tensors; q and k themselves:
-    in place).  Returns (q_out, k_out)."""
+    in place; no other memory of q, k or each other).  Returns (q_out, k_out)."""
     N, Hq, Hk, d, rot, n_pos, dev = _qk_check(q, k, (weight_q, weight_k), cos, sin, positions)
     outs = []
     for x, y in ((q, q_out), (k, k_out)):

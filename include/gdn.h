@@ -509,7 +509,9 @@ size_t gdn_linear_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  *               0: not read)
  *   positions   [N] int32 on the device, or NULL: token t is at position t;
  *               clamped to 0 .. n_pos - 1
- *   q_out, k_out  as q and k; may be q and k (in place, the same stride)
+ *   q_out, k_out  as q and k; may be q and k (in place, the same stride), or
+ *               lie between rows of theirs that have the same stride; any other
+ *               memory of an input or of each other's: GDN_E_ARG
  * Statistics and products in fp32, rounded once; the sum of a row's x^2 has to
  * stay within fp32.  A row's NaN and infinities stay in the row.  No workspace.
  * d a multiple of 16 up to 256, rot of 16 up to d, else GDN_E_UNSUPPORTED (rot
@@ -531,7 +533,8 @@ int gdn_qk_norm_fwd(int64_t N, int64_t Hq, int64_t Hk, int64_t d, int64_t rot, i
  *   grad_q_out, grad_k_out  as q and k, with strides of their own
  *   grad_q, grad_k  [N, Hq, d], [N, Hk, d], dtype, contiguous; may be the
  *               incoming gradient's buffer or q's and k's where those are
- *               contiguous;  grad_weight_q, grad_weight_k [d] fp32.  NULL: not
+ *               contiguous (any other memory of an input or of another gradient:
+ *               GDN_E_ARG);  grad_weight_q, grad_weight_k [d] fp32.  NULL: not
  *               wanted (both of a side NULL: that side is not read)
  *   workspace   gdn_qk_norm_workspace_bytes(N, Hq, Hk, d), for the weights'
  *               gradients

@@ -151,6 +151,25 @@ def test_in_place_and_into_slices():
         assert torch.equal(a[0]._base[:, 6:], rest)  # the rest of the projection
 
 
+def test_into_other_slices_of_the_same_projection():
+    """Results between the inputs' rows are no memory of theirs; swapped or shifted
+    by a token they are, and refused."""
+    import torch
+    c = Case(90, 4, 2, 64, 32, seed=16)
+    a = c.args()
+    want = gdn.qk_norm_fwd(*a, **c.kw())
+    wide = torch.full((91, 14, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    wide[:90, :4], wide[:90, 7:9] = a[0], a[1]
+    q, k, yk, yq = wide[:90, :4], wide[:90, 7:9], wide[:90, 4:6], wide[:90, 9:13]
+    gdn.qk_norm_fwd(q, k, *a[2:], **c.kw(), q_out=yq, k_out=yk)
+    torch.cuda.synchronize()
+    assert torch.equal(yq, want[0]) and torch.equal(yk, want[1]) and torch.equal(q, a[0]) and torch.equal(k, a[1])
+    assert (wide[:, 6] == 3).all() and (wide[:, 13] == 3).all() and (wide[90] == 3).all()
+    for out in (dict(q_out=wide[1:, :4]), dict(q_out=wide[:90, 6:10]), dict(k_out=wide[:90, 3:5]), dict(q_out=yq, k_out=wide[:90, 12:])):
+        with pytest.raises(gdn.GdnError):
+            gdn.qk_norm_fwd(q, k, *a[2:], **c.kw(), **out)
+
+
 def test_gradients_into_their_own_buffers():
     """grad_q, grad_k over the incoming gradients (raw entry point)."""
     import ctypes

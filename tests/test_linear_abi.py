@@ -190,6 +190,37 @@ def test_qk_norm_backward_refusals(kw, want):
     assert qk_bwd(**kw) == want
 
 
+QROW, KROW = 4 * 64 * 2, 2 * 64 * 2  # bytes of a token's queries and keys
+
+
+@pytest.mark.parametrize("over,kw", [
+    ({"qo": ("k", 0), "ko": ("q", 0)}, {}),                                 # swapped
+    ({"qo": ("k", 0)}, {}), ({"ko": ("q", 16)}, {}),
+    ({"qo": ("q", QROW)}, {}), ({"q": ("qo", 9 * QROW)}, {}), ({"ko": ("k", 9 * KROW)}, {}),  # by whole tokens
+    ({"qo": ("q", 16)}, {}), ({"qo": ("q", 0)}, dict(so=512)), ({"ko": ("k", 0)}, dict(sk=512)),  # one stride of two
+    ({"qo": ("ko", 10 * KROW - 16)}, {}), ({"qo": ("ko", 0)}, {}),
+    # in one projection of 512 elements a token: q's columns 0 .., k's 256 ..
+    ({"k": ("q", 512), "qo": ("q", 0), "ko": ("q", 512 - 16)}, dict(sq=512, sk=512, so=512, sp=512)),
+    ({"k": ("q", 512), "qo": ("q", 0), "ko": ("q", 512 + 1024)}, dict(sq=512, sk=512, so=512, sp=512)),
+    ({"qo": ("wk", 0)}, {}), ({"ko": ("cos", 100 * 64 - 16)}, {}), ({"ko": ("pos", 32)}, {}),
+])
+def test_qk_norm_refuses_shared_memory(over, kw):
+    assert apart(qk, over, **kw) == ARG
+
+
+@pytest.mark.parametrize("over,kw", [
+    ({"dq": ("k", 0)}, {}), ({"dq": ("gk", 0)}, {}), ({"dkk": ("gq", 0)}, {}), ({"dkk": ("q", 16)}, {}),
+    ({"dq": ("q", QROW)}, {}), ({"dq": ("gq", 16)}, {}), ({"dkk": ("gk", 9 * KROW)}, {}),
+    ({"dq": ("q", 0)}, dict(sq=512)), ({"dq": ("gq", 0)}, dict(sgq=512)), ({"dkk": ("gk", 0)}, dict(sgk=512)),
+    ({"dq": ("dkk", 0)}, {}), ({"dwq": ("dwk", 0)}, {}), ({"dwq": ("dq", 16)}, {}), ({"dwk": ("ws", 0)}, {}),
+    ({"ws": ("q", 0)}, {}), ({"ws": ("gk", 0)}, {}), ({"ws": ("wq", 0)}, {}), ({"ws": ("dq", 0)}, {}),
+    ({"dq": ("sin", 0)}, {}), ({"dkk": ("wk", 0)}, {}),
+])
+def test_qk_norm_backward_refuses_shared_memory(over, kw):
+    assert apart(qk_bwd, over, **kw) == ARG
+    assert apart(qk_bwd, over, **{**kw, "wsb": 16}) == WS  # the last of the checks
+
+
 def test_qk_norm_workspace():
     ws = gdn.gdn_qk_norm_workspace_bytes
     assert ws(1, 4, 2, 64) == 2 * 64 * 4 and ws(0, 4, 2, 64) == 0 and ws(10, 4, 2, 60) == 0
