@@ -115,6 +115,14 @@ def test_forward(i):
     check(c, *run(c))
 
 
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("i,lengths,hk,hv,dk,dv", [(0, (300, 33, 513, 2), 1, 2, 128, 64), (1, (257, 40), 2, 4, 112, 48),
+                                                   (2, (31, 32, 256, 1000), 1, 3, 80, 16)])
+def test_keys_wider_than_values(i, lengths, hk, hv, dk, dv, inplace):
+    c = Linear(lengths, hk, hv, dk, dv, slots=1, seed=50 + i).make()
+    check(c, *run(c, inplace=inplace), inplace=inplace)
+
+
 @pytest.mark.parametrize("lengths,dk,dv", [((1, 1, 1), 128, 128), ((3, 90, 1200, 256), 128, 128), ((5, 600, 33), 48, 96)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_in_place(lengths, dk, dv, dtype):

@@ -138,6 +138,30 @@ def test_forward_and_backward(i):
     check(CASES[i])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("N,hq,hk,d", [(9000, 16, 16, 128), (4001, 31, 5, 48)])
+def test_gradients_of_more_rows_than_workgroups_hold(N, hq, hk, d, interleaved, dtype):
+    """Workgroups that take several rounds, the last of them in part.  A weight's
+    gradient is a chain of a lane's rows, of a workgroup's groups of lanes and, in 64
+    chains joined by a tree, of the workgroups: each addition off by u of sums that
+    are at most the sum of sizes, each term by (d / 2 + 8) u of itself.  One
+    workgroup adds some twenty times that."""
+    import torch
+    c = Case(N, hq, hk, d, 32, dtype=dtype, interleaved=interleaved, n_pos=1000, seed=17)
+    got = gdn.qk_norm_backward(*(c.up(x, True) for x in c.dy), *c.args(), **c.kw())
+    torch.cuda.synchronize()
+    per = 256 // (1 << (d // 8 - 1).bit_length())  # groups of four heads that a workgroup takes a round
+    for i, (dx, size, dw, dwsize) in enumerate(c.backward()):
+        h = (hq, hk)[i]
+        units = N * -(-h // 4)
+        blocks = min(-(-units // per), 1024 * h // (hq + hk))
+        rounds = -(-units // (per * blocks))
+        assert rounds > 1 and units % (per * blocks) != 0
+        near(got[i], dx, (2 * d + 16) * U * size, dtype)
+        near(got[2 + i], dw, (4 * rounds + per + -(-blocks // 64) + 6 + d / 2 + 8) * U * dwsize, "f32")
+
+
 def test_in_place_and_into_slices():
     import torch
     for dtype in ("bf16", "f32"):
