@@ -912,6 +912,17 @@ __device__ __forceinline__ void gather(f32x4 (&acc)[IT][D / 16], const f32x4 (&p
     }
 }
 
+// As split4, each element's terms formed from itself alone: there an infinity or a
+// NaN makes its neighbour's low term a NaN too.
+__device__ __forceinline__ void split4_apart(const f32x4& x, u16x4& hi, u16x4& lo) {
+    auto low = [](uint32_t h, float a, float b) {
+        return pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xFFFF0000u));
+    };
+    const uint32_t h0 = pack_bf16(x[0], x[1]), h1 = pack_bf16(x[2], x[3]);
+    hi = __builtin_bit_cast(u16x4, u32x2{h0, h1});
+    lo = __builtin_bit_cast(u16x4, u32x2{low(h0, x[0], x[1]), low(h1, x[2], x[3])});
+}
+
 // 32 rows (TR: columns) of a state [dv][dk] on their way to LDS, where they lie
 // split into terms, and their products with a wave's rows.
 template <int DT, int DV, int DK, bool TR, int NT, int TERMS>
@@ -947,7 +958,8 @@ struct Slab {
                 for (int e = 0; e < 3; ++e) *reinterpret_cast<u32x2*>(to + e * LO) = t[e];
             } else if constexpr (TERMS == 2) {
                 u16x4 hi, lo;
-                split4(r[k], hi, lo);
+                if (TR) split4_apart(r[k], hi, lo);  // (neighbours are features of two results)
+                else split4(r[k], hi, lo);  // (of one sum)
                 *reinterpret_cast<u16x4*>(to) = hi;
                 *reinterpret_cast<u16x4*>(to + LO) = lo;
             } else {

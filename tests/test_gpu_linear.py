@@ -316,6 +316,29 @@ def test_non_finite_inputs_propagate(what, value, dtype):
     near(c, got[~bad], ends[~bad], esize[~bad], "f32")
 
 
+@pytest.mark.parametrize("value", [np.inf, np.nan])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,da", [((64, 64), True), ((128, 128), False), ((80, 48), False), ((64, 128), False), ((128, 64), True)])
+def test_non_finite_states_leave_the_features_beside_theirs(d, da, dtype, value):
+    """One infinity or NaN in a start state or in the gradient of an end state, at
+    an even and at an odd key feature: dq (dk) is non-finite in that feature alone,
+    dv in its value feature, with or without dalpha."""
+    for n, i, at in (("pool", 24, 1), ("pool", 25, 1), ("dstate", 24, 2), ("dstate", 25, 2), ("dstate", 12, 0)):
+        c = Linear((300, 40, 33), 1, 2, *d, dtype=dtype, seed=48).make()
+        c.a[n][c.a["slots_in"][at] if n == "pool" else at, 1, 5, i] = value
+        got = grads_of(c, want_grad_alpha=da)
+        with np.errstate(invalid="ignore"):
+            want, sizes = c.backward(), c.backward(size=True)
+        for name, x, ref, size in zip(("dq", "dk", "dv", "dalpha", "dstate0"), got, want, sizes):
+            if x is None:
+                continue
+            fine = np.isfinite(ref)
+            wrong = np.argwhere(np.isfinite(x) != fine)
+            assert not len(wrong), (n, name, len(wrong), wrong[0], wrong[-1])
+            if name != "dalpha":
+                near(c, x[fine], ref[fine], size[fine], "f32" if name == "dstate0" else dtype)
+
+
 @pytest.mark.parametrize("dk", [16, 48, 80, 112])
 def test_infinite_states_of_single_tokens(dk):
     """Token by token an infinity stays what the formula makes of it, in the last
