@@ -422,6 +422,34 @@ struct Tile {
             *reinterpret_cast<u32x4*>(tile + p / PPR * LD + V * (p % PPR)) = r[k];
         }
     }
+    // Whether one of the pieces holds an infinity or a NaN: its exponent is all ones,
+    // and one more carries into the sign's place
+    __device__ __forceinline__ bool odd() const {
+        constexpr uint32_t ones = sizeof(T) == 2 ? 0x7F807F80u : 0x7F800000u, one = sizeof(T) == 2 ? 0x00800080u : 0x00800000u;
+        uint32_t x = 0;
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x |= (r[k][j] & ones) + one;
+        return (x & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u)) != 0;
+    }
+    // Sets infinities and NaN of the thread's pieces in LDS to zero and the bit of their
+    // row in their feature's word of `mask`
+    static __device__ __forceinline__ void clear_odd(T* tile, uint32_t* mask, int tid) {
+        asm volatile("" ::: "memory");  // (they were put as vectors of another type)
+#pragma unroll 1
+        for (int x = 0; x < NP * V; ++x) {
+            const int p = tid + x / V * NT, row = p / PPR, f = V * (p % PPR) + x % V;
+            if (ALL < NT && p >= ALL) return;
+            T* at = tile + row * LD + f;
+            uint32_t exponent;
+            if constexpr (sizeof(T) == 2) exponent = (uint32_t)*at << 16;
+            else exponent = __float_as_uint(*at);
+            if ((exponent & 0x7F800000u) != 0x7F800000u) continue;
+            *at = T(0);
+            atomicOr(mask + f, 1u << row);
+        }
+    }
 };
 
 // ---------------------------------------------------------------------------
@@ -1069,14 +1097,30 @@ constexpr int rows_lds() {
     constexpr int tiles = 2 * (Tile<DT, DK, kThreads>::kSize + Tile<DT, DV, kThreads>::kSize), TERMS = state_terms<DT, SLOPES>();
     return std::max(tiles, 2 * std::max(Slab<DT, DV, DK, false, kThreads, TERMS>::kSize, Slab<DT, DV, DK, true, kThreads, TERMS>::kSize));
 }
+// The tiles of keys that a workgroup's own rows lie in are seen in part: the keys
+// behind a row (REV: in front of it) have a weight of zero, and zero times an infinity
+// or a NaN would be a NaN in a row that does not see it.  What is not finite in B is
+// set to zero in these tiles (PARTS of them) and noted, and behind the last tile the
+// rows that see it are made NaN in its feature.  Looking for it costs 1 to 3 % of a
+// call (one of 65531 tokens 2, a training step of 16384 1.5, prompts with heads of 64 3).
+template <int PARTS>
+struct Odd {
+    int found;
+    uint32_t mask[PARTS][128];  // of each feature, the tile's rows
+    template <int NT>
+    __device__ __forceinline__ void clear(int tid) {
+        if (tid == 0) found = 0;
+        for (int x = tid; x < PARTS * 128; x += NT) (&mask[0][0])[x] = 0;
+    }
+};
 template <int DT, int DK, int DV, int NT, int IT, int KIND, bool SLOPES>
 __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned blocks, typename El<DT>::T* lds, float* tab,
-                                        float* sums) {
+                                        Odd<Shape<DT>::ROWS / El<DT>::TT>& odd, float* sums) {
     using E = El<DT>;
     using T = typename E::T;
     using Op = typename E::Op;
     constexpr bool REV = Made<KIND>::REV, TR = Made<KIND>::TR, SUM = Made<KIND>::SUM;
-    constexpr int DX = TR ? DV : DK, DM = TR ? DK : DV, TT = E::TT, kBlockRows = NT / 4 * IT;
+    constexpr int DX = TR ? DV : DK, DM = TR ? DK : DV, TT = E::TT, kBlockRows = NT / 4 * IT, PARTS = kBlockRows / TT;
     using TA = Tile<DT, DX, NT>;
     using TB = Tile<DT, DM, NT>;
     constexpr int TERMS = state_terms<DT, SLOPES>();
@@ -1109,6 +1153,7 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
     for (int it = 0; it < IT; ++it)
 #pragma unroll
         for (int mt = 0; mt < DM / 16; ++mt) acc[it][mt] = zero4();
+    odd.template clear<NT>(thread);  // (the barrier in front of the first tile is behind this)
     for (int j = from; j < to; ++j) {
         const int tid = SUM ? anew(thread) : thread, g = (tid & 63) >> 4, i = tid & 15;
         const int h = hh * nh + j, hk = SUM ? hh : hh / a.group;
@@ -1183,14 +1228,19 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
                 }
                 in_order<DT>();
             }
-            __syncthreads();
         }
+        __syncthreads();
         fetch(first, 0);
         fetch(first + 1, 1);
         auto step = [&](int t, int b) {
             T *ba = lds + b * TA::kSize, *bb = lds + 2 * TA::kSize + b * TB::kSize;
             ta[b].put(ba, tid);
             tb[b].put(bb, tid);
+            const unsigned part = t - rb * kBlockRows / TT;
+            if (__builtin_expect(part < PARTS && tb[b].odd(), 0)) {
+                odd.found = 1;
+                TB::clear_odd(bb, odd.mask[part], anew(tid));
+            }
             fetch(t + 2, b);
             __syncthreads();
             const int kblk = t * TT / 16;
@@ -1218,6 +1268,27 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
             step(t + 1, 1);
         }
         if (t < nt) step(t, 0);
+        if (__builtin_expect(odd.found, 0)) {
+            const int own = anew(tid), g = (own & 63) >> 4, i = own & 15;
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll 1
+                for (int part = 0; part < PARTS; ++part) {
+                    const int x = 16 * (rblk + it) - (rb * kBlockRows + part * TT) + i;  // the row's own place in the tile
+                    const uint32_t see = REV ? (x > 31 ? 0u : ~0u << max(x, 0)) : (x < 0 ? 0u : ~0u >> (31 - min(x, 31)));
+#pragma unroll
+                    for (int mt = 0; mt < DM / 16; ++mt) {
+                        in_order();  // (few registers)
+                        const uint32_t* m = odd.mask[part] + 16 * mt + 4 * g;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[it][mt][e] = m[e] & see ? __builtin_nanf("") : acc[it][mt][e];
+                    }
+                }
+            if (j + 1 < to) {
+                __syncthreads();
+                odd.template clear<NT>(own);
+            }
+        }
         if constexpr (SLOPES) sum_to<NT>(da, sums, part + j * a.parts, tid);
     }
     T* out = static_cast<T*>(KIND == kOut ? p.out : KIND == kDq ? a.dq : KIND == kDk ? a.dk : a.dv) + (int64_t)hh * dm;
@@ -1246,10 +1317,11 @@ __device__ __forceinline__ void rows_of(const Lin& a, unsigned block, unsigned b
 }
 
 template <int DT, int DK, int DV>
-__global__ __launch_bounds__((OutShape<DT, DV>::NT), (OutShape<DT, DV>::WAVES)) void k_lin_out(Lin a) {
+__global__ __launch_bounds__((OutShape<DT, DV>::NT), (DK + DV > 128 ? OutShape<DT, DV>::WAVES : 4)) void k_lin_out(Lin a) {
     __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV, false>()];
     __shared__ __attribute__((aligned(16))) float tab[kSeg];
-    rows_of<DT, DK, DV, OutShape<DT, DV>::NT, OutShape<DT, DV>::IT, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, nullptr);
+    __shared__ Odd<Shape<DT>::ROWS / El<DT>::TT> odd;
+    rows_of<DT, DK, DV, OutShape<DT, DV>::NT, OutShape<DT, DV>::IT, kOut, false>(a, blockIdx.x, gridDim.x, lds, tab, odd, nullptr);
 }
 // dalpha's pairs of tokens: sum over i > j of (i - j) a^(i-j-1) (q_i.k_j)
 // (do_i.v_j), rows j of a value head, both kinds of scores at once.
@@ -1346,14 +1418,15 @@ __global__ __launch_bounds__(Shape<DT>::NT, Shape<DT>::WAVES) void k_lin_grads(L
     constexpr int NT = Shape<DT>::NT, IT = Shape<DT>::IT;
     __shared__ __attribute__((aligned(16))) typename El<DT>::T lds[rows_lds<DT, DK, DV, SLOPES>()];
     __shared__ __attribute__((aligned(16))) float tab[kSeg];
+    __shared__ Odd<Shape<DT>::ROWS / El<DT>::TT> odd;
     __shared__ float sums[NT / 64];
     unsigned b = blockIdx.x;
     if (b < blocks_k) {
-        rows_of<DT, DK, DV, NT, IT, kDk, false>(a, b, blocks_k, lds, tab, sums);
+        rows_of<DT, DK, DV, NT, IT, kDk, false>(a, b, blocks_k, lds, tab, odd, sums);
     } else if ((b -= blocks_k) < blocks_k) {
-        rows_of<DT, DK, DV, NT, IT, kDq, SLOPES>(a, b, blocks_k, lds, tab, sums);
+        rows_of<DT, DK, DV, NT, IT, kDq, SLOPES>(a, b, blocks_k, lds, tab, odd, sums);
     } else if ((b -= blocks_k) < blocks_v) {
-        rows_of<DT, DK, DV, NT, IT, kDv, SLOPES>(a, b, blocks_v, lds, tab, sums);
+        rows_of<DT, DK, DV, NT, IT, kDv, SLOPES>(a, b, blocks_v, lds, tab, odd, sums);
     } else if constexpr (SLOPES) {
         slopes_of<DT, DK, DV, NT, IT>(a, b - blocks_v, blocks_v, lds, tab, sums);
     }

@@ -432,9 +432,8 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  * multiplied with a power of alpha as two (scores, start states: 2^-17) or three
  * (what enters the states: exact) bf16 terms.  The others run token by token.
  * All sums and states are fp32; out is rounded once.
- * NaN and infinities propagate as in the formula, to nothing of other sequences;
- * in segments an infinity may become a NaN, and one in v may reach, within its
- * value feature, the 31 tokens in front of its own.
+ * NaN and infinities propagate as in the formula, to nothing of other sequences and
+ * no token in front of theirs; in segments an infinity may become a NaN.
  * Everything else (empty sequences, offsets out of order or range, capture,
  * alignment, statuses and limits, those of chunk kernels where there are
  * segments) is as for gdn_packed_fwd.
@@ -471,11 +470,9 @@ size_t gdn_linear_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, 
  *                   grad_k in fp32 parts: 32 MiB of them at most
  * No gradient, nor the workspace, may lie in memory of an input (all slots of
  * state_in's pool count) or of another of them: GDN_E_ARG.  S Hv = 0: nothing is
- * enqueued, the gradients are left as they were.  Sums are
- * taken in a fixed order (repeated calls give identical results).  NaN and
- * infinities as in gdn_linear_fwd: one in k may reach, within its feature of
- * grad_q, the 31 tokens in front of its own, one in q or grad_out, within its
- * feature of grad_k or grad_v, the 31 behind it.  Alignment: as
+ * enqueued, the gradients are left as they were.  Sums are taken in a fixed order
+ * (repeated calls give identical results).  NaN and infinities as in
+ * gdn_linear_fwd, to nothing that the chain rule keeps from them.  Alignment: as
  * gdn_packed_backward; limits as of a call with segments, in fp32 half of them
  * (S Hv over 2^18, N Hv over 2^27: GDN_E_SHAPE).
  */

@@ -339,6 +339,37 @@ def test_non_finite_states_leave_the_features_beside_theirs(d, da, dtype, value)
                 near(c, x[fine], ref[fine], size[fine], "f32" if name == "dstate0" else dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [np.inf, np.nan])
+@pytest.mark.parametrize("what", ["q", "k", "v", "dout"])
+@pytest.mark.parametrize("d,at", [((64, 64), (0, 300)), ((128, 128), (31, 511)), ((64, 128), (143, 440)), ((80, 48), (255, 256)),
+                                  ((128, 64), (17, 699))])
+def test_non_finite_inputs_reach_no_token_that_does_not_see_them(d, at, what, value, dtype):
+    """Infinities or NaN at two tokens of one sequence: outputs, states and gradients
+    are non-finite where the formula is, and right everywhere else, in front of
+    those tokens (dk, dv: behind them) as well."""
+    c = Linear((40, 700, 33), 1, 2, *d, dtype=dtype, seed=46).make()
+    for i, t in enumerate(at):
+        if what in ("v", "dout"):
+            c.a[what][40 + t, 1, 5 + 20 * i] = value
+        else:
+            c.a[what][40 + t, 0, 5 + 20 * i] = -value
+    out, pool = run(c)
+    got = [out, pool[c.a["slots_out"]], *grads_of(c)]
+    with np.errstate(invalid="ignore"):
+        want = [*c.forward(), *c.backward()]
+        sizes = [*c.forward(size=True), *c.backward(size=True)]
+    for name, x, ref, size in zip(("out", "states", "dq", "dk", "dv", "dalpha", "dstate0"), got, want, sizes):
+        fine = np.isfinite(ref)
+        wrong = np.argwhere(np.isfinite(x) != fine)
+        assert not len(wrong), (name, len(wrong), wrong[0], wrong[-1])
+        if name == "dalpha":
+            lim = (2.0**-16 + (max(c.lengths) + 2 * c.dk + 2 * c.dv) * 2.0**-24) * size
+            assert (np.abs(x - ref) <= lim)[fine].all()
+        else:
+            near(c, x[fine], ref[fine], size[fine], "f32" if name in ("states", "dstate0") else dtype)
+
+
 @pytest.mark.parametrize("dk", [16, 48, 80, 112])
 def test_infinite_states_of_single_tokens(dk):
     """Token by token an infinity stays what the formula makes of it, in the last
