@@ -62,11 +62,9 @@ constexpr int lin_min(int dtype) { return dtype == GDN_BF16 ? 32 : 64; }
 // Tokens of a segment.
 constexpr int kSeg = 256;
 
-// A segment: its tokens, its sequence, whether it is that one's first or last,
-// and above these two bits that one's rank.
+// A segment: its tokens, its sequence, whether it is that one's first or last.
 struct Seg {
     int begin, n, seq, ends;
-    __device__ int rank() const { return ends >> 2; }
 };
 constexpr int kFirst = 1, kLast = 2;
 
@@ -205,7 +203,7 @@ __device__ __forceinline__ void plan_segments(const Lin& a, int tid) {
         x.begin = x.n > 0 ? (int)(sp.begin + from) : 0;
         x.seq = s;
         // (where the table ends, so does the sequence: no segment looks behind it)
-        x.ends = (from == 0 ? kFirst : 0) | (from + kSeg >= sp.n || i + 1 == total[1] ? kLast : 0) | lo << 2;
+        x.ends = (from == 0 ? kFirst : 0) | (from + kSeg >= sp.n || i + 1 == total[1] ? kLast : 0);
         a.segs[i] = x;
     }
 }
@@ -602,7 +600,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_lin_add(Lin a, unsigned recs) {
     const Seg sg = segment(a, si);
     if (sg.n == 0) return;
     if (rev ? (sg.ends & kFirst) && !a.ds0 : (sg.ends & kLast) && (a.late || !a.p.s_out)) return;
-    if (!rev && sg.ends == (kFirst | kLast | sg.rank() << 2)) {
+    if (!rev && sg.ends == (kFirst | kLast)) {
         end_state<DT, DV, DK>(a, sg, si, h, lds, wt);
         return;
     }
