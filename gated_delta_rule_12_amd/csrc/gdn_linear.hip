@@ -21,7 +21,8 @@
 // of 128, as much as 256 tokens of it in one array), and what is quadratic in a
 // segment grows with its length.  512 tokens: outputs 122 instead of 88 us, the scan
 // 20 instead of 33, additions 43 instead of 45 (one sequence of 65531 tokens, 4
-// heads of 128).
+// heads of 128, bf16; fp32, where products cost eight times as much, was not
+// measured with others).
 //
 // Forward: k_lin_plan (where the segments lie), k_lin_add (what each adds to its
 // state; short sequences beside that), k_lin_scan (the states between), k_lin_out (the
@@ -30,18 +31,23 @@
 // for states and gradients of states at once, k_lin_grads has all rows, k_lin_join
 // sums addends.  Sequences of few tokens: k_lin_rec alone.
 //
-// Kernel times in us, and what bounds them (bf16, heads of 128; 6.05 TB/s is the rate
-// of a copy on this card):
-//   one sequence of 65531 tokens, 4 heads: plan 5, add 46 (201 MB moved: 4.4 TB/s;
-//     without products 43, without stores 36, with few loads 37),
-//     scan 35 (134 MB, one chain of 256 segments an element), out 84 (335 MB: 55 at
-//     least; with waves of 32 rows 88, of which loads alone 66, without tiles of tokens
-//     46, without the start states 71, with scores of one term 80)
-//   40 sequences, 16384 tokens, 16 heads: 6, 67 (short sequences inside), 28, 86
+// Kernel times in us, and what bounds them (bf16, heads of 128; averages of a kernel
+// trace of 45 calls behind 5, from a device that was idle: such calls take 200, 185
+// and 558 us without a trace as well, the same in a long row 179, 170 and 526; 6.05
+// TB/s is the rate of a copy on this card):
+//   40 sequences, 16384 tokens, 16 heads: plan 6, add 69 (short sequences inside), scan
+//     29, out 96; in place 6, 54, 25, 93, end 25
+//   one sequence of 65531 tokens, 4 heads: 5, add 46 (201 MB moved: 4.4 TB/s; without
+//     products 43, without stores 36, with few loads 37), scan 36 (134 MB, one chain
+//     of 256 segments an element), out 96 (335 MB: 55 at least); in place 5, 46, 36,
+//     92, end 16.  Best times of the outputs with waves of 32 rows: 88, loads alone 66,
+//     without tiles of tokens 46, without the start states 71, with scores of one
+//     term 80
 //   7 sequences, 16384 tokens, 16 heads, backward: 6, add 82 (260 MB moved), scan 58
-//     (235 MB), gradients 392 (870 MB from and to HBM take 145; matrix cores are busy
+//     (235 MB), gradients 403 (870 MB from and to HBM take 145; matrix cores are busy
 //     21 % of the time, vector ALU 28 %, LDS 19 %; waves wait for memory and barriers
-//     37 % and for each other's issue 34 %), join 5
+//     37 % and for each other's issue 34 %; 27 of 256 registers a lane are spilled),
+//     join 5
 //   a step of 256 single tokens, 16 heads: 92 (the states at 5.8 TB/s)
 #include "gdn_elements.h"
 #include "gdn_internal.h"
@@ -55,7 +61,7 @@ namespace {
 // Sequences of fewer tokens go token by token (forward): a chain of latencies that
 // many sequences share a chip for, against one pass of a segment.  Heads of 128, 16
 // heads, tokens against segments: bf16 16 sequences of 32 tokens 29.6 and 30 us,
-// 256 of 32 352 and 322, 256 of 48 516 and 344; fp32 (an eighth of the matrix
+// 256 of 32 352 and 322, 256 of 48 516 and 357; fp32 (an eighth of the matrix
 // rate) 16 of 48 37 and 60, 256 of 48 532 and 852, 16 of 200 142 and 110, 256 of
 // 200 1894 and 1621: about even from 64 tokens (few) to 130 (many) on.
 constexpr int lin_min(int dtype) { return dtype == GDN_BF16 ? 32 : 64; }
@@ -456,8 +462,8 @@ struct Tile {
 // M[r][c] = sum_j w_j X[j][r] Y[j][c] over a segment: to its end state (X = v,
 // Y = k, w_j = a^{n-1-j}) or to the gradient of its start state (X = do, Y = q,
 // w_j = scale a^{j+1}).  Y is an exact operand; w_j X[j] is an fp32 value, which
-// three bf16 terms hold to the last bit, so that states are as exact as fp32
-// arithmetic makes them.
+// three bf16 terms hold to the last bit (above 2^-102, where the third is no
+// subnormal), so that states are as exact as fp32 arithmetic makes them.
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l) {
     auto top = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); };
     auto two = [](float x, float y) { return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u); };
@@ -1069,12 +1075,13 @@ __device__ __forceinline__ int anew(int x) {
 // A workgroup has 128 rows of a head (fp32: 64); dq's and dk's are a key head's,
 // its value heads one after the other in one sum.  Four waves of 32 rows (fp32: 16)
 // read each operand from LDS for twice as many products as eight of 16: gradients
-// of a training step 430 instead of 615 us (heads of 128: the eight spill), outputs
-// with values of 64 68 instead of 76 us.  Outputs with values of 128 are made by
-// eight, whose registers let sixteen waves share a compute unit (one sequence of
-// 65531: 84 instead of 88 us, a mixed batch 86 instead of 88).  With 256 rows a
-// workgroup, tiles are read once but waves wait for the last rows' (94 instead of
-// 92, 100 instead of 88).
+// of a training step 430 instead of 615 us (heads of 128; the loop over value heads
+// takes registers: the four waves spill 27 of 256, the eight more of their 128, so
+// that this says nothing of eight waves without the loop), outputs with values of 64
+// 68 instead of 76 us.  Outputs with values of 128 are made by eight, whose registers
+// let sixteen waves share a compute unit (best times: one sequence of 65531 84 instead
+// of 88 us, a mixed batch 86 instead of 88).  With 256 rows a workgroup, tiles are
+// read once but waves wait for the last rows' (94 instead of 92, 100 instead of 88).
 template <int DT>
 struct Shape {
     static constexpr int NT = 256, IT = DT == GDN_BF16 ? 2 : 1, ROWS = NT / 4 * IT, WAVES = 2;
@@ -1085,7 +1092,9 @@ struct OutShape {
 };
 // Terms of the states.  Rows of bf16 results are far from seeing an error of
 // 2^-17; dalpha, an fp32 sum over all tokens, is not (two terms left it 1e-6 to 9e-6
-// off, three leave 1e-7 to 4e-7), and three hold an fp32 state exactly.
+// off on inputs where three leave 1e-8 to 4e-7; where terms of both signs nearly
+// cancel, three leave up to 2e-6, as fp32 sums do), and three hold an fp32 state
+// exactly (above 2^-102).
 template <int DT, bool SLOPES>
 constexpr int state_terms() {
     return DT == GDN_BF16 && SLOPES ? 3 : El<DT>::TERMS;
@@ -1447,7 +1456,8 @@ LinSizes sizes(const Linear& p, int64_t least) {
 int64_t scan_blocks(const Linear& p) { return (p.dk * p.dv + 4 * kThreads - 1) / (4 * kThreads); }
 // Whether a sequence may have many segments: few workgroups then carry long chains
 // (one of 65531 tokens, 4 heads: 34 us with 8 pieces in flight, 31.6 with 16; 40
-// sequences of 16384 tokens, 16 heads: 36 and 50).
+// sequences of 16384 tokens, 16 heads: 36 and 50).  The gradients' call knows no bound
+// on the lengths: more than 8192 tokens count as one sequence there.
 bool long_chains(const Linear& p) { return std::min(p.N, p.max_len) > 32 * kSeg; }
 bool overlap(const Linear& p) {
     const char *a = reinterpret_cast<const char*>(p.s_in), *b = reinterpret_cast<const char*>(p.s_out);

@@ -430,7 +430,7 @@ size_t gdn_packed_backward_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int
  * Sequences of 32 tokens or more (fp32: 64) run in segments of 256 on the matrix
  * cores, for every dk and dv: fp32 as it is; bf16 q, k and v exactly, what is
  * multiplied with a power of alpha as two (scores, start states: 2^-17) or three
- * (what enters the states: exact) bf16 terms.  The others run token by token.
+ * (what enters the states: exact above 2^-102) bf16 terms.  The others run token by token.
  * All sums and states are fp32; out is rounded once.
  * NaN and infinities propagate as in the formula, to nothing of other sequences and
  * no token in front of theirs; in segments an infinity may become a NaN.
@@ -460,12 +460,14 @@ size_t gdn_linear_workspace_bytes(int64_t N, int64_t S, int64_t Hk, int64_t Hv, 
  *                   head in fp32 and rounded once;  grad_v [N, Hv, dv], dtype;
  *                   rows outside every sequence are set to zero
  *   grad_alpha      [Hv] fp32, summed over all sequences (states enter it as
- *                   three bf16 terms, exactly); NULL: not wanted
+ *                   three bf16 terms, exactly above 2^-102); NULL: not
+ *                   wanted
  *   grad_state0     [S, Hv, dv, dk] fp32: dL/d of each sequence's start state
  *                   (sequences that share a slot each have their own); NULL:
  *                   not wanted
  *   workspace       gdn_linear_backward_workspace_bytes(...): twice 4 Hv dk dv
- *                   for each sequence and for every 256 tokens, grad_alpha's
+ *                   for each sequence and for every 256 tokens, however many
+ *                   (4096 of 10 tokens, 16 heads of 128: 8.9 GB), grad_alpha's
  *                   addends, and for few tokens (N Hk below 2^14) grad_q and
  *                   grad_k in fp32 parts: 32 MiB of them at most
  * No gradient, nor the workspace, may lie in memory of an input (all slots of

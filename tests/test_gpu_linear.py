@@ -166,6 +166,27 @@ def test_without_states():
     assert torch.equal(out, again) and (pool == 7.0).all()
 
 
+@pytest.mark.parametrize("lengths", [(3, 1, 2), (90, 700, 2, 256)])
+def test_end_states_not_wanted(lengths):
+    """state_out NULL, which the entry point takes and the binding does not pass on."""
+    import ctypes
+
+    import torch
+    c = Linear(lengths, 1, 2, 64, 64, seed=52, slots=1).make()
+    t = {n: c.cuda(n) for n in NAMES}
+    want, _ = run(c)
+    N, S = sum(lengths), len(lengths)
+    out = torch.full((N, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    n = gdn.gdn_linear_workspace_bytes(N, S, 1, 2, 64, 64, max(lengths), 1)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    p = lambda x: ctypes.c_void_p(x.data_ptr())  # noqa: E731
+    rc = gdn.lib().gdn_linear_fwd(N, S, 1, 2, 64, 64, S + 1, 0, max(lengths), 1, 1.0, p(t["q"]), 64, p(t["k"]), 64, p(t["v"]), 128,
+                                  p(t["alpha"]), p(t["cu"]), p(t["pool"]), p(t["slots_in"]), None, None, p(out), p(ws), n,
+                                  ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert rc == 0 and np.array_equal(out.float().cpu().numpy(), want)
+
+
 def test_slices_of_one_projection():
     import torch
     c = Linear((90, 300, 3), 2, 4, 64, 64, seed=10).make()
